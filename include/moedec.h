@@ -59,6 +59,8 @@ enum moe_status {
 #define MOE_DEVERR_EXPERT_ID 0x1 /* an expert id outside [0, E) was skipped */
 #define MOE_DEVERR_TIMEOUT 0x2   /* a kernel's bounded wait gave up (never expected) */
 #define MOE_DEVERR_LOGIT 0x4     /* a router row had fewer than k logits above -inf */
+#define MOE_DEVERR_PAGE 0x8      /* a page id, slot or sequence length beyond its range */
+#define MOE_DEVERR_WORKSPACE 0x10 /* attention counters that were not zero at the call */
 
 /* Limits of the decode kernels (moe_gate_up, moe_down, moe_layer*). */
 #define MOE_MAX_EXPERTS 1024  /* E */
@@ -71,6 +73,45 @@ enum moe_status {
 #define MOE_ROUTER_MAX_K 32
 #define MOE_ROUTER_SOFTMAX 0
 #define MOE_ROUTER_SIGMOID 1
+
+/* Element types of the attention, rotary, norm and 4-bit entry points. */
+#define MOE_BF16 0
+#define MOE_F16 1
+#define MOE_F32 2
+#define MOE_E4M3 3
+/* Limits of moe_paged_attention, moe_rope_append, moe_norm_residual, moe_matvec4. */
+#define MOE_ATTN_MAX_BATCH 1024
+#define MOE_ATTN_MAX_DIM 256
+#define MOE_ROPE_MAX_DIM 512
+#define MOE_NORM_MAX_DIM 32768
+#define MOE_MATVEC_MAX_TOKENS 256
+/* Norm kinds, gate functions and frequency scalings. */
+#define MOE_NORM_RMS 0
+#define MOE_NORM_LAYER 1
+#define MOE_GATE_NONE 0
+#define MOE_GATE_SIGMOID 1
+#define MOE_ROPE_PLAIN 0
+#define MOE_ROPE_LINEAR 1
+#define MOE_ROPE_NTK 2
+#define MOE_ROPE_BY_PARTS 3
+
+/* One half (keys or values) of a paged cache: [num_pages][page_size][Hkv][D]
+ * in any order of its first three dims, D contiguous; strides in elements.
+ * scale: what an E4M3 code is multiplied by (ignored for 16-bit caches). */
+typedef struct {
+    void* data;
+    int64_t page_stride, token_stride, head_stride;
+    float scale;
+} moe_cache_t;
+
+/* A norm over rows of d: weight w and bias b ([d], of the call's dtype; each
+ * NULL for none), kind MOE_NORM_*. */
+typedef struct {
+    const void* w;
+    const void* b;
+    float eps;
+    int kind;
+} moe_norm_t;
 
 /* One MXFP8 weight tensor: codes [E][rows][K] and scales [E][rows][K/32].
  * Both device pointers; `w` must be 32-byte aligned (K % 32 == 0 then keeps
@@ -347,6 +388,132 @@ int moe_router_topk(const float* logits, int B, int E, int k, int score, float s
  * is unique.
  */
 int moe_mx_requant(const void* in, void* out, int64_t rows, int K, moe_stream_t stream);
+
+/*
+ * The decode block around the expert layer.  The four entry points below are
+ * the other steps of a decoder block, so that a token's whole step stays in
+ * this library; the source pages describe the expert layer alone, and these
+ * have no counterpart there.  Each is one launch.
+ *
+ * moe_paged_attention -- attention of one new token per sequence over a paged
+ * key-value cache.  For sequence b and query head h (key-value head
+ * h / (Hq/Hkv)), over the visible tokens j < seq_lens[b]:
+ *     s_j = scale * sum_c q[b,h,c] * k[j,c]
+ *     out[b,h] = sum_j exp(s_j - max s) v[j] / sum_j exp(s_j - max s)
+ *     lse[b,h] = log sum_j exp(s_j)
+ *   window = 0: every j is visible; window > 0: those with
+ *   j >= seq_lens[b] - window or j < sinks.  Tokens that are not visible are
+ *   not read.  Scores, softmax and sums are FP32, out is rounded once.  A
+ *   sequence of length 0 gets out = 0 and lse = -inf.
+ * Arguments
+ *   q          [B][Hq][D] of dtype MOE_BF16 or MOE_F16; strides in elements,
+ *              multiples of 8, 16-byte aligned.  out [B][Hq][D] contiguous of
+ *              the same dtype.  lse float32 [B][Hq] or NULL.
+ *   k, v       the cache, of cache_dtype = dtype or MOE_E4M3; rows 16-byte
+ *              aligned (data and strides).  Token j of sequence b is row
+ *              j % page_size of page block_table[b][j / page_size].
+ *   block_table int32 [B][max_pages], row stride table_stride; only the
+ *              entries of visible tokens are read.  An entry outside
+ *              [0, num_pages) leaves its tokens out and sets MOE_DEVERR_PAGE.
+ *   seq_lens   int32 [B], device memory; a length below 0 or above
+ *              max_pages * page_size is cut to that range and sets
+ *              MOE_DEVERR_PAGE.
+ *   workspace  >= moe_paged_attention_workspace_bytes, 256-byte aligned.  Its
+ *              first MOE_ATTN_COUNTER_BYTES must be zero before the first
+ *              call; every call leaves them zero, so a workspace is cleared
+ *              once and kept, for calls of any shape that it is large enough
+ *              for.  Calls that overlap in time need workspaces of their own.
+ *              Counters found not zero set MOE_DEVERR_WORKSPACE.
+ * The result does not depend on timing (no floating-point atomics).
+ * Limits: B <= MOE_ATTN_MAX_BATCH, D a multiple of 16 up to MOE_ATTN_MAX_DIM,
+ * Hq a multiple of Hkv.
+ */
+#define MOE_ATTN_COUNTER_BYTES 2048
+int moe_paged_attention_workspace_bytes(int Hq, int Hkv, int D, size_t* bytes);
+int moe_paged_attention(const void* q, int64_t q_stride, int64_t q_head_stride, int B, int Hq, int Hkv, int D,
+                        int dtype, moe_cache_t k, moe_cache_t v, int cache_dtype, int num_pages, int page_size,
+                        const int32_t* block_table, int64_t table_stride, int max_pages, const int32_t* seq_lens,
+                        float scale, int window, int sinks, void* workspace, size_t workspace_bytes, void* out,
+                        float* lse, moe_stream_t stream);
+
+/*
+ * moe_rope_append -- rotary positions for new tokens, and their keys and
+ * values into the paged cache.  Per token t and pair i < rot/2, with
+ * a = positions[t] * freqs[i] (exact to 2^-33 turns for any int32 position):
+ *     (x, y) -> mscale * (x cos a - y sin a, y cos a + x sin a)
+ *   on the pairs (x_i, x_{i + rot/2}) of a head, or (x_{2i}, x_{2i+1}) when
+ *   interleaved; dims from rot on are unchanged.  q is rotated into q_out,
+ *   k is rotated and written, v is written, at row slots[t] % page_size of
+ *   page slots[t] / page_size.  A negative slot writes no cache row (padding);
+ *   one beyond the cache is skipped and sets MOE_DEVERR_PAGE.  Two tokens of
+ *   one call must not share a slot.
+ * Arguments
+ *   q [T][Hq][D], k and v [T][Hkv][D], q_out [T][Hq][D]: dtype MOE_BF16 or
+ *   MOE_F16, strides in elements, D contiguous; q_out may be q itself.  The
+ *   cache's dtype is dtype or MOE_E4M3 (value / scale, nearest even,
+ *   saturated at 448).  positions int32 [T], slots int64 [T], freqs float64
+ *   [rot/2] in radians per position (see moe_rope_freqs).
+ *   1 <= D <= MOE_ROPE_MAX_DIM, rot even, 0 <= rot <= D.
+ */
+int moe_rope_append(const void* q, int64_t q_stride, int64_t q_head_stride, const void* k, int64_t k_stride,
+                    int64_t k_head_stride, const void* v, int64_t v_stride, int64_t v_head_stride, int T, int Hq,
+                    int Hkv, int D, int dtype, const int32_t* positions, const int64_t* slots, const double* freqs,
+                    int rot, int interleaved, float mscale, moe_cache_t k_cache, moe_cache_t v_cache, int cache_dtype,
+                    int num_pages, int page_size, void* q_out, int64_t qo_stride, int64_t qo_head_stride,
+                    moe_stream_t stream);
+
+/*
+ * moe_rope_freqs -- host function: freqs_host[i] = base^(-2i/rot), i < rot/2,
+ * in radians per position, scaled for contexts longer than the original one:
+ *   MOE_ROPE_LINEAR    divided by factor;
+ *   MOE_ROPE_NTK       with base * factor^(rot/(rot-2)) as the base;
+ *   MOE_ROPE_BY_PARTS  f * (g + (1-g)/factor), g = clamp((n - beta_slow) /
+ *                      (beta_fast - beta_slow), 0, 1), n = original_length *
+ *                      f / 2 pi the turns within the original length.
+ * rot even and >= 2 (NTK: > 2), base > 0, factor > 0, beta_fast > beta_slow.
+ */
+int moe_rope_freqs(int rot, double base, int scaling, double factor, double original_length, double beta_fast,
+                   double beta_slow, double* freqs_host);
+
+/*
+ * moe_norm_residual -- the step between two blocks, per row of d:
+ *     u = post(y);  r' = resid + alpha * u * act(gate);  out = pre(r')
+ *   resid_out gets r' and out gets pre(r'), which is computed from the
+ *   unrounded r'; all inside is FP32.  post, pre: RMS
+ *   v / sqrt(mean(v^2) + eps) * w + b, or layer norm (the same on v - mean).
+ * Arguments (NULL leaves a part out)
+ *   y       [T][d] of dtype MOE_BF16 / MOE_F16, row stride y_stride.
+ *   resid   [T][d] of resid_dtype = dtype or MOE_F32; NULL: r' = alpha u act(gate).
+ *   post, pre  moe_norm_t or NULL.
+ *   gate    of dtype: element (t, c) at gate[t * gate_row_stride + c *
+ *           gate_col_stride] (a stride of 0 broadcasts; the column stride is
+ *           0 or 1).  gate_act MOE_GATE_NONE or MOE_GATE_SIGMOID.
+ *   resid_out [T][d] contiguous of resid_dtype; may be resid when that is
+ *           contiguous.  out [T][d] contiguous of dtype; may be y likewise.
+ *           At least one of the two.
+ *   1 <= d <= MOE_NORM_MAX_DIM.  Any alignment of the elements' own size.
+ */
+int moe_norm_residual(const void* y, int64_t y_stride, int T, int d, int dtype, const void* resid,
+                      int64_t resid_stride, int resid_dtype, const moe_norm_t* post, const void* gate,
+                      int64_t gate_row_stride, int64_t gate_col_stride, int gate_act, float alpha,
+                      const moe_norm_t* pre, void* resid_out, void* out, moe_stream_t stream);
+
+/*
+ * moe_matvec4 -- products of few activation rows with 4-bit weights:
+ *     y[t,n] = sum_k (c[n,k] - z[n,k/group]) * s[n,k/group] * x[t,k]
+ * Arguments
+ *   x       [T][K] of dtype MOE_BF16 / MOE_F16, finite, row stride x_stride
+ *           (a multiple of 8), 16-byte aligned.
+ *   codes   [N][K/2] bytes, two unsigned codes 0..15 each, the lower k in the
+ *           low nibble; 16-byte aligned.
+ *   scales  [N][K/group] of dtype.  zeros uint8 [N][K/group], or NULL for 8.
+ *   group   32, 64 or 128; K a multiple of group.
+ *   y       [T][N] of dtype, row stride y_stride.
+ *   T <= MOE_MATVEC_MAX_TOKENS (the codes are read once per 32 rows of x), K <= 2^24.
+ * Products are exact, sums FP32, the weights are not rounded; y is rounded once.
+ */
+int moe_matvec4(const void* x, int64_t x_stride, int T, int K, int dtype, const uint8_t* codes, const void* scales,
+                const uint8_t* zeros, int N, int group, void* y, int64_t y_stride, moe_stream_t stream);
 
 /*
  * moe_device_error -- synchronise `stream`, then read and clear the sticky

@@ -26,7 +26,8 @@ EXPORTS = ("moe_version", "moe_strerror", "moe_gate_up", "moe_down", "moe_layer_
            "moe_align_block_size", "moe_align_block_size_static", "moe_align_static_fits",
            "moe_copy", "moe_device_error", "moe_router_topk", "moe_mx_requant", "moe_gate_up_fp4",
            "moe_layer_grouped_workspace_bytes", "moe_layer_grouped",
-           "moe_down_fp4")
+           "moe_down_fp4", "moe_paged_attention_workspace_bytes", "moe_paged_attention", "moe_rope_append",
+           "moe_rope_freqs", "moe_norm_residual", "moe_matvec4")
 
 
 class MoEError(RuntimeError):
@@ -37,6 +38,15 @@ class MoEError(RuntimeError):
 
 class MXView(ctypes.Structure):
     _fields_ = [("w", ctypes.c_void_p), ("s", ctypes.c_void_p)]
+
+
+class CacheView(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("scale", ctypes.c_float)]
+
+
+class NormView(ctypes.Structure):
+    _fields_ = [("w", ctypes.c_void_p), ("b", ctypes.c_void_p), ("eps", ctypes.c_float), ("kind", ctypes.c_int)]
 
 
 class MX(NamedTuple):
@@ -59,6 +69,7 @@ def load(path: str = LIB_PATH):
     lib = ctypes.CDLL(path)
     P, I, S = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
     MXP = ctypes.POINTER(MXView)
+    L, F, D, NP = ctypes.c_int64, ctypes.c_float, ctypes.c_double, ctypes.POINTER(NormView)
     sig = {
         "moe_version": ([], I),
         "moe_strerror": ([I], ctypes.c_char_p),
@@ -81,6 +92,14 @@ def load(path: str = LIB_PATH):
         "moe_device_error": ([P, ctypes.POINTER(I)], I),
         "moe_layer_grouped_workspace_bytes": ([I, I, I, I, I, I, ctypes.POINTER(S)], I),
         "moe_layer_grouped": ([P, I, I, P, P, I, MXView, MXView, MXView, I, I, MXP, MXP, MXP, I, P, S, P, P], I),
+        "moe_paged_attention_workspace_bytes": ([I, I, I, ctypes.POINTER(S)], I),
+        "moe_paged_attention": ([P, L, L, I, I, I, I, I, CacheView, CacheView, I, I, I, P, L, I, P, F, I, I, P, S, P,
+                                 P, P], I),
+        "moe_rope_append": ([P, L, L, P, L, L, P, L, L, I, I, I, I, I, P, P, P, I, I, F, CacheView, CacheView, I, I, I,
+                             P, L, L, P], I),
+        "moe_rope_freqs": ([I, D, I, D, D, D, D, P], I),
+        "moe_norm_residual": ([P, L, I, I, I, P, L, I, NP, P, L, L, I, F, NP, P, P, P], I),
+        "moe_matvec4": ([P, L, I, I, I, P, P, P, I, I, P, L, P], I),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -419,3 +438,294 @@ def mx_requant(x, out=None):
     rows = x.numel() // K if K else 0
     _check("moe_mx_requant", lib.moe_mx_requant(x.data_ptr(), out.data_ptr(), rows, K, _stream(x.device)))
     return out
+
+
+# ------------------------------------------------- the block around the layer
+
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2, torch.float8_e4m3fn: 3}
+ATTN_COUNTER_BYTES = 2048
+
+
+def _is(t, name: str, dtype, device, ndim: int):
+    """Dtype, device and dimension checks of a strided tensor."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dims, got {tuple(t.shape)}")
+
+
+def _half(t, name: str) -> int:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"{name} must be bfloat16 or float16, got {t.dtype}")
+    return DTYPES[t.dtype]
+
+
+def _heads(t, name: str, dtype, device, shape=None):
+    """Strides of a [tokens, heads, D] tensor with contiguous heads' rows."""
+    _is(t, name, dtype, device, 3)
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    st, sh, sd = t.stride()
+    if sd != 1 and t.shape[2] > 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    # the stride of a dimension of one element is free: 0 keeps it aligned
+    return (st if t.shape[0] > 1 else 0), (sh if t.shape[1] > 1 else 0)
+
+
+def _cache(t, name: str, dtype, device, scale: float):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype and t.dtype != torch.float8_e4m3fn:
+        raise TypeError(f"{name} must be {dtype} or float8_e4m3fn, got {t.dtype}")
+    _is(t, name, t.dtype, device, 4)
+    sp, st, sh, sd = t.stride()
+    if sd != 1 and t.shape[3] > 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    n, p, h, _ = t.shape
+    return CacheView(t.data_ptr(), sp if n > 1 else 0, st if p > 1 else 0, sh if h > 1 else 0, scale)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def attention_workspace_bytes(Hq: int, Hkv: int, D: int) -> int:
+    """Workspace bytes paged_attention needs for a head layout (any batch)."""
+    out = ctypes.c_size_t()
+    _check("moe_paged_attention_workspace_bytes",
+           load().moe_paged_attention_workspace_bytes(Hq, Hkv, D, ctypes.byref(out)))
+    return out.value
+
+
+def attention_workspace(Hq: int, Hkv: int, D: int, device=None) -> torch.Tensor:
+    """A cleared workspace to keep for paged_attention calls on one stream."""
+    return torch.zeros(attention_workspace_bytes(Hq, Hkv, D), dtype=torch.uint8, device=device or "cuda")
+
+
+def paged_attention(q, k_cache, v_cache, block_table, seq_lens, scale: Optional[float] = None, window: int = 0,
+                    sinks: int = 0, k_scale: float = 1.0, v_scale: float = 1.0,
+                    workspace: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                    return_lse: bool = False, lse: Optional[torch.Tensor] = None):
+    """moe_paged_attention: one new token per sequence over a paged cache.
+
+    q [B, Hq, D] BF16 or FP16 (any strides, D contiguous); k_cache, v_cache
+    [num_pages, page_size, Hkv, D] of q's dtype or float8_e4m3fn (any order of
+    the first three dims; times k_scale / v_scale); block_table int32
+    [B, max_pages]; seq_lens int32 [B].  scale defaults to D ** -0.5; window
+    and sinks as in include/moedec.h.  Pass a kept workspace (see
+    attention_workspace) to avoid clearing one per call.  Returns out
+    [B, Hq, D], or (out, lse float32 [B, Hq]) with return_lse."""
+    lib = load()
+    dt = _half(q, "q")
+    dev = q.device
+    q_st, q_sh = _heads(q, "q", q.dtype, dev)
+    B, Hq, D = q.shape
+    kv = _cache(k_cache, "k_cache", q.dtype, dev, k_scale)
+    vv = _cache(v_cache, "v_cache", k_cache.dtype, dev, v_scale)
+    pages, page, Hkv, Dk = k_cache.shape
+    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype or Dk != D:
+        raise ValueError(f"k_cache and v_cache must be alike and have q's head size {D}, got "
+                         f"{tuple(k_cache.shape)} {k_cache.dtype} / {tuple(v_cache.shape)} {v_cache.dtype}")
+    _is(block_table, "block_table", torch.int32, dev, 2)
+    if block_table.shape[0] != B or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError("block_table must be [B, max_pages] with contiguous rows")
+    _need(seq_lens, "seq_lens", torch.int32, dev, 1)
+    if seq_lens.shape[0] != B:
+        raise ValueError("seq_lens must be [B]")
+    if workspace is None:
+        workspace = torch.empty(attention_workspace_bytes(Hq, Hkv, D), dtype=torch.uint8, device=dev)
+        workspace[:ATTN_COUNTER_BYTES].zero_()
+    else:
+        _need(workspace, "workspace", torch.uint8, dev)
+    if out is None:
+        out = torch.empty((B, Hq, D), dtype=q.dtype, device=dev)
+    else:
+        _need(out, "out", q.dtype, dev, 3)
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+    if lse is not None:
+        _need(lse, "lse", torch.float32, dev, 2)
+        if lse.shape != (B, Hq):
+            raise ValueError("lse must be [B, Hq]")
+    elif return_lse:
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
+    rc = lib.moe_paged_attention(
+        q.data_ptr(), q_st, q_sh, B, Hq, Hkv, D, dt, kv, vv, DTYPES[k_cache.dtype], pages, page,
+        block_table.data_ptr(), block_table.stride(0), block_table.shape[1], seq_lens.data_ptr(),
+        D ** -0.5 if scale is None else scale, window, sinks, workspace.data_ptr(), workspace.numel(), out.data_ptr(),
+        _ptr(lse), _stream(dev))
+    _check("moe_paged_attention", rc)
+    return (out, lse) if return_lse else out
+
+
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3}
+
+
+def rope_freqs(rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+               original_length: float = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0, device="cpu"):
+    """moe_rope_freqs: float64 [rot / 2], radians per position."""
+    out = torch.empty(max(rot // 2, 0), dtype=torch.float64)
+    _check("moe_rope_freqs", load().moe_rope_freqs(rot, base, ROPE_SCALINGS[scaling], factor, original_length,
+                                                   beta_fast, beta_slow, out.data_ptr()))
+    return out.to(device)
+
+
+def rope_append(q, k, v, positions, slots, freqs, k_cache, v_cache, interleaved: bool = False, mscale: float = 1.0,
+                k_scale: float = 1.0, v_scale: float = 1.0, q_out: Optional[torch.Tensor] = None):
+    """moe_rope_append: rotates q [T, Hq, D] (returned) and k [T, Hkv, D] by
+    positions int32 [T], and writes k and v at slots int64 [T] (page *
+    page_size + row; negative: not written) of the caches [num_pages,
+    page_size, Hkv, D], in place.  freqs float64 [rot / 2] on the device; the
+    first rot dims of a head turn.  q_out may be q."""
+    lib = load()
+    dt = _half(q, "q")
+    dev = q.device
+    q_st, q_sh = _heads(q, "q", q.dtype, dev)
+    T, Hq, D = q.shape
+    kc = _cache(k_cache, "k_cache", q.dtype, dev, k_scale)
+    vc = _cache(v_cache, "v_cache", k_cache.dtype, dev, v_scale)
+    pages, page, Hkv, Dk = k_cache.shape
+    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype or Dk != D:
+        raise ValueError(f"k_cache and v_cache must be alike and have q's head size {D}, got "
+                         f"{tuple(k_cache.shape)} {k_cache.dtype} / {tuple(v_cache.shape)} {v_cache.dtype}")
+    k_st, k_sh = _heads(k, "k", q.dtype, dev, (T, Hkv, D))
+    v_st, v_sh = _heads(v, "v", q.dtype, dev, (T, Hkv, D))
+    _need(positions, "positions", torch.int32, dev, 1)
+    _need(slots, "slots", torch.int64, dev, 1)
+    _need(freqs, "freqs", torch.float64, dev, 1)
+    if positions.shape[0] != T or slots.shape[0] != T:
+        raise ValueError("positions and slots must be [T]")
+    if q_out is None:
+        q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=dev)
+    qo_st, qo_sh = _heads(q_out, "q_out", q.dtype, dev, (T, Hq, D))
+    rc = lib.moe_rope_append(
+        q.data_ptr(), q_st, q_sh, k.data_ptr(), k_st, k_sh, v.data_ptr(), v_st, v_sh, T, Hq, Hkv, D, dt,
+        positions.data_ptr(), slots.data_ptr(), freqs.data_ptr(), 2 * freqs.shape[0], int(bool(interleaved)), mscale,
+        kc, vc, DTYPES[k_cache.dtype], pages, page, q_out.data_ptr(), qo_st, qo_sh, _stream(dev))
+    _check("moe_rope_append", rc)
+    return q_out
+
+
+class Norm(NamedTuple):
+    """A norm over the last dimension: weight and bias [d] or None, kind "rms" or "layer"."""
+    w: Optional[torch.Tensor] = None
+    b: Optional[torch.Tensor] = None
+    eps: float = 1e-6
+    kind: str = "rms"
+
+
+NORM_KINDS = {"rms": 0, "layer": 1}
+GATE_ACTS = {"none": 0, "sigmoid": 1}
+
+
+def _norm(n: Optional[Norm], name: str, dtype, device, d: int):
+    if n is None:
+        return None
+    for t, part in ((n.w, "w"), (n.b, "b")):
+        if t is not None:
+            _need(t, f"{name}.{part}", dtype, device, 1)
+            if t.shape[0] != d:
+                raise ValueError(f"{name}.{part} must be [{d}], got {tuple(t.shape)}")
+    return NormView(_ptr(n.w), _ptr(n.b), n.eps, NORM_KINDS[n.kind])
+
+
+def norm_residual(y, resid=None, post: Optional[Norm] = None, gate=None, gate_act: str = "none", alpha: float = 1.0,
+                  pre: Optional[Norm] = None, resid_out: Optional[torch.Tensor] = None,
+                  out: Optional[torch.Tensor] = None):
+    """moe_norm_residual: r' = resid + alpha * post(y) * act(gate), x = pre(r').
+
+    y [T, d] BF16 or FP16 (row stride free); resid [T, d] of y's dtype or
+    float32, or None; gate [T or 1, d or 1] of y's dtype.  Returns
+    (r', x); r' has resid's dtype (y's without one) and may be written over
+    resid (resid_out=resid), x has y's.  Without resid and resid_out, returns
+    x alone."""
+    lib = load()
+    dt = _half(y, "y")
+    dev = y.device
+    _is(y, "y", y.dtype, dev, 2)
+    T, d = y.shape
+    if d > 1 and y.stride(1) != 1:
+        raise ValueError("y's last dimension must be contiguous")
+    r_dtype, r_stride = y.dtype, 0
+    if resid is not None:
+        r_dtype = resid.dtype
+        if r_dtype not in (y.dtype, torch.float32):
+            raise TypeError(f"resid must be {y.dtype} or float32, got {r_dtype}")
+        _is(resid, "resid", r_dtype, dev, 2)
+        if resid.shape != y.shape or (d > 1 and resid.stride(1) != 1):
+            raise ValueError("resid must have y's shape and contiguous rows")
+        r_stride = resid.stride(0)
+    g_row = g_col = 0
+    if gate is not None:
+        _is(gate, "gate", y.dtype, dev, 2)
+        gt, gd = gate.shape
+        if gt not in (1, T) or gd not in (1, d) or (gd > 1 and gate.stride(1) not in (0, 1)):
+            raise ValueError(f"gate must be [{T} or 1, {d} or 1] with contiguous rows, got {tuple(gate.shape)}")
+        g_row = gate.stride(0) if gt > 1 else 0
+        g_col = gate.stride(1) if gd > 1 else 0
+    vp, vq = _norm(post, "post", y.dtype, dev, d), _norm(pre, "pre", y.dtype, dev, d)
+    both = resid is not None or resid_out is not None
+    if both:
+        if resid_out is None:
+            resid_out = torch.empty((T, d), dtype=r_dtype, device=dev)
+        else:
+            _need(resid_out, "resid_out", r_dtype, dev, 2)
+            if resid_out.shape != y.shape:
+                raise ValueError("resid_out must have y's shape")
+    if out is None:
+        out = torch.empty((T, d), dtype=y.dtype, device=dev)
+    else:
+        _need(out, "out", y.dtype, dev, 2)
+        if out.shape != y.shape:
+            raise ValueError("out must have y's shape")
+    rc = lib.moe_norm_residual(y.data_ptr(), y.stride(0), T, d, dt, _ptr(resid), r_stride, DTYPES[r_dtype], _ref(vp),
+                               _ptr(gate), g_row, g_col, GATE_ACTS[gate_act], alpha, _ref(vq), _ptr(resid_out),
+                               out.data_ptr(), _stream(dev))
+    _check("moe_norm_residual", rc)
+    return (resid_out, out) if both else out
+
+
+class W4(NamedTuple):
+    """4-bit weights: codes uint8 [N, K/2] (the lower k in the low nibble), scales [N, K/group], zeros uint8
+    [N, K/group] or None (8 everywhere)."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    zeros: Optional[torch.Tensor] = None
+
+
+def matvec4(x, w: W4, y: Optional[torch.Tensor] = None):
+    """moe_matvec4: x [T, K] BF16 or FP16 times 4-bit weights -> y [T, N]; the
+    group size is K / w.scales.shape[1] (32, 64 or 128)."""
+    lib = load()
+    dt = _half(x, "x")
+    dev = x.device
+    _is(x, "x", x.dtype, dev, 2)
+    T, K = x.shape
+    if K > 1 and x.stride(1) != 1:
+        raise ValueError("x's last dimension must be contiguous")
+    _need(w.codes, "w.codes", torch.uint8, dev, 2)
+    _need(w.scales, "w.scales", x.dtype, dev, 2)
+    N, groups = w.scales.shape
+    if K % 2 or tuple(w.codes.shape) != (N, K // 2) or groups == 0 or K % groups:
+        raise ValueError(f"codes must be [N, K/2] and scales [N, K/group] for K = {K}, got "
+                         f"{tuple(w.codes.shape)} / {tuple(w.scales.shape)}")
+    if w.zeros is not None:
+        _need(w.zeros, "w.zeros", torch.uint8, dev, 2)
+        if w.zeros.shape != w.scales.shape:
+            raise ValueError("zeros must have the shape of scales")
+    if y is None:
+        y = torch.empty((T, N), dtype=x.dtype, device=dev)
+    else:
+        _is(y, "y", x.dtype, dev, 2)
+        if tuple(y.shape) != (T, N) or (N > 1 and y.stride(1) != 1):
+            raise ValueError("y must be [T, N] with contiguous rows")
+    rc = lib.moe_matvec4(x.data_ptr(), x.stride(0) if T > 1 else 0, T, K, dt, w.codes.data_ptr(), w.scales.data_ptr(), _ptr(w.zeros), N,
+                         K // groups, y.data_ptr(), y.stride(0), _stream(dev))
+    _check("moe_matvec4", rc)
+    return y

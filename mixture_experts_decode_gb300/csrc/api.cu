@@ -1,6 +1,7 @@
 // api.cu -- the extern "C" boundary of libmoedec.so: argument checks,
 // workspace carving and launches.  No allocation anywhere in the library.
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
 #include <mutex>
 
@@ -189,6 +190,16 @@ int check_grouped_shape(int T, int k, int E, int d, int I) {
     if (ns > 0x7fffffffLL || (int64_t)T * k * d > ((int64_t)1 << 40)) return MOE_ERR_LIMIT;
     return MOE_OK;
 }
+
+// Strides that keep every row of a cache or activation `bytes`-aligned.
+bool strides_aligned(int64_t elem, size_t bytes, int64_t s0, int64_t s1, int64_t s2) {
+    const int64_t m = (int64_t)bytes / elem;
+    return s0 % m == 0 && s1 % m == 0 && s2 % m == 0;
+}
+
+bool half_type(int dtype) { return dtype == MOE_BF16 || dtype == MOE_F16; }
+
+NormSpec norm_spec(const moe_norm_t* n) { return n ? NormSpec{n->w, n->b, n->eps, n->kind} : NormSpec{nullptr, nullptr, 0.f, -1}; }
 
 }  // namespace
 
@@ -460,6 +471,142 @@ int moe_copy(void* dst, const void* src, size_t bytes, moe_stream_t stream) {
     if (!dst || !src) return MOE_ERR_ARG;
     if (!aligned(dst, 32) || !aligned(src, 32) || bytes % 32) return MOE_ERR_ALIGN;
     return cuda_status(launch_copy(dst, src, bytes, (cudaStream_t)stream));
+}
+
+int moe_paged_attention_workspace_bytes(int Hq, int Hkv, int D, size_t* bytes) {
+    if (!bytes || Hq < 1 || Hkv < 1 || D < 1) return MOE_ERR_ARG;
+    if (Hq % Hkv || D % 16) return MOE_ERR_SHAPE;
+    if (D > MOE_ATTN_MAX_DIM) return MOE_ERR_LIMIT;
+    *bytes = round_up(attn_workspace_bytes(Hq, Hkv, D), 256);
+    return MOE_OK;
+}
+
+int moe_paged_attention(const void* q, int64_t q_stride, int64_t q_head_stride, int B, int Hq, int Hkv, int D,
+                        int dtype, moe_cache_t k, moe_cache_t v, int cache_dtype, int num_pages, int page_size,
+                        const int32_t* block_table, int64_t table_stride, int max_pages, const int32_t* seq_lens,
+                        float scale, int window, int sinks, void* workspace, size_t workspace_bytes, void* out,
+                        float* lse, moe_stream_t stream) {
+    if (B < 0 || Hq < 1 || Hkv < 1 || D < 1 || num_pages < 0 || page_size < 1 || max_pages < 0 || window < 0 || sinks < 0)
+        return MOE_ERR_ARG;
+    if (!half_type(dtype) || (cache_dtype != dtype && cache_dtype != MOE_E4M3)) return MOE_ERR_ARG;
+    size_t need = 0;
+    const int rc = moe_paged_attention_workspace_bytes(Hq, Hkv, D, &need);
+    if (rc) return rc;
+    if (B > MOE_ATTN_MAX_BATCH || (int64_t)Hq * D > (1 << 24)) return MOE_ERR_LIMIT;
+    if (B == 0) return MOE_OK;
+    if (!q || !seq_lens || !out) return MOE_ERR_ARG;
+    if (num_pages > 0 && max_pages > 0 && (!k.data || !v.data || !block_table)) return MOE_ERR_ARG;
+    if (!workspace || workspace_bytes < need) return MOE_ERR_WORKSPACE;
+    const int es = cache_dtype == MOE_E4M3 ? 1 : 2;
+    if (!aligned(q, 16) || !strides_aligned(2, 16, q_stride, q_head_stride, 0) || !aligned(k.data, 16) ||
+        !aligned(v.data, 16) || !strides_aligned(es, 16, k.page_stride, k.token_stride, k.head_stride) ||
+        !strides_aligned(es, 16, v.page_stride, v.token_stride, v.head_stride) || !aligned(workspace, 256) ||
+        !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(out, 2) || !aligned(lse, 4))
+        return MOE_ERR_ALIGN;
+    const bool e4 = cache_dtype == MOE_E4M3;
+    AttnArgs a{};
+    a.q = q, a.q_sb = q_stride, a.q_sh = q_head_stride;
+    a.k = k.data, a.k_sp = k.page_stride, a.k_st = k.token_stride, a.k_sh = k.head_stride;
+    a.v = v.data, a.v_sp = v.page_stride, a.v_st = v.token_stride, a.v_sh = v.head_stride;
+    a.table = block_table, a.table_stride = table_stride, a.lens = seq_lens;
+    a.B = B, a.Hq = Hq, a.Hkv = Hkv, a.D = D;
+    a.num_pages = num_pages, a.page = page_size, a.max_pages = max_pages;
+    a.window = window, a.sinks = sinks;
+    a.scale_log2 = scale * (e4 ? k.scale : 1.f) * 1.44269504088896341f;
+    a.v_scale = e4 ? v.scale : 1.f;
+    a.out = out, a.lse = lse;
+    return cuda_status(launch_paged_attention(a, dtype, cache_dtype, workspace, (cudaStream_t)stream));
+}
+
+int moe_rope_append(const void* q, int64_t q_stride, int64_t q_head_stride, const void* k, int64_t k_stride,
+                    int64_t k_head_stride, const void* v, int64_t v_stride, int64_t v_head_stride, int T, int Hq,
+                    int Hkv, int D, int dtype, const int32_t* positions, const int64_t* slots, const double* freqs,
+                    int rot, int interleaved, float mscale, moe_cache_t k_cache, moe_cache_t v_cache, int cache_dtype,
+                    int num_pages, int page_size, void* q_out, int64_t qo_stride, int64_t qo_head_stride,
+                    moe_stream_t stream) {
+    if (T < 0 || Hq < 1 || Hkv < 1 || D < 1 || rot < 0 || num_pages < 0 || page_size < 1) return MOE_ERR_ARG;
+    if (!half_type(dtype) || (cache_dtype != dtype && cache_dtype != MOE_E4M3)) return MOE_ERR_ARG;
+    if (interleaved != 0 && interleaved != 1) return MOE_ERR_ARG;
+    if (rot % 2 || rot > D) return MOE_ERR_SHAPE;
+    if (D > MOE_ROPE_MAX_DIM || (int64_t)(Hq + (int64_t)2 * Hkv) * D > (1 << 24)) return MOE_ERR_LIMIT;
+    if (T == 0) return MOE_OK;
+    if (!q || !k || !v || !positions || !slots || (rot && !freqs) || !q_out) return MOE_ERR_ARG;
+    if (num_pages > 0 && (!k_cache.data || !v_cache.data)) return MOE_ERR_ARG;
+    const bool e4 = cache_dtype == MOE_E4M3;
+    const size_t ca = e4 ? 1 : 2;
+    if (!aligned(q, 2) || !aligned(k, 2) || !aligned(v, 2) || !aligned(q_out, 2) || !aligned(k_cache.data, ca) ||
+        !aligned(v_cache.data, ca) || !aligned(positions, 4) || !aligned(slots, 8) || !aligned(freqs, 8))
+        return MOE_ERR_ALIGN;
+    RopeArgs a{};
+    a.q = q, a.q_st = q_stride, a.q_sh = q_head_stride;
+    a.k = k, a.k_st = k_stride, a.k_sh = k_head_stride;
+    a.v = v, a.v_st = v_stride, a.v_sh = v_head_stride;
+    a.q_out = q_out, a.qo_st = qo_stride, a.qo_sh = qo_head_stride;
+    a.kc = k_cache.data, a.kc_sp = k_cache.page_stride, a.kc_st = k_cache.token_stride, a.kc_sh = k_cache.head_stride;
+    a.vc = v_cache.data, a.vc_sp = v_cache.page_stride, a.vc_st = v_cache.token_stride, a.vc_sh = v_cache.head_stride;
+    a.positions = positions, a.slots = slots, a.freqs = freqs;
+    a.T = T, a.Hq = Hq, a.Hkv = Hkv, a.D = D, a.rot = rot, a.interleaved = interleaved;
+    a.num_pages = num_pages, a.page = page_size;
+    a.mscale = mscale, a.k_scale = k_cache.scale, a.v_scale = v_cache.scale;
+    return cuda_status(launch_rope_append(a, dtype, cache_dtype, (cudaStream_t)stream));
+}
+
+int moe_rope_freqs(int rot, double base, int scaling, double factor, double original_length, double beta_fast,
+                   double beta_slow, double* freqs_host) {
+    if (!freqs_host || !(base > 0) || scaling < MOE_ROPE_PLAIN || scaling > MOE_ROPE_BY_PARTS) return MOE_ERR_ARG;
+    if (rot < 2 || rot % 2 || (scaling == MOE_ROPE_NTK && rot <= 2)) return MOE_ERR_SHAPE;
+    if (scaling != MOE_ROPE_PLAIN && !(factor > 0)) return MOE_ERR_ARG;
+    if (scaling == MOE_ROPE_BY_PARTS && !(beta_fast > beta_slow && original_length > 0)) return MOE_ERR_ARG;
+    if (scaling == MOE_ROPE_NTK) base *= std::pow(factor, (double)rot / (rot - 2));
+    for (int i = 0; i < rot / 2; ++i) {
+        double f = std::pow(base, -2.0 * i / rot);
+        if (scaling == MOE_ROPE_LINEAR) f /= factor;
+        if (scaling == MOE_ROPE_BY_PARTS) {
+            const double turns = original_length * f / 6.283185307179586477;
+            const double g = std::min(1.0, std::max(0.0, (turns - beta_slow) / (beta_fast - beta_slow)));
+            f *= g + (1.0 - g) / factor;
+        }
+        freqs_host[i] = f;
+    }
+    return MOE_OK;
+}
+
+int moe_norm_residual(const void* y, int64_t y_stride, int T, int d, int dtype, const void* resid,
+                      int64_t resid_stride, int resid_dtype, const moe_norm_t* post, const void* gate,
+                      int64_t gate_row_stride, int64_t gate_col_stride, int gate_act, float alpha,
+                      const moe_norm_t* pre, void* resid_out, void* out, moe_stream_t stream) {
+    if (T < 0 || d < 1 || !half_type(dtype) || (resid_dtype != dtype && resid_dtype != MOE_F32)) return MOE_ERR_ARG;
+    if (gate_act != MOE_GATE_NONE && gate_act != MOE_GATE_SIGMOID) return MOE_ERR_ARG;
+    if (gate && gate_col_stride != 0 && gate_col_stride != 1) return MOE_ERR_ARG;
+    for (const moe_norm_t* n : {post, pre})
+        if (n && n->kind != MOE_NORM_RMS && n->kind != MOE_NORM_LAYER) return MOE_ERR_ARG;
+    if (d > MOE_NORM_MAX_DIM) return MOE_ERR_LIMIT;
+    if (T == 0) return MOE_OK;
+    if (!y || (!resid_out && !out)) return MOE_ERR_ARG;
+    const size_t rs = resid_dtype == MOE_F32 ? 4 : 2;
+    for (const moe_norm_t* n : {post, pre})
+        if (n && (!aligned(n->w, 2) || !aligned(n->b, 2))) return MOE_ERR_ALIGN;
+    if (!aligned(y, 2) || !aligned(resid, rs) || !aligned(gate, 2) || !aligned(resid_out, rs) || !aligned(out, 2))
+        return MOE_ERR_ALIGN;
+    NormArgs a{};
+    a.y = y, a.y_stride = y_stride, a.resid = resid, a.r_stride = resid_stride;
+    a.gate = gate, a.gate_row = gate_row_stride, a.gate_col = gate_col_stride, a.gate_act = gate_act;
+    a.alpha = alpha, a.post = norm_spec(post), a.pre = norm_spec(pre);
+    a.resid_out = resid_out, a.out = out, a.T = T, a.d = d;
+    return cuda_status(launch_norm_residual(a, dtype, resid_dtype, (cudaStream_t)stream));
+}
+
+int moe_matvec4(const void* x, int64_t x_stride, int T, int K, int dtype, const uint8_t* codes, const void* scales,
+                const uint8_t* zeros, int N, int group, void* y, int64_t y_stride, moe_stream_t stream) {
+    if (T < 0 || K < 0 || N < 0 || !half_type(dtype)) return MOE_ERR_ARG;
+    if ((group != 32 && group != 64 && group != 128) || K == 0 || K % group) return MOE_ERR_SHAPE;
+    if (T > MOE_MATVEC_MAX_TOKENS || K > (1 << 24)) return MOE_ERR_LIMIT;
+    if (T == 0 || N == 0) return MOE_OK;
+    if (!x || !codes || !scales || !y) return MOE_ERR_ARG;
+    if (!aligned(x, 16) || x_stride % 8 || !aligned(codes, 16) || !aligned(scales, 2) || !aligned(y, 2))
+        return MOE_ERR_ALIGN;
+    const Matvec4Args a{x, x_stride, codes, scales, zeros, y, y_stride, T, N, K, group};
+    return cuda_status(launch_matvec4(a, dtype, (cudaStream_t)stream));
 }
 
 int moe_device_error(moe_stream_t stream, int* bits) {

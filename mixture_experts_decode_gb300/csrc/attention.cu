@@ -1,0 +1,664 @@
+// attention.cu -- attention of one new token per sequence over a paged
+// key-value cache, with an optional sliding window and first tokens that stay
+// visible, split evenly over the grid and joined inside the same launch.
+//
+// Mathematics.  For each sequence b and query head h (key-value head
+// h / (Hq / Hkv)), over the visible keys j:
+//   s_j = scale * q . k_j,   o = sum_j exp(s_j - m) v_j / sum_j exp(s_j - m)
+// in one pass: each warp keeps the running maximum m (base 2), sum l and
+// unnormalised o, rescaling o only when m grows; warps, then pieces of a
+// sequence, combine by exp2(m_piece - m) weights.  All of it is FP32.
+//
+// Bound: HBM, each visible K and V row once (2 * D * bytes per key and
+// key-value head).  The query heads that share a key-value head are the N
+// columns of the products, so a key row is read once for all of them:
+//   S^T [16 keys x heads] = K [16 x D] * Q^T,   O^T [D x heads] += V^T * P^T
+// with mma.m16n8k16: 8 heads fill one N tile exactly, and the score
+// accumulator becomes the second product's B operand by one 8x8 transpose
+// (movmatrix).  A tcgen05 product needs 64 or 128 rows in M and moves its
+// accumulator through TMEM; here the products take a few percent of the issue
+// slots, so the warp-level instruction with registers is the shorter path.
+//
+// Rounding choices: scores, softmax and sums are FP32.  The second product
+// takes 16-bit operands; p is given to it as hi + lo (two 16-bit values, an
+// error near 2^-17 of p in BF16 and 2^-22 in FP16), because one 16-bit
+// rounding of p would cost as much as rounding the output.  FP16 operands
+// hold 2^14 p (at most 2^14), so that a long tail of keys far below the
+// maximum is kept down to p = 2^-38; l carries the same factor.  E4M3 codes widen to FP16 exactly; a
+// BF16 q then goes to FP16 after a power-of-two scaling of its head's row
+// (the largest element in [2^9, 2^10]), exact for elements within 2^-23 of
+// the row's largest, and smaller ones are off by less than FP32's own sum.
+//
+// Layout: every warp has its own ring of cp.async stages of 16 keys (K and V),
+// so no barrier of the block sits in the main loop.  Work is counted in units
+// of 64 visible keys of one (sequence, key-value head) item; each block takes
+// an equal contiguous run of units (so ragged batches stay balanced), and the
+// last block to finish an item that was cut joins its pieces in order, which
+// keeps the result independent of timing.
+#include "common.cuh"
+#include "internal.h"
+
+namespace moedec {
+
+namespace {
+
+constexpr int ATT_WARPS = 4;
+constexpr int ATT_THREADS = ATT_WARPS * 32;
+constexpr int ATT_STEP = 16;                     // keys per warp step
+constexpr int ATT_UNIT = ATT_STEP * ATT_WARPS;   // keys per unit of work
+constexpr int KV_BF16 = 0, KV_F16 = 1, KV_E4M3 = 2;
+
+// Stages per warp: what two resident blocks per SM can hold (about 96 KB
+// each), at least three.
+constexpr int att_stages(int dp, int es) {
+    const int s = 98304 / (ATT_WARPS * 2 * ATT_STEP * dp * es);
+    return s < 3 ? 3 : (s > 6 ? 6 : s);
+}
+
+__device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm_x4_t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+template <bool BF>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if (BF)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <bool BF>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    uint32_t r;
+    if (BF)
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+template <bool BF>
+__device__ __forceinline__ float2 unpack2(uint32_t v) {
+    if (BF) return bf16x2_to_float2(v);
+    __half2 h;
+    memcpy(&h, &v, 4);
+    return __half22float2(h);
+}
+// Two E4M3 codes in the low / high half of a word -> FP16 pair, exact.
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    asm("{ .reg .b16 l, h;\n\t mov.b32 {l, h}, %2;\n\t cvt.rn.f16x2.e4m3x2 %0, l;\n\t cvt.rn.f16x2.e4m3x2 %1, h; }"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+    float r;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float finite_or_zero(float m) { return m == -INFINITY ? 0.f : m; }
+
+}  // namespace
+
+// The visible keys of a sequence of n tokens, as one run 0 .. vis-1 that maps
+// to tokens: the first `head` stand for tokens 0 .. head-1, the rest for
+// tokens from head + skip on.
+struct Visible {
+    int vis, head, skip;
+};
+__device__ __forceinline__ Visible visible_keys(int n, int window, int sinks) {
+    if (window == 0 || n <= window) return {n, n, 0};
+    const int start = n - window;
+    const int head = min(sinks, start);
+    return {head + window, head, start - head};
+}
+
+// One output value from its joined sums; l = 0 (no visible key, or every score
+// -inf) gives 0 and a log-sum of -inf.
+template <bool QBF>
+__device__ __forceinline__ void store_head(const AttnArgs& a, int b, int h, int dim, float sum, float l, float m,
+                                           float shift) {
+    const int64_t row = (int64_t)b * a.Hq + h;
+    const float v = l == 0.f ? 0.f : sum / l * a.v_scale;
+    if (QBF)
+        static_cast<__nv_bfloat16*>(a.out)[row * a.D + dim] = __float2bfloat16_rn(v);
+    else
+        static_cast<__half*>(a.out)[row * a.D + dim] = __float2half_rn(v);
+    if (dim == 0 && a.lse) a.lse[row] = l == 0.f ? -INFINITY : (m - shift + log2f(l)) * 0.693147180559945309f;
+}
+
+template <int DP, int NT, int KV, bool QBF>
+__global__ void __launch_bounds__(ATT_THREADS) paged_attention_kernel(const AttnArgs a) {
+    constexpr int ES = KV == KV_E4M3 ? 1 : 2;
+    constexpr bool BF = KV == KV_BF16;  // operand type of the products
+    constexpr int ROW = DP * ES;        // bytes of a key's row in shared memory
+    constexpr int CHP = ROW / 16;
+    constexpr int NST = att_stages(DP, ES);
+    constexpr int HALF = ATT_STEP * ROW;  // bytes of K (or V) in a stage
+    constexpr int NK = DP / 16;
+    constexpr int NH = NT * 8;
+    constexpr float P_SHIFT = BF ? 0.f : 14.f;
+
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int tid = threadIdx.x, lane = tid & 31, warp = warp_index();
+    const int g = lane >> 2, t = lane & 3;
+    uint8_t* ring = smem + (size_t)warp * NST * 2 * HALF;
+    uint8_t* tail = smem + (size_t)ATT_WARPS * NST * 2 * HALF;
+    uint32_t* live = reinterpret_cast<uint32_t*>(tail) + warp * NST;  // readable keys of each stage
+    float* sm_m = reinterpret_cast<float*>(tail + ATT_WARPS * NST * 4);  // [warps][NH]
+    float* sm_l = sm_m + ATT_WARPS * NH;
+    int64_t* sm_warp = reinterpret_cast<int64_t*>(sm_l + ATT_WARPS * NH);  // [warps] + carry
+    int64_t* prefix = sm_warp + 8;                                         // [B] units up to and with b
+
+    const int nk = a.D / 16;
+    const int chunks16 = a.D * ES / 16;
+    const int64_t cap = (int64_t)a.max_pages * a.page;
+
+    // units of each sequence, scanned over the batch
+    int64_t carry = 0;
+    for (int b0 = 0; b0 < a.B; b0 += ATT_THREADS) {
+        const int b = b0 + tid;
+        int64_t u = 0;
+        if (b < a.B) {
+            const int n = a.lens[b];
+            if (n < 0 || n > cap) {
+                if (blockIdx.x == 0) atomicOr(a.err, MOE_DEVERR_PAGE);
+            }
+            const int nn = (int)(n < 0 ? 0 : (n > cap ? cap : n));
+            const Visible v = visible_keys(nn, a.window, a.sinks);
+            u = ((int64_t)v.vis + ATT_UNIT - 1) / ATT_UNIT;
+        }
+        int64_t s = u;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(FULL_MASK, s, o);
+            if (lane >= o) s += v;
+        }
+        if (lane == 31) sm_warp[warp] = s;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) s += sm_warp[w];
+        if (b < a.B) prefix[b] = s + carry;
+        if (tid == ATT_THREADS - 1) sm_warp[ATT_WARPS] = s;
+        __syncthreads();
+        carry += sm_warp[ATT_WARPS];
+    }
+    // a sequence without keys has no units: its rows are written here
+    for (int b = blockIdx.x; b < a.B; b += gridDim.x)
+        if (prefix[b] == (b ? prefix[b - 1] : 0)) {
+            for (int i = tid; i < a.Hq * a.D; i += ATT_THREADS)
+                static_cast<uint16_t*>(a.out)[(int64_t)b * a.Hq * a.D + i] = 0;
+            if (a.lse)
+                for (int h = tid; h < a.Hq; h += ATT_THREADS) a.lse[(int64_t)b * a.Hq + h] = -INFINITY;
+        }
+    const int items = a.Hkv * a.chunks;  // items of one sequence
+    const int64_t total = carry * items;
+    const int64_t blocks = total < gridDim.x ? total : gridDim.x;
+    if ((int64_t)blockIdx.x >= blocks) return;
+    int64_t u = total * blockIdx.x / blocks;
+    const int64_t u_end = total * (blockIdx.x + 1) / blocks;
+    int b = 0;
+    {
+        int lo = 0, hi = a.B - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (prefix[mid] * items > u)
+                hi = mid;
+            else
+                lo = mid + 1;
+        }
+        b = lo;
+    }
+
+    while (u < u_end) {
+        while (prefix[b] * items <= u) ++b;
+        const int64_t before = b ? prefix[b - 1] : 0;
+        const int64_t units = prefix[b] - before;
+        const int64_t rel = u - before * items;
+        const int item = (int)(rel / units);
+        const int64_t t0 = rel - (int64_t)item * units;
+        const int64_t t1 = min(units, t0 + (u_end - u));
+        const int kvh = item / a.chunks, chunk = item - kvh * a.chunks;
+        const int head0 = kvh * a.G + chunk * a.hpi;
+        const int heads = min(a.hpi, a.G - chunk * a.hpi);
+        const int n_raw = a.lens[b];
+        const int n = (int)(n_raw > cap ? cap : n_raw);
+        const Visible vis = visible_keys(n, a.window, a.sinks);
+        const int key_end = (int)min((int64_t)vis.vis, t1 * ATT_UNIT);
+        const int step0 = (int)(t0 * ATT_WARPS) + warp;
+        const int64_t step_end = ((int64_t)key_end + ATT_STEP - 1) / ATT_STEP;
+        const int steps = step0 < step_end ? (int)((step_end - step0 + ATT_WARPS - 1) / ATT_WARPS) : 0;
+        const int32_t* table = a.table + (int64_t)b * a.table_stride;
+        const uint8_t* kbase = static_cast<const uint8_t*>(a.k) + (int64_t)kvh * a.k_sh * ES;
+        const uint8_t* vbase = static_cast<const uint8_t*>(a.v) + (int64_t)kvh * a.v_sh * ES;
+
+        // Nothing from here to the sums' end branches per lane, because the
+        // matrix instructions need the whole warp together.
+        // Lanes 0..15 (and again 16..31) find the page of one key each, one
+        // step ahead of its use; beyond the last key they look the last one up
+        // again and drop it.  page < 0: nothing to read.
+        int page = -1, off = 0;
+        auto find = [&](int i) {
+            if (i >= steps) return;
+            const int64_t k64 = ((int64_t)step0 + (int64_t)i * ATT_WARPS) * ATT_STEP + (lane & 15);
+            const int key = (int)min(k64, (int64_t)key_end - 1);
+            const int tok = key < vis.head ? key : key + vis.skip;
+            const int pi = tok / a.page;
+            off = tok - pi * a.page;
+            const int pg = table[pi];
+            const bool known = pg >= 0 && pg < a.num_pages;
+            if (__any_sync(FULL_MASK, !known)) atomicOr(a.err, known ? 0 : MOE_DEVERR_PAGE);
+            page = known && k64 < key_end ? pg : -1;
+        };
+        auto issue = [&](int i) {
+            const int st = i % NST;
+            if (i < steps) {
+                const uint32_t mask = __ballot_sync(FULL_MASK, page >= 0) & 0xffffu;
+                live[st] = mask;
+                uint8_t* sk = ring + st * 2 * HALF;
+#pragma unroll
+                for (int it = 0; it < ATT_STEP * CHP / 32; ++it) {
+                    const int c = it * 32 + lane;
+                    const int row = c / CHP, col = c % CHP;
+                    const int pg = __shfl_sync(FULL_MASK, page, row);
+                    const int of = __shfl_sync(FULL_MASK, off, row);
+                    // 0 bytes write zeros: a key that is not there, or columns beyond D
+                    const bool on = pg >= 0 && col < chunks16;
+                    const int bytes = on ? 16 : 0;
+                    const int64_t p = on ? pg : 0, o = on ? of : 0, at = on ? col * 16 : 0;
+                    const int ck = KV == KV_E4M3 ? (CHP >= 8 ? col ^ ((row & 1) << 2) : col) : col ^ (row & 7);
+                    const int cv = KV == KV_E4M3 ? (CHP >= 8 ? col ^ (((row >> 1) & 3) << 1) : col ^ (((row >> 1) & 1) << 1))
+                                                 : col ^ (row & 7);
+                    cp_async_16_zfill(sk + row * ROW + ck * 16, kbase + (p * a.k_sp + o * a.k_st) * ES + at, bytes);
+                    cp_async_16_zfill(sk + HALF + row * ROW + cv * 16, vbase + (p * a.v_sp + o * a.v_st) * ES + at, bytes);
+                }
+            }
+            cp_async_commit();
+        };
+        find(0);
+#pragma unroll
+        for (int i = 0; i < NST - 1; ++i) {
+            issue(i);
+            find(i + 1);
+        }
+
+        // q as the first product's B operand (column = head g of the tile)
+        uint32_t qf[NT][NK][2];
+        float sl[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int h = nt * 8 + g;
+            const uint16_t* qrow =
+                static_cast<const uint16_t*>(a.q) + (int64_t)b * a.q_sb + (int64_t)(head0 + (h < heads ? h : 0)) * a.q_sh;
+            if (KV != KV_E4M3) {
+#pragma unroll
+                for (int kk = 0; kk < NK; ++kk) {
+                    const bool on = h < heads && kk < nk;
+                    qf[nt][kk][0] = on ? *reinterpret_cast<const uint32_t*>(qrow + kk * 16 + 2 * t) : 0u;
+                    qf[nt][kk][1] = on ? *reinterpret_cast<const uint32_t*>(qrow + kk * 16 + 2 * t + 8) : 0u;
+                }
+                sl[nt][0] = sl[nt][1] = a.scale_log2;
+            } else {
+                // the thread's 16 codes of a key are dims 64j + 16t ..; product i
+                // of the block takes four of them
+                float amax = 0.f;
+#pragma unroll
+                for (int kk = 0; kk < NK; ++kk) {
+                    const int dim = (kk >> 2) * 64 + t * 16 + (kk & 3) * 4;
+                    const bool on = h < heads && dim < a.D;
+                    uint2 v = on ? *reinterpret_cast<const uint2*>(qrow + dim) : make_uint2(0u, 0u);
+                    qf[nt][kk][0] = v.x;
+                    qf[nt][kk][1] = v.y;
+                    if (QBF) {
+                        const float2 p = bf16x2_to_float2(v.x), r = bf16x2_to_float2(v.y);
+                        amax = fmaxf(fmaxf(amax, fmaxf(fabsf(p.x), fabsf(p.y))), fmaxf(fabsf(r.x), fabsf(r.y)));
+                    }
+                }
+                float back = 1.f;
+                if (QBF) {
+                    amax = fmaxf(amax, __shfl_xor_sync(FULL_MASK, amax, 1));
+                    amax = fmaxf(amax, __shfl_xor_sync(FULL_MASK, amax, 2));
+                    // 2^e <= amax < 2^(e+1); q * 2^(9-e), undone in the scale
+                    int e = (int)(__float_as_uint(amax) >> 23) - 127;
+                    e = max(-100, min(e, 127));
+                    const float fwd = __uint_as_float((uint32_t)(127 + min(9 - e, 109)) << 23);
+                    back = __uint_as_float((uint32_t)(127 - min(9 - e, 109)) << 23);
+#pragma unroll
+                    for (int kk = 0; kk < NK; ++kk)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const float2 p = bf16x2_to_float2(qf[nt][kk][r]);
+                            qf[nt][kk][r] = pack2<false>(p.x * fwd, p.y * fwd);
+                        }
+                }
+                sl[nt][0] = a.scale_log2 * __shfl_sync(FULL_MASK, back, 8 * t);
+                sl[nt][1] = a.scale_log2 * __shfl_sync(FULL_MASK, back, 8 * t + 4);
+            }
+        }
+
+        float o[NK][NT][4], m[NT][2], l[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            m[nt][0] = m[nt][1] = -INFINITY;
+            l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+            for (int kk = 0; kk < NK; ++kk)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[kk][nt][i] = 0.f;
+        }
+
+        for (int i = 0; i < steps; ++i) {
+            cp_async_wait<NST - 2>();
+            __syncwarp();
+            issue(i + NST - 1);  // into the stage that step i - 1 has left
+            find(i + NST);
+            const uint8_t* sk = ring + (i % NST) * 2 * HALF;
+            const uint8_t* sv = sk + HALF;
+            const uint32_t mask = live[i % NST];
+
+            float s[NT][4];
+            {
+                float s2[NT][2][4];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) s2[nt][0][j] = s2[nt][1][j] = 0.f;
+                if (KV != KV_E4M3) {
+                    const int row = lane & 15;
+                    const uint32_t base = smem_addr(sk + row * ROW);
+#pragma unroll
+                    for (int kk = 0; kk < NK; ++kk)
+                        if (kk < nk) {
+                            uint32_t k4[4];
+                            ldsm_x4(k4, base + (((kk * 2 + (lane >> 4)) ^ (row & 7)) << 4));
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) mma16816<BF>(s2[nt][kk & 1], k4, qf[nt][kk][0], qf[nt][kk][1]);
+                        }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < (DP + 63) / 64; ++j) {
+                        const int col = j * 4 + t;
+                        const int sw = CHP >= 8 ? col ^ ((g & 1) << 2) : col;
+                        const uint4 lo = *reinterpret_cast<const uint4*>(sk + g * ROW + sw * 16);
+                        const uint4 hi = *reinterpret_cast<const uint4*>(sk + (g + 8) * ROW + sw * 16);
+                        const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            uint32_t k4[4];
+                            e4m3x4_to_f16(wl[q], k4[0], k4[2]);
+                            e4m3x4_to_f16(wh[q], k4[1], k4[3]);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma16816<false>(s2[nt][q & 1], k4, qf[nt][j * 4 + q][0], qf[nt][j * 4 + q][1]);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const bool on = (mask >> (g + (j >> 1) * 8)) & 1u;
+                        s[nt][j] = on ? (s2[nt][0][j] + s2[nt][1][j]) * sl[nt][j & 1] : -INFINITY;
+                    }
+            }
+
+            // running maximum and sum, p as hi + lo operands
+            uint32_t ph[NT][2], pl[NT][2];
+            float scale_o[NT][2];
+            bool grew = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float mx = fmaxf(s[nt][c], s[nt][c + 2]);
+                    mx = fmaxf(mx, __shfl_xor_sync(FULL_MASK, mx, 4));
+                    mx = fmaxf(mx, __shfl_xor_sync(FULL_MASK, mx, 8));
+                    mx = fmaxf(mx, __shfl_xor_sync(FULL_MASK, mx, 16));
+                    const float mn = fmaxf(m[nt][c], mx);
+                    grew |= mn > m[nt][c];
+                    const float mu = finite_or_zero(mn);
+                    scale_o[nt][c] = exp2_fast(m[nt][c] - mu);
+                    m[nt][c] = mn;
+                    s[nt][c] = exp2_fast(s[nt][c] - mu + P_SHIFT);
+                    s[nt][c + 2] = exp2_fast(s[nt][c + 2] - mu + P_SHIFT);
+                }
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const uint32_t hi = pack2<BF>(s[nt][2 * r], s[nt][2 * r + 1]);
+                    const float2 back = unpack2<BF>(hi);
+                    const uint32_t lo = pack2<BF>(s[nt][2 * r] - back.x, s[nt][2 * r + 1] - back.y);
+                    ph[nt][r] = transpose_8x8(hi);
+                    pl[nt][r] = transpose_8x8(lo);
+                }
+            }
+            if (__any_sync(FULL_MASK, grew)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    l[nt][0] *= scale_o[nt][0];
+                    l[nt][1] *= scale_o[nt][1];
+#pragma unroll
+                    for (int kk = 0; kk < NK; ++kk)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) o[kk][nt][j] *= scale_o[nt][j & 1];
+                }
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                l[nt][0] += s[nt][0] + s[nt][2];
+                l[nt][1] += s[nt][1] + s[nt][3];
+            }
+
+            if (KV != KV_E4M3) {
+                const int key = (lane & 7) + ((lane >> 4) << 3);
+                const uint32_t base = smem_addr(sv + key * ROW);
+#pragma unroll
+                for (int kk = 0; kk < NK; ++kk)
+                    if (kk < nk) {
+                        uint32_t v4[4];
+                        ldsm_x4_t(v4, base + (((kk * 2 + ((lane >> 3) & 1)) ^ (key & 7)) << 4));
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma16816<BF>(o[kk][nt], v4, ph[nt][0], ph[nt][1]);
+                            mma16816<BF>(o[kk][nt], v4, pl[nt][0], pl[nt][1]);
+                        }
+                    }
+            } else {
+                // 32 dims at a time: the thread's four codes (dims 32j + 4g ..) of
+                // keys 2t, 2t+1, 2t+8, 2t+9, interleaved into key pairs
+#pragma unroll
+                for (int j = 0; j < (DP + 31) / 32; ++j) {
+                    uint32_t w[4];
+                    const int col = j * 2 + (g >> 2);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int key = 2 * t + (r & 1) + (r >> 1) * 8;
+                        const int sw = CHP >= 8 ? col ^ (((key >> 1) & 3) << 1) : col ^ (((key >> 1) & 1) << 1);
+                        w[r] = *reinterpret_cast<const uint32_t*>(sv + key * ROW + sw * 16 + (g & 3) * 4);
+                    }
+                    uint32_t f[8];  // dims 4g + i: f[i] keys 2t, 2t+1; f[4 + i] keys 2t+8, 2t+9
+                    e4m3x4_to_f16(__byte_perm(w[0], w[1], 0x5140), f[0], f[1]);
+                    e4m3x4_to_f16(__byte_perm(w[0], w[1], 0x7362), f[2], f[3]);
+                    e4m3x4_to_f16(__byte_perm(w[2], w[3], 0x5140), f[4], f[5]);
+                    e4m3x4_to_f16(__byte_perm(w[2], w[3], 0x7362), f[6], f[7]);
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const uint32_t v4[4] = {f[2 * r], f[2 * r + 1], f[4 + 2 * r], f[4 + 2 * r + 1]};
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma16816<false>(o[2 * j + r][nt], v4, ph[nt][0], ph[nt][1]);
+                            mma16816<false>(o[2 * j + r][nt], v4, pl[nt][0], pl[nt][1]);
+                        }
+                    }
+                }
+            }
+        }
+        cp_async_wait<0>();
+
+        // combine the warps: o to shared memory (each warp over its own ring),
+        // weighted by exp2(m_warp - m)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float v = l[nt][c];
+                v += __shfl_xor_sync(FULL_MASK, v, 4);
+                v += __shfl_xor_sync(FULL_MASK, v, 8);
+                v += __shfl_xor_sync(FULL_MASK, v, 16);
+                if (g == 0) {
+                    sm_m[warp * NH + nt * 8 + 2 * t + c] = m[nt][c];
+                    sm_l[warp * NH + nt * 8 + 2 * t + c] = v;
+                }
+            }
+        __syncwarp();
+        float* so = reinterpret_cast<float*>(ring);  // [NH][DP]
+#pragma unroll
+        for (int kk = 0; kk < NK; ++kk)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int h = nt * 8 + 2 * t + (j & 1);
+                    const int dim = KV == KV_E4M3 ? (kk >> 1) * 32 + 4 * g + (kk & 1) * 2 + (j >> 1)
+                                                  : kk * 16 + g + (j >> 1) * 8;
+                    so[h * DP + dim] = o[kk][nt][j];
+                }
+        __syncthreads();
+
+        const bool whole = t0 == 0 && t1 == units;
+        const int slot = 2 * (int)blockIdx.x + (t0 == 0 ? 1 : 0);
+        float* ws_o = a.ws_o + (int64_t)slot * a.hpi * a.D;
+        float* ws_ml = a.ws_ml + (int64_t)slot * a.hpi * 2;
+        for (int e = tid; e < heads * a.D; e += ATT_THREADS) {
+            const int h = e / a.D, dim = e - h * a.D;
+            float mm = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < ATT_WARPS; ++w) mm = fmaxf(mm, sm_m[w * NH + h]);
+            const float mu = finite_or_zero(mm);
+            float sum = 0.f, ll = 0.f;
+#pragma unroll
+            for (int w = 0; w < ATT_WARPS; ++w) {
+                const float f = exp2_fast(sm_m[w * NH + h] - mu);
+                ll += f * sm_l[w * NH + h];
+                sum += f * reinterpret_cast<const float*>(smem + (size_t)w * NST * 2 * HALF)[h * DP + dim];
+            }
+            if (whole) {
+                store_head<QBF>(a, b, head0 + h, dim, sum, ll, mm, P_SHIFT);
+            } else {
+                ws_o[e] = sum;
+                if (dim == 0) {
+                    ws_ml[2 * h] = mm;
+                    ws_ml[2 * h + 1] = ll;
+                }
+            }
+        }
+
+        if (!whole) {
+            // the pieces of this item belong to blocks c1 .. c2
+            const int64_t first_u = before * items + (int64_t)item * units, last_u = first_u + units - 1;
+            const int c1 = (int)(((first_u + 1) * blocks - 1) / total);
+            const int c2 = (int)(((last_u + 1) * blocks - 1) / total);
+            __threadfence();
+            __syncthreads();
+            int* flag = reinterpret_cast<int*>(sm_warp);
+            if (tid == 0) {
+                const int pieces = c2 - c1 + 1;
+                const int old = atomicAdd(a.counters + c1, 1);
+                if (old < 0 || old >= pieces) atomicOr(a.err, MOE_DEVERR_WORKSPACE);
+                if (old == pieces - 1) {
+                    a.counters[c1] = 0;
+                    __threadfence();
+                }
+                *flag = old == pieces - 1;
+            }
+            __syncthreads();
+            if (*flag) {
+                for (int e = tid; e < heads * a.D; e += ATT_THREADS) {
+                    const int h = e / a.D, dim = e - h * a.D;
+                    float mm = -INFINITY;
+                    for (int c = c1; c <= c2; ++c)
+                        mm = fmaxf(mm, __ldcg(a.ws_ml + ((int64_t)(2 * c + (c == c1)) * a.hpi + h) * 2));
+                    const float mu = finite_or_zero(mm);
+                    float sum = 0.f, ll = 0.f;
+                    for (int c = c1; c <= c2; ++c) {
+                        const int64_t sl_ = 2 * c + (c == c1);
+                        const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.ws_ml + (sl_ * a.hpi + h) * 2));
+                        const float f = exp2_fast(ml.x - mu);
+                        ll += f * ml.y;
+                        sum += f * __ldcg(a.ws_o + sl_ * a.hpi * a.D + e);
+                    }
+                    store_head<QBF>(a, b, head0 + h, dim, sum, ll, mm, P_SHIFT);
+                }
+            }
+        }
+        __syncthreads();  // the ring and the flags are free again
+        u += t1 - t0;
+    }
+}
+
+template <int DP, int NT, int KV, bool QBF>
+static cudaError_t launch_attn(const AttnArgs& a, const DeviceInfo& di, cudaStream_t st) {
+    constexpr int ES = KV == KV_E4M3 ? 1 : 2;
+    const size_t smem = (size_t)ATT_WARPS * att_stages(DP, ES) * 2 * ATT_STEP * DP * ES +
+                        ATT_WARPS * att_stages(DP, ES) * 4 + 2 * ATT_WARPS * NT * 8 * 4 + 64 + (size_t)a.B * 8;
+    auto kernel = paged_attention_kernel<DP, NT, KV, QBF>;
+    static SmemOnce once;
+    cudaError_t e = once.set(reinterpret_cast<const void*>(kernel), di.max_smem_optin);
+    if (e != cudaSuccess) return e;
+    if (smem > (size_t)di.max_smem_optin) return cudaErrorInvalidValue;
+    int per_sm = (int)((size_t)di.smem_per_sm / (smem + 1024));
+    per_sm = per_sm < 1 ? 1 : (per_sm > 2 ? 2 : per_sm);
+    const int grid = min(di.sm_count * per_sm, ATTN_MAX_BLOCKS);
+    kernel<<<grid, ATT_THREADS, smem, st>>>(a);
+    return cudaGetLastError();
+}
+
+template <int KV, bool QBF>
+static cudaError_t launch_attn_kv(const AttnArgs& a, const DeviceInfo& di, cudaStream_t st) {
+    const bool two = a.hpi > 8;
+    if (a.D <= 64) return two ? launch_attn<64, 2, KV, QBF>(a, di, st) : launch_attn<64, 1, KV, QBF>(a, di, st);
+    if (a.D <= 128) return two ? launch_attn<128, 2, KV, QBF>(a, di, st) : launch_attn<128, 1, KV, QBF>(a, di, st);
+    return two ? launch_attn<256, 2, KV, QBF>(a, di, st) : launch_attn<256, 1, KV, QBF>(a, di, st);
+}
+
+// Query heads of one item: the group of a key-value head in equal parts of at
+// most 16 (two N tiles; a third would not leave registers for D = 256).
+int attn_heads_per_item(int G) {
+    const int chunks = (G + 15) / 16;
+    return (G + chunks - 1) / chunks;
+}
+
+size_t attn_workspace_bytes(int Hq, int Hkv, int D) {
+    const size_t hpi = attn_heads_per_item(Hq / Hkv);
+    return ATTN_COUNTER_BYTES + (size_t)2 * ATTN_MAX_BLOCKS * hpi * (D + 2) * 4;
+}
+
+cudaError_t launch_paged_attention(AttnArgs a, int dtype, int cache_dtype, void* ws, cudaStream_t st) {
+    DeviceInfo di;
+    const cudaError_t e = device_info(&di);
+    if (e != cudaSuccess) return e;
+    a.err = di.err_word;
+    a.G = a.Hq / a.Hkv;
+    a.hpi = attn_heads_per_item(a.G);
+    a.chunks = (a.G + a.hpi - 1) / a.hpi;
+    a.counters = static_cast<int*>(ws);
+    a.ws_ml = reinterpret_cast<float*>(static_cast<char*>(ws) + ATTN_COUNTER_BYTES);
+    a.ws_o = a.ws_ml + (size_t)2 * ATTN_MAX_BLOCKS * a.hpi * 2;
+    if (cache_dtype == MOE_E4M3)
+        return dtype == MOE_BF16 ? launch_attn_kv<KV_E4M3, true>(a, di, st) : launch_attn_kv<KV_E4M3, false>(a, di, st);
+    return dtype == MOE_BF16 ? launch_attn_kv<KV_BF16, true>(a, di, st) : launch_attn_kv<KV_F16, false>(a, di, st);
+}
+
+}  // namespace moedec

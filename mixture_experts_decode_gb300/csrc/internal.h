@@ -5,6 +5,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <mutex>
+
 namespace moedec {
 
 struct MXView {
@@ -89,5 +91,107 @@ size_t grouped_smem_bytes(int d, int I);
 cudaError_t launch_grouped(const uint16_t* x, int T, int d, const int32_t* ids, const float* w, int k, MXView wg,
                            MXView wu, MXView wd, MXView shg, MXView shu, MXView shd, int E, int I, bool act_mx,
                            const GroupedWorkspace& ws, uint16_t* y, cudaStream_t st);
+
+// Raises a kernel's dynamic shared memory limit once per device.
+struct SmemOnce {
+    std::mutex mu;
+    bool have[64] = {false};
+    cudaError_t set(const void* kernel, int bytes) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+        std::lock_guard<std::mutex> lock(mu);
+        if (have[dev]) return cudaSuccess;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e == cudaSuccess) have[dev] = true;
+        return e;
+    }
+};
+
+// Paged attention: blocks of a launch at most (a join counter and two pieces
+// of workspace each), and the counters' bytes at the start of the workspace.
+constexpr int ATTN_MAX_BLOCKS = 320;
+constexpr size_t ATTN_COUNTER_BYTES = 2048;  // MOE_ATTN_COUNTER_BYTES
+static_assert(ATTN_MAX_BLOCKS * 4 <= ATTN_COUNTER_BYTES, "a counter per block");
+struct AttnArgs {
+    const void* q;
+    int64_t q_sb, q_sh;  // strides in elements, here and below
+    const void* k;
+    int64_t k_sp, k_st, k_sh;  // page, token, head
+    const void* v;
+    int64_t v_sp, v_st, v_sh;
+    const int32_t* table;
+    int64_t table_stride;
+    const int32_t* lens;
+    int B, Hq, Hkv, D, num_pages, page, max_pages, window, sinks;
+    float scale_log2, v_scale;
+    void* out;
+    float* lse;
+    // filled by the launch
+    int G, hpi, chunks;  // query heads of a key-value head, of an item; items of a group
+    int* counters;
+    float* ws_ml;  // [2 * blocks][hpi][2] maximum and sum of a piece
+    float* ws_o;   // [2 * blocks][hpi][D]
+    int* err;
+};
+size_t attn_workspace_bytes(int Hq, int Hkv, int D);
+cudaError_t launch_paged_attention(AttnArgs a, int dtype, int cache_dtype, void* ws, cudaStream_t st);
+
+struct RopeArgs {
+    const void* q;
+    int64_t q_st, q_sh;  // token, head
+    const void* k;
+    int64_t k_st, k_sh;
+    const void* v;
+    int64_t v_st, v_sh;
+    void* q_out;
+    int64_t qo_st, qo_sh;
+    void* kc;
+    int64_t kc_sp, kc_st, kc_sh;
+    void* vc;
+    int64_t vc_sp, vc_st, vc_sh;
+    const int32_t* positions;
+    const int64_t* slots;
+    const double* freqs;
+    int T, Hq, Hkv, D, rot, interleaved, num_pages, page;
+    float mscale, k_scale, v_scale;
+    int* err;
+};
+cudaError_t launch_rope_append(RopeArgs a, int dtype, int cache_dtype, cudaStream_t st);
+
+struct NormSpec {
+    const void* w;
+    const void* b;
+    float eps;
+    int kind;  // MOE_NORM_*; -1: no norm
+};
+struct NormArgs {
+    const void* y;
+    int64_t y_stride;
+    const void* resid;
+    int64_t r_stride;
+    const void* gate;
+    int64_t gate_row, gate_col;  // strides in elements (0 broadcasts)
+    int gate_act;
+    float alpha;
+    NormSpec post, pre;
+    void* resid_out;
+    void* out;
+    int T, d;
+};
+cudaError_t launch_norm_residual(const NormArgs& a, int dtype, int resid_dtype, cudaStream_t st);
+
+struct Matvec4Args {
+    const void* x;
+    int64_t x_stride;
+    const uint8_t* codes;
+    const void* scales;
+    const uint8_t* zeros;
+    void* y;
+    int64_t y_stride;
+    int T, N, K, group;
+};
+cudaError_t launch_matvec4(const Matvec4Args& a, int dtype, cudaStream_t st);
 
 }  // namespace moedec
