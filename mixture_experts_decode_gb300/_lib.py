@@ -1,4 +1,5 @@
-"""ctypes binding of libmoedec.so: argument marshalling only.
+"""Binding of libmoedec.so: argument marshalling only (ctypes; the decode block's
+calls through the compiled module _block, which checks the same things faster).
 
 Every compute step runs in the library's CUDA kernels; this module checks
 tensor dtypes/devices, allocates outputs with torch when the caller gives
@@ -442,57 +443,26 @@ def mx_requant(x, out=None):
 
 # ------------------------------------------------- the block around the layer
 
-DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2, torch.float8_e4m3fn: 3}
-ATTN_COUNTER_BYTES = 2048
+_block_module = None
 
 
-def _is(t, name: str, dtype, device, ndim: int):
-    """Dtype, device and dimension checks of a strided tensor."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if t.dim() != ndim:
-        raise ValueError(f"{name} must have {ndim} dims, got {tuple(t.shape)}")
+def _fail(fn: str, rc: int):
+    raise MoEError(fn, rc, load().moe_strerror(rc).decode())
 
 
-def _half(t, name: str) -> int:
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in (torch.bfloat16, torch.float16):
-        raise TypeError(f"{name} must be bfloat16 or float16, got {t.dtype}")
-    return DTYPES[t.dtype]
-
-
-def _heads(t, name: str, dtype, device, shape=None):
-    """Strides of a [tokens, heads, D] tensor with contiguous heads' rows."""
-    _is(t, name, dtype, device, 3)
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    st, sh, sd = t.stride()
-    if sd != 1 and t.shape[2] > 1:
-        raise ValueError(f"{name}'s last dimension must be contiguous")
-    # the stride of a dimension of one element is free: 0 keeps it aligned
-    return (st if t.shape[0] > 1 else 0), (sh if t.shape[1] > 1 else 0)
-
-
-def _cache(t, name: str, dtype, device, scale: float):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype and t.dtype != torch.float8_e4m3fn:
-        raise TypeError(f"{name} must be {dtype} or float8_e4m3fn, got {t.dtype}")
-    _is(t, name, t.dtype, device, 4)
-    sp, st, sh, sd = t.stride()
-    if sd != 1 and t.shape[3] > 1:
-        raise ValueError(f"{name}'s last dimension must be contiguous")
-    n, p, h, _ = t.shape
-    return CacheView(t.data_ptr(), sp if n > 1 else 0, st if p > 1 else 0, sh if h > 1 else 0, scale)
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+def _block():
+    """The compiled binding (raises if it has not been built)."""
+    global _block_module
+    if _block_module is None:
+        load()
+        try:
+            from . import _block as module
+        except ImportError as e:
+            raise RuntimeError(f"the compiled binding _block.so cannot be loaded ({e}): build it first "
+                               "(python -m mixture_experts_decode_gb300.build)") from e
+        module.set_fail(_fail)
+        _block_module = module
+    return _block_module
 
 
 def attention_workspace_bytes(Hq: int, Hkv: int, D: int) -> int:
@@ -521,47 +491,8 @@ def paged_attention(q, k_cache, v_cache, block_table, seq_lens, scale: Optional[
     and sinks as in include/moedec.h.  Pass a kept workspace (see
     attention_workspace) to avoid clearing one per call.  Returns out
     [B, Hq, D], or (out, lse float32 [B, Hq]) with return_lse."""
-    lib = load()
-    dt = _half(q, "q")
-    dev = q.device
-    q_st, q_sh = _heads(q, "q", q.dtype, dev)
-    B, Hq, D = q.shape
-    kv = _cache(k_cache, "k_cache", q.dtype, dev, k_scale)
-    vv = _cache(v_cache, "v_cache", k_cache.dtype, dev, v_scale)
-    pages, page, Hkv, Dk = k_cache.shape
-    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype or Dk != D:
-        raise ValueError(f"k_cache and v_cache must be alike and have q's head size {D}, got "
-                         f"{tuple(k_cache.shape)} {k_cache.dtype} / {tuple(v_cache.shape)} {v_cache.dtype}")
-    _is(block_table, "block_table", torch.int32, dev, 2)
-    if block_table.shape[0] != B or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
-        raise ValueError("block_table must be [B, max_pages] with contiguous rows")
-    _need(seq_lens, "seq_lens", torch.int32, dev, 1)
-    if seq_lens.shape[0] != B:
-        raise ValueError("seq_lens must be [B]")
-    if workspace is None:
-        workspace = torch.empty(attention_workspace_bytes(Hq, Hkv, D), dtype=torch.uint8, device=dev)
-        workspace[:ATTN_COUNTER_BYTES].zero_()
-    else:
-        _need(workspace, "workspace", torch.uint8, dev)
-    if out is None:
-        out = torch.empty((B, Hq, D), dtype=q.dtype, device=dev)
-    else:
-        _need(out, "out", q.dtype, dev, 3)
-        if out.shape != q.shape:
-            raise ValueError("out must have q's shape")
-    if lse is not None:
-        _need(lse, "lse", torch.float32, dev, 2)
-        if lse.shape != (B, Hq):
-            raise ValueError("lse must be [B, Hq]")
-    elif return_lse:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
-    rc = lib.moe_paged_attention(
-        q.data_ptr(), q_st, q_sh, B, Hq, Hkv, D, dt, kv, vv, DTYPES[k_cache.dtype], pages, page,
-        block_table.data_ptr(), block_table.stride(0), block_table.shape[1], seq_lens.data_ptr(),
-        D ** -0.5 if scale is None else scale, window, sinks, workspace.data_ptr(), workspace.numel(), out.data_ptr(),
-        _ptr(lse), _stream(dev))
-    _check("moe_paged_attention", rc)
-    return (out, lse) if return_lse else out
+    return (_block_module or _block()).paged_attention(q, k_cache, v_cache, block_table, seq_lens, scale, window, sinks,
+                                                       k_scale, v_scale, workspace, out, return_lse, lse)
 
 
 ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3}
@@ -583,33 +514,8 @@ def rope_append(q, k, v, positions, slots, freqs, k_cache, v_cache, interleaved:
     page_size + row; negative: not written) of the caches [num_pages,
     page_size, Hkv, D], in place.  freqs float64 [rot / 2] on the device; the
     first rot dims of a head turn.  q_out may be q."""
-    lib = load()
-    dt = _half(q, "q")
-    dev = q.device
-    q_st, q_sh = _heads(q, "q", q.dtype, dev)
-    T, Hq, D = q.shape
-    kc = _cache(k_cache, "k_cache", q.dtype, dev, k_scale)
-    vc = _cache(v_cache, "v_cache", k_cache.dtype, dev, v_scale)
-    pages, page, Hkv, Dk = k_cache.shape
-    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype or Dk != D:
-        raise ValueError(f"k_cache and v_cache must be alike and have q's head size {D}, got "
-                         f"{tuple(k_cache.shape)} {k_cache.dtype} / {tuple(v_cache.shape)} {v_cache.dtype}")
-    k_st, k_sh = _heads(k, "k", q.dtype, dev, (T, Hkv, D))
-    v_st, v_sh = _heads(v, "v", q.dtype, dev, (T, Hkv, D))
-    _need(positions, "positions", torch.int32, dev, 1)
-    _need(slots, "slots", torch.int64, dev, 1)
-    _need(freqs, "freqs", torch.float64, dev, 1)
-    if positions.shape[0] != T or slots.shape[0] != T:
-        raise ValueError("positions and slots must be [T]")
-    if q_out is None:
-        q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=dev)
-    qo_st, qo_sh = _heads(q_out, "q_out", q.dtype, dev, (T, Hq, D))
-    rc = lib.moe_rope_append(
-        q.data_ptr(), q_st, q_sh, k.data_ptr(), k_st, k_sh, v.data_ptr(), v_st, v_sh, T, Hq, Hkv, D, dt,
-        positions.data_ptr(), slots.data_ptr(), freqs.data_ptr(), 2 * freqs.shape[0], int(bool(interleaved)), mscale,
-        kc, vc, DTYPES[k_cache.dtype], pages, page, q_out.data_ptr(), qo_st, qo_sh, _stream(dev))
-    _check("moe_rope_append", rc)
-    return q_out
+    return (_block_module or _block()).rope_append(q, k, v, positions, slots, freqs, k_cache, v_cache, interleaved,
+                                                   mscale, k_scale, v_scale, q_out)
 
 
 class Norm(NamedTuple):
@@ -620,19 +526,7 @@ class Norm(NamedTuple):
     kind: str = "rms"
 
 
-NORM_KINDS = {"rms": 0, "layer": 1}
 GATE_ACTS = {"none": 0, "sigmoid": 1}
-
-
-def _norm(n: Optional[Norm], name: str, dtype, device, d: int):
-    if n is None:
-        return None
-    for t, part in ((n.w, "w"), (n.b, "b")):
-        if t is not None:
-            _need(t, f"{name}.{part}", dtype, device, 1)
-            if t.shape[0] != d:
-                raise ValueError(f"{name}.{part} must be [{d}], got {tuple(t.shape)}")
-    return NormView(_ptr(n.w), _ptr(n.b), n.eps, NORM_KINDS[n.kind])
 
 
 def norm_residual(y, resid=None, post: Optional[Norm] = None, gate=None, gate_act: str = "none", alpha: float = 1.0,
@@ -645,50 +539,8 @@ def norm_residual(y, resid=None, post: Optional[Norm] = None, gate=None, gate_ac
     (r', x); r' has resid's dtype (y's without one) and may be written over
     resid (resid_out=resid), x has y's.  Without resid and resid_out, returns
     x alone."""
-    lib = load()
-    dt = _half(y, "y")
-    dev = y.device
-    _is(y, "y", y.dtype, dev, 2)
-    T, d = y.shape
-    if d > 1 and y.stride(1) != 1:
-        raise ValueError("y's last dimension must be contiguous")
-    r_dtype, r_stride = y.dtype, 0
-    if resid is not None:
-        r_dtype = resid.dtype
-        if r_dtype not in (y.dtype, torch.float32):
-            raise TypeError(f"resid must be {y.dtype} or float32, got {r_dtype}")
-        _is(resid, "resid", r_dtype, dev, 2)
-        if resid.shape != y.shape or (d > 1 and resid.stride(1) != 1):
-            raise ValueError("resid must have y's shape and contiguous rows")
-        r_stride = resid.stride(0)
-    g_row = g_col = 0
-    if gate is not None:
-        _is(gate, "gate", y.dtype, dev, 2)
-        gt, gd = gate.shape
-        if gt not in (1, T) or gd not in (1, d) or (gd > 1 and gate.stride(1) not in (0, 1)):
-            raise ValueError(f"gate must be [{T} or 1, {d} or 1] with contiguous rows, got {tuple(gate.shape)}")
-        g_row = gate.stride(0) if gt > 1 else 0
-        g_col = gate.stride(1) if gd > 1 else 0
-    vp, vq = _norm(post, "post", y.dtype, dev, d), _norm(pre, "pre", y.dtype, dev, d)
-    both = resid is not None or resid_out is not None
-    if both:
-        if resid_out is None:
-            resid_out = torch.empty((T, d), dtype=r_dtype, device=dev)
-        else:
-            _need(resid_out, "resid_out", r_dtype, dev, 2)
-            if resid_out.shape != y.shape:
-                raise ValueError("resid_out must have y's shape")
-    if out is None:
-        out = torch.empty((T, d), dtype=y.dtype, device=dev)
-    else:
-        _need(out, "out", y.dtype, dev, 2)
-        if out.shape != y.shape:
-            raise ValueError("out must have y's shape")
-    rc = lib.moe_norm_residual(y.data_ptr(), y.stride(0), T, d, dt, _ptr(resid), r_stride, DTYPES[r_dtype], _ref(vp),
-                               _ptr(gate), g_row, g_col, GATE_ACTS[gate_act], alpha, _ref(vq), _ptr(resid_out),
-                               out.data_ptr(), _stream(dev))
-    _check("moe_norm_residual", rc)
-    return (resid_out, out) if both else out
+    return (_block_module or _block()).norm_residual(y, resid, post, gate, GATE_ACTS[gate_act], alpha, pre, resid_out,
+                                                     out)
 
 
 class W4(NamedTuple):
@@ -702,30 +554,4 @@ class W4(NamedTuple):
 def matvec4(x, w: W4, y: Optional[torch.Tensor] = None):
     """moe_matvec4: x [T, K] BF16 or FP16 times 4-bit weights -> y [T, N]; the
     group size is K / w.scales.shape[1] (32, 64 or 128)."""
-    lib = load()
-    dt = _half(x, "x")
-    dev = x.device
-    _is(x, "x", x.dtype, dev, 2)
-    T, K = x.shape
-    if K > 1 and x.stride(1) != 1:
-        raise ValueError("x's last dimension must be contiguous")
-    _need(w.codes, "w.codes", torch.uint8, dev, 2)
-    _need(w.scales, "w.scales", x.dtype, dev, 2)
-    N, groups = w.scales.shape
-    if K % 2 or tuple(w.codes.shape) != (N, K // 2) or groups == 0 or K % groups:
-        raise ValueError(f"codes must be [N, K/2] and scales [N, K/group] for K = {K}, got "
-                         f"{tuple(w.codes.shape)} / {tuple(w.scales.shape)}")
-    if w.zeros is not None:
-        _need(w.zeros, "w.zeros", torch.uint8, dev, 2)
-        if w.zeros.shape != w.scales.shape:
-            raise ValueError("zeros must have the shape of scales")
-    if y is None:
-        y = torch.empty((T, N), dtype=x.dtype, device=dev)
-    else:
-        _is(y, "y", x.dtype, dev, 2)
-        if tuple(y.shape) != (T, N) or (N > 1 and y.stride(1) != 1):
-            raise ValueError("y must be [T, N] with contiguous rows")
-    rc = lib.moe_matvec4(x.data_ptr(), x.stride(0) if T > 1 else 0, T, K, dt, w.codes.data_ptr(), w.scales.data_ptr(), _ptr(w.zeros), N,
-                         K // groups, y.data_ptr(), y.stride(0), _stream(dev))
-    _check("moe_matvec4", rc)
-    return y
+    return (_block_module or _block()).matvec4(x, w, y)

@@ -1,4 +1,5 @@
-"""Build libmoedec.so (the C-ABI CUDA library) in-tree for sm_103a.
+"""Build libmoedec.so (the C-ABI CUDA library) in-tree for sm_103a, and _block.so
+(the compiled binding of the decode block's entry points, linked against it).
 
 Each .cu translation unit is compiled by its own nvcc process (in parallel),
 then linked into mixture_experts_decode_gb300/libmoedec.so with the static
@@ -11,12 +12,14 @@ import hashlib
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmoedec.so")
+BLOCK = os.path.join(PKG, "_block.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 SOURCES = ["api.cu", "gate_up.cu", "down.cu", "grouped.cu", "align.cu", "router.cu", "requant.cu", "decode_fp4.cu",
            "attention.cu", "rope.cu", "norm.cu", "matvec4.cu"]
@@ -45,14 +48,37 @@ def _digest(extra) -> str:
     return h.hexdigest()
 
 
+def _block_commands():
+    """(compile command without -o, its object's link command without -o) of _block.so."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")]
+    cxx = os.environ.get("CXX", "g++")
+    comp = [cxx, "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            *[f"-isystem{d}" for d in inc], "-c", os.path.join(CSRC, "binding.cpp")]
+    link = [cxx, "-shared", "-L" + os.path.join(root, "lib"), "-L" + PKG, "-Wl,-rpath,$ORIGIN"]
+    libs = ["-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-l:libmoedec.so"]
+    return comp, link, libs, torch.__version__
+
+
+def _run(cmd, what):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+    return r.stdout + r.stderr
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=(), lib_path: str = LIB) -> str:
     """Compile every CUDA source and link the library (default: the in-tree
     libmoedec.so; extra_flags/lib_path build a variant elsewhere); returns
     the library path."""
     extra = list(extra_flags)
-    want = _digest(extra)
+    in_tree = lib_path == LIB
+    comp, link, libs, torch_version = _block_commands()
+    want = _digest(extra + [torch_version])
     stamp = lib_path + ".src-sha"
-    if not force and os.path.exists(lib_path) and os.path.exists(stamp):
+    if not force and os.path.exists(lib_path) and os.path.exists(stamp) and (not in_tree or os.path.exists(BLOCK)):
         with open(stamp) as f:
             if f.read().strip() == want:
                 return lib_path
@@ -61,27 +87,29 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), lib_path: 
     obj_dir = os.path.join(BUILD_DIR, os.path.basename(lib_path) + ".objs")
     os.makedirs(obj_dir, exist_ok=True)
     nvcc = _nvcc()
+    block_obj = os.path.join(obj_dir, "binding.o")
 
     def compile_one(src):
+        if src == "binding.cpp":
+            return block_obj, _run([*comp, "-o", block_obj], "g++ for binding.cpp")
         obj = os.path.join(obj_dir, src.replace(".cu", ".o"))
-        cmd = [nvcc, *ARCH, *NVCC_FLAGS, *extra, "-c", os.path.join(CSRC, src), "-o", obj]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
-        return obj, r.stdout + r.stderr
+        return obj, _run([nvcc, *ARCH, *NVCC_FLAGS, *extra, "-c", os.path.join(CSRC, src), "-o", obj], f"nvcc for {src}")
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
-        results = list(ex.map(compile_one, SOURCES))
+    todo = SOURCES + (["binding.cpp"] if in_tree else [])
+    with cf.ThreadPoolExecutor(max_workers=len(todo)) as ex:
+        results = list(ex.map(compile_one, todo))
     if verbose:
         for _, log in results:
             if log.strip():
                 print(log)
     tmp = lib_path + f".tmp{os.getpid()}"
-    cmd = [nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *[o for o, _ in results]]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    _run([nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, "-Xlinker", "-soname=libmoedec.so",
+          *[o for o, _ in results if o != block_obj]], "link")
     os.replace(tmp, lib_path)
+    if in_tree:
+        tmp = BLOCK + f".tmp{os.getpid()}"
+        _run([*link, "-o", tmp, block_obj, *libs], "link of _block.so")
+        os.replace(tmp, BLOCK)
     with open(stamp, "w") as f:
         f.write(want + "\n")
     return lib_path
