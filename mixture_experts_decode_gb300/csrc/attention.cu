@@ -127,22 +127,127 @@ __device__ __forceinline__ Visible visible_keys(int n, int window, int sinks) {
     return {head + window, head, start - head};
 }
 
-// One output value from its joined sums; l = 0 (no visible key, or every score
-// -inf) gives 0 and a log-sum of -inf.
+__device__ __forceinline__ void add_scaled(float4& s, float f, const float4& v) {
+    s.x += f * v.x, s.y += f * v.y, s.z += f * v.z, s.w += f * v.w;
+}
+
+// Four output values of a head from its joined sums; ml = (maximum, l).
+// l = 0 (no visible key, or every score -inf) gives 0 and a log-sum of -inf.
 template <bool QBF>
-__device__ __forceinline__ void store_head(const AttnArgs& a, int b, int h, int dim, float sum, float l, float m,
-                                           float shift) {
+__device__ __forceinline__ void store_head4(const AttnArgs& a, int b, int h, int dim, const float4& sum, float2 ml,
+                                            float shift) {
     const int64_t row = (int64_t)b * a.Hq + h;
-    const float v = l == 0.f ? 0.f : sum / l * a.v_scale;
-    if (QBF)
-        static_cast<__nv_bfloat16*>(a.out)[row * a.D + dim] = __float2bfloat16_rn(v);
-    else
-        static_cast<__half*>(a.out)[row * a.D + dim] = __float2half_rn(v);
-    if (dim == 0 && a.lse) a.lse[row] = l == 0.f ? -INFINITY : (m - shift + log2f(l)) * 0.693147180559945309f;
+    const float f = ml.y == 0.f ? 0.f : a.v_scale / ml.y;
+    float v[4] = {sum.x * f, sum.y * f, sum.z * f, sum.w * f};
+    uint16_t* out = static_cast<uint16_t*>(a.out) + row * a.D + dim;
+    const uint32_t lo = pack2<QBF>(v[0], v[1]), hi = pack2<QBF>(v[2], v[3]);
+    if (a.out_aligned) {
+        *reinterpret_cast<uint2*>(out) = make_uint2(lo, hi);
+    } else {
+        out[0] = (uint16_t)lo, out[1] = (uint16_t)(lo >> 16);
+        out[2] = (uint16_t)hi, out[3] = (uint16_t)(hi >> 16);
+    }
+    if (dim == 0 && a.lse) a.lse[row] = ml.y == 0.f ? -INFINITY : (ml.x - shift + log2f(ml.y)) * 0.693147180559945309f;
+}
+
+// Joins n pieces of an item, piece i at slot(i), in their order: the sums go
+// to `put` four dims at a time with the joined (maximum, l).  Called by a
+// whole block; factors live in sm_f [n][heads] (n <= ATT_JOIN_MOST).
+constexpr int ATT_JOIN = 8;                                     // pieces of a group
+constexpr int ATT_JOIN_MOST = ATTN_MAX_BLOCKS / ATT_JOIN + 1;   // groups of an item
+template <class Slot, class Put>
+__device__ __forceinline__ void join_slots(const AttnArgs& a, int n, int heads, float2* head_ml, float* sm_f, Slot slot,
+                                           Put put) {
+    const float2* mls = reinterpret_cast<const float2*>(a.ws_ml);
+    for (int i = threadIdx.x; i < n * heads; i += ATT_THREADS) {
+        const int p = i / heads, h = i - p * heads;
+        const float2 v = __ldcg(mls + (int64_t)slot(p) * a.hpi + h);
+        sm_f[2 * i] = v.x;
+        sm_f[2 * i + 1] = v.y;
+    }
+    __syncthreads();
+    if ((int)threadIdx.x < heads) {
+        const int h = threadIdx.x;
+        float mm = -INFINITY, ll = 0.f;
+        for (int p = 0; p < n; ++p) mm = fmaxf(mm, sm_f[2 * (p * heads + h)]);
+        const float mu = finite_or_zero(mm);
+        for (int p = 0; p < n; ++p) {
+            const float f = exp2_fast(sm_f[2 * (p * heads + h)] - mu);
+            ll += f * sm_f[2 * (p * heads + h) + 1];
+            sm_f[2 * (p * heads + h)] = f;
+        }
+        head_ml[h] = make_float2(mm, ll);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < heads * (a.D / 4); e += ATT_THREADS) {
+        const int h = e / (a.D / 4), dim = (e - h * (a.D / 4)) * 4;
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int p0 = 0; p0 < n; p0 += 8) {
+            float4 v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)  // the last piece again beyond the end
+                v[i] = __ldcg(reinterpret_cast<const float4*>(a.ws_o + ((int64_t)slot(min(p0 + i, n - 1)) * a.hpi + h) * a.D + dim));
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (p0 + i < n) add_scaled(sum, sm_f[2 * ((p0 + i) * heads + h)], v[i]);
+        }
+        put(h, dim, sum);
+    }
+}
+
+// True in every thread of the block that is the last of `n` to arrive at the
+// counter, which is then zero again.  What the blocks wrote before is visible
+// to it.
+__device__ __forceinline__ bool arrive_last(int* counter, int n, int* err, int* flag) {
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        const int old = atomicAdd(counter, 1);
+        if (old < 0 || old >= n) atomicOr(err, MOE_DEVERR_WORKSPACE);
+        if (old == n - 1) *counter = 0;
+        __threadfence();
+        *flag = old == n - 1;
+    }
+    __syncthreads();
+    return *flag != 0;
+}
+
+// The pieces of an item cut over blocks c1 .. c2 (this block's is written):
+// the last block of each eight joins theirs into the first one's place, the
+// last of those joins the groups (one level where eight blocks suffice), so
+// no block reads more than 41 pieces.  Counters: an item's first group by c1
+// (no other item begins in that block and goes on), its later groups and the
+// item itself by block / 8 (an item of more than eight blocks is the only one
+// with a later group, or an end, in such a place).
+template <bool QBF>
+__device__ __noinline__ void join_pieces(const AttnArgs& a, int c1, int c2, int b, int head0, int heads, float shift,
+                                         float2* head_ml, float* sm_f, int* flag) {
+    const int pieces = c2 - c1 + 1;
+    const int grp = ((int)blockIdx.x - c1) / ATT_JOIN;
+    const int g0 = c1 + grp * ATT_JOIN;
+    const int in_group = min(ATT_JOIN, pieces - grp * ATT_JOIN);
+    int* const later = a.counters + ATTN_MAX_BLOCKS;
+    int* const ends = later + ATT_JOIN_MOST;
+    auto slot = [&](int c) { return 2 * c + (c == c1 ? 1 : 0); };
+    auto finish = [&](int h, int dim, const float4& sum) { store_head4<QBF>(a, b, head0 + h, dim, sum, head_ml[h], shift); };
+    if (!arrive_last(grp == 0 ? a.counters + c1 : later + g0 / ATT_JOIN, in_group, a.err, flag)) return;
+    if (pieces <= ATT_JOIN) {
+        join_slots(a, pieces, heads, head_ml, sm_f, [&](int p) { return slot(c1 + p); }, finish);
+        return;
+    }
+    const int64_t to = (int64_t)slot(g0) * a.hpi;
+    join_slots(a, in_group, heads, head_ml, sm_f, [&](int p) { return slot(g0 + p); }, [&](int h, int dim, const float4& sum) {
+        // (each thread has read its own place of every piece by now)
+        *reinterpret_cast<float4*>(a.ws_o + (to + h) * a.D + dim) = sum;
+    });
+    if ((int)threadIdx.x < heads) reinterpret_cast<float2*>(a.ws_ml)[to + threadIdx.x] = head_ml[threadIdx.x];
+    const int groups = (pieces + ATT_JOIN - 1) / ATT_JOIN;
+    if (!arrive_last(ends + c1 / ATT_JOIN, groups, a.err, flag)) return;
+    join_slots(a, groups, heads, head_ml, sm_f, [&](int p) { return slot(c1 + p * ATT_JOIN); }, finish);
 }
 
 template <int DP, int NT, int KV, bool QBF>
-__global__ void __launch_bounds__(ATT_THREADS) paged_attention_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(ATT_THREADS) paged_attention_kernel(const __grid_constant__ AttnArgs a) {
     constexpr int ES = KV == KV_E4M3 ? 1 : 2;
     constexpr bool BF = KV == KV_BF16;  // operand type of the products
     constexpr int ROW = DP * ES;        // bytes of a key's row in shared memory
@@ -161,7 +266,8 @@ __global__ void __launch_bounds__(ATT_THREADS) paged_attention_kernel(const Attn
     uint32_t* live = reinterpret_cast<uint32_t*>(tail) + warp * NST;  // readable keys of each stage
     float* sm_m = reinterpret_cast<float*>(tail + ATT_WARPS * NST * 4);  // [warps][NH]
     float* sm_l = sm_m + ATT_WARPS * NH;
-    int64_t* sm_warp = reinterpret_cast<int64_t*>(sm_l + ATT_WARPS * NH);  // [warps] + carry
+    float2* head_ml = reinterpret_cast<float2*>(sm_l + ATT_WARPS * NH);      // [NH]
+    int64_t* sm_warp = reinterpret_cast<int64_t*>(head_ml + NH);            // [warps] + carry
     int64_t* prefix = sm_warp + 8;                                         // [B] units up to and with b
 
     const int nk = a.D / 16;
@@ -289,7 +395,7 @@ __global__ void __launch_bounds__(ATT_THREADS) paged_attention_kernel(const Attn
             cp_async_commit();
         };
         find(0);
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < NST - 1; ++i) {
             issue(i);
             find(i + 1);
@@ -537,71 +643,45 @@ __global__ void __launch_bounds__(ATT_THREADS) paged_attention_kernel(const Attn
                 }
         __syncthreads();
 
-        const bool whole = t0 == 0 && t1 == units;
-        const int slot = 2 * (int)blockIdx.x + (t0 == 0 ? 1 : 0);
-        float* ws_o = a.ws_o + (int64_t)slot * a.hpi * a.D;
-        float* ws_ml = a.ws_ml + (int64_t)slot * a.hpi * 2;
-        for (int e = tid; e < heads * a.D; e += ATT_THREADS) {
-            const int h = e / a.D, dim = e - h * a.D;
+        // factors of the warps' sums, once per head: exp2(m_warp - m)
+        if (tid < NH) {
             float mm = -INFINITY;
 #pragma unroll
-            for (int w = 0; w < ATT_WARPS; ++w) mm = fmaxf(mm, sm_m[w * NH + h]);
+            for (int w = 0; w < ATT_WARPS; ++w) mm = fmaxf(mm, sm_m[w * NH + tid]);
             const float mu = finite_or_zero(mm);
-            float sum = 0.f, ll = 0.f;
+            float ll = 0.f;
 #pragma unroll
             for (int w = 0; w < ATT_WARPS; ++w) {
-                const float f = exp2_fast(sm_m[w * NH + h] - mu);
-                ll += f * sm_l[w * NH + h];
-                sum += f * reinterpret_cast<const float*>(smem + (size_t)w * NST * 2 * HALF)[h * DP + dim];
+                const float f = exp2_fast(sm_m[w * NH + tid] - mu);
+                ll += f * sm_l[w * NH + tid];
+                sm_m[w * NH + tid] = f;
             }
-            if (whole) {
-                store_head<QBF>(a, b, head0 + h, dim, sum, ll, mm, P_SHIFT);
-            } else {
-                ws_o[e] = sum;
-                if (dim == 0) {
-                    ws_ml[2 * h] = mm;
-                    ws_ml[2 * h + 1] = ll;
-                }
-            }
+            head_ml[tid] = make_float2(mm, ll);
         }
-
+        __syncthreads();
+        const bool whole = t0 == 0 && t1 == units;
+        const int slot = 2 * (int)blockIdx.x + (t0 == 0 ? 1 : 0);
+        const int vecs = heads * (a.D / 4);  // four dims a thread
+        for (int e = tid; e < vecs; e += ATT_THREADS) {
+            const int h = e / (a.D / 4), dim = (e - h * (a.D / 4)) * 4;
+            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < ATT_WARPS; ++w)
+                add_scaled(sum, sm_m[w * NH + h],
+                           *reinterpret_cast<const float4*>(smem + (size_t)w * NST * 2 * HALF + (h * DP + dim) * 4));
+            if (whole)
+                store_head4<QBF>(a, b, head0 + h, dim, sum, head_ml[h], P_SHIFT);
+            else
+                *reinterpret_cast<float4*>(a.ws_o + ((int64_t)slot * a.hpi + h) * a.D + dim) = sum;
+        }
         if (!whole) {
+            if (tid < heads) reinterpret_cast<float2*>(a.ws_ml)[(int64_t)slot * a.hpi + tid] = head_ml[tid];
             // the pieces of this item belong to blocks c1 .. c2
             const int64_t first_u = before * items + (int64_t)item * units, last_u = first_u + units - 1;
             const int c1 = (int)(((first_u + 1) * blocks - 1) / total);
             const int c2 = (int)(((last_u + 1) * blocks - 1) / total);
-            __threadfence();
-            __syncthreads();
-            int* flag = reinterpret_cast<int*>(sm_warp);
-            if (tid == 0) {
-                const int pieces = c2 - c1 + 1;
-                const int old = atomicAdd(a.counters + c1, 1);
-                if (old < 0 || old >= pieces) atomicOr(a.err, MOE_DEVERR_WORKSPACE);
-                if (old == pieces - 1) {
-                    a.counters[c1] = 0;
-                    __threadfence();
-                }
-                *flag = old == pieces - 1;
-            }
-            __syncthreads();
-            if (*flag) {
-                for (int e = tid; e < heads * a.D; e += ATT_THREADS) {
-                    const int h = e / a.D, dim = e - h * a.D;
-                    float mm = -INFINITY;
-                    for (int c = c1; c <= c2; ++c)
-                        mm = fmaxf(mm, __ldcg(a.ws_ml + ((int64_t)(2 * c + (c == c1)) * a.hpi + h) * 2));
-                    const float mu = finite_or_zero(mm);
-                    float sum = 0.f, ll = 0.f;
-                    for (int c = c1; c <= c2; ++c) {
-                        const int64_t sl_ = 2 * c + (c == c1);
-                        const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.ws_ml + (sl_ * a.hpi + h) * 2));
-                        const float f = exp2_fast(ml.x - mu);
-                        ll += f * ml.y;
-                        sum += f * __ldcg(a.ws_o + sl_ * a.hpi * a.D + e);
-                    }
-                    store_head<QBF>(a, b, head0 + h, dim, sum, ll, mm, P_SHIFT);
-                }
-            }
+            join_pieces<QBF>(a, c1, c2, b, head0, heads, P_SHIFT, head_ml, reinterpret_cast<float*>(smem),
+                             reinterpret_cast<int*>(sm_warp));
         }
         __syncthreads();  // the ring and the flags are free again
         u += t1 - t0;
@@ -612,7 +692,7 @@ template <int DP, int NT, int KV, bool QBF>
 static cudaError_t launch_attn(const AttnArgs& a, const DeviceInfo& di, cudaStream_t st) {
     constexpr int ES = KV == KV_E4M3 ? 1 : 2;
     const size_t smem = (size_t)ATT_WARPS * att_stages(DP, ES) * 2 * ATT_STEP * DP * ES +
-                        ATT_WARPS * att_stages(DP, ES) * 4 + 2 * ATT_WARPS * NT * 8 * 4 + 64 + (size_t)a.B * 8;
+                        ATT_WARPS * att_stages(DP, ES) * 4 + 2 * ATT_WARPS * NT * 8 * 4 + NT * 8 * 8 + 64 + (size_t)a.B * 8;
     auto kernel = paged_attention_kernel<DP, NT, KV, QBF>;
     static SmemOnce once;
     cudaError_t e = once.set(reinterpret_cast<const void*>(kernel), di.max_smem_optin);
@@ -653,6 +733,7 @@ cudaError_t launch_paged_attention(AttnArgs a, int dtype, int cache_dtype, void*
     a.G = a.Hq / a.Hkv;
     a.hpi = attn_heads_per_item(a.G);
     a.chunks = (a.G + a.hpi - 1) / a.hpi;
+    a.out_aligned = reinterpret_cast<uintptr_t>(a.out) % 8 == 0;
     a.counters = static_cast<int*>(ws);
     a.ws_ml = reinterpret_cast<float*>(static_cast<char*>(ws) + ATTN_COUNTER_BYTES);
     a.ws_o = a.ws_ml + (size_t)2 * ATTN_MAX_BLOCKS * a.hpi * 2;

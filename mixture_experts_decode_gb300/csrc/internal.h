@@ -113,7 +113,7 @@ struct SmemOnce {
 // of workspace each), and the counters' bytes at the start of the workspace.
 constexpr int ATTN_MAX_BLOCKS = 320;
 constexpr size_t ATTN_COUNTER_BYTES = 2048;  // MOE_ATTN_COUNTER_BYTES
-static_assert(ATTN_MAX_BLOCKS * 4 <= ATTN_COUNTER_BYTES, "a counter per block");
+static_assert((ATTN_MAX_BLOCKS + 2 * (ATTN_MAX_BLOCKS / 8 + 1)) * 4 <= ATTN_COUNTER_BYTES, "a counter per block, two per eight");
 struct AttnArgs {
     const void* q;
     int64_t q_sb, q_sh;  // strides in elements, here and below
@@ -129,6 +129,7 @@ struct AttnArgs {
     void* out;
     float* lse;
     // filled by the launch
+    bool out_aligned;    // to 8 bytes
     int G, hpi, chunks;  // query heads of a key-value head, of an item; items of a group
     int* counters;
     float* ws_ml;  // [2 * blocks][hpi][2] maximum and sum of a piece
