@@ -10,10 +10,12 @@
 // output is rounded once; a layer norm's variance is the mean of the centred
 // squares (a second reduction), not a difference of moments.
 //
-// Bound: HBM, every operand in or out once.  A warp or a block holds a row
-// (vectors of 8 elements, at most 4 per thread), so statistics cost one
-// reduction in registers each; rows that are odd, unaligned or longer than
-// 16384 go through a block with the row in shared memory.
+// Bound: HBM, every operand in or out once; for one row, latency.  One to
+// sixteen warps hold a row, as NV vectors of VW elements per thread: VW is 8,
+// or what d and the addresses allow (4, 1).  The residual and the gate are
+// loaded as they lie before the first reduction, and kept unconverted until
+// used, so that two blocks of 512 threads fit an SM and one's loads run under
+// the other's reductions.  Rows beyond 16384 go through shared memory.
 #include <algorithm>
 
 #include "common.cuh"
@@ -42,37 +44,91 @@ __device__ __forceinline__ uint16_t norm_from_f(float f) {
     }
     return r;
 }
+template <bool BF>
+__device__ __forceinline__ float2 norm_to_f2(uint32_t w) {
+    if (BF) return bf16x2_to_float2(w);
+    __half2 h;
+    memcpy(&h, &w, 4);
+    return __half22float2(h);
+}
+template <bool BF>
+__device__ __forceinline__ uint32_t norm_from_f2(float a, float b) {
+    uint32_t r;
+    if (BF)
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    else
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+}
 
-// Eight consecutive elements, 16-bit or (F32) 32-bit.
-template <bool BF, bool F32>
-__device__ __forceinline__ void row_load8(const void* p, int64_t at, float (&f)[8]) {
-    if (F32) {
-        const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
-        const float4 a = q[0], b = q[1];
-        f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
-        f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-    } else {
-        const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// VW consecutive elements as they lie in memory: 16-bit (F32 false) or 32-bit.
+template <int VW, bool F32>
+struct Raw {
+    uint32_t w[F32 ? VW : (VW + 1) / 2];
+};
+template <int VW, bool F32>
+__device__ __forceinline__ Raw<VW, F32> raw_load(const void* p, int64_t at) {
+    Raw<VW, F32> r;
+    if constexpr (F32) {
+        const float* q = static_cast<const float*>(p) + at;
+        if constexpr (VW >= 4) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[2 * i] = norm_to_f<BF>((uint16_t)w[i]);
-            f[2 * i + 1] = norm_to_f<BF>((uint16_t)(w[i] >> 16));
+            for (int i = 0; i < VW / 4; ++i) {
+                const uint4 v = reinterpret_cast<const uint4*>(q)[i];
+                r.w[4 * i] = v.x, r.w[4 * i + 1] = v.y, r.w[4 * i + 2] = v.z, r.w[4 * i + 3] = v.w;
+            }
+        } else {
+            r.w[0] = __float_as_uint(q[0]);
+        }
+    } else {
+        const uint16_t* q = static_cast<const uint16_t*>(p) + at;
+        if constexpr (VW == 8) {
+            const uint4 v = *reinterpret_cast<const uint4*>(q);
+            r.w[0] = v.x, r.w[1] = v.y, r.w[2] = v.z, r.w[3] = v.w;
+        } else if constexpr (VW == 4) {
+            const uint2 v = *reinterpret_cast<const uint2*>(q);
+            r.w[0] = v.x, r.w[1] = v.y;
+        } else {
+            r.w[0] = q[0];
+        }
+    }
+    return r;
+}
+template <int VW, bool BF, bool F32>
+__device__ __forceinline__ void raw_floats(const Raw<VW, F32>& r, float (&f)[VW]) {
+    if constexpr (F32) {
+#pragma unroll
+        for (int j = 0; j < VW; ++j) f[j] = __uint_as_float(r.w[j]);
+    } else if constexpr (VW == 1) {
+        f[0] = norm_to_f<BF>((uint16_t)r.w[0]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < VW / 2; ++j) {
+            const float2 v = norm_to_f2<BF>(r.w[j]);
+            f[2 * j] = v.x, f[2 * j + 1] = v.y;
         }
     }
 }
-template <bool BF, bool F32>
-__device__ __forceinline__ void row_store8(void* p, int64_t at, const float (&f)[8]) {
-    if (F32) {
-        float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + at);
-        q[0] = make_float4(f[0], f[1], f[2], f[3]);
-        q[1] = make_float4(f[4], f[5], f[6], f[7]);
-    } else {
-        uint32_t w[4];
+template <int VW, bool BF, bool F32>
+__device__ __forceinline__ void raw_store(void* p, int64_t at, const float (&f)[VW]) {
+    if constexpr (F32) {
+        float* q = static_cast<float*>(p) + at;
+        if constexpr (VW >= 4) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            w[i] = (uint32_t)norm_from_f<BF>(f[2 * i]) | (uint32_t)norm_from_f<BF>(f[2 * i + 1]) << 16;
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int i = 0; i < VW / 4; ++i)
+                reinterpret_cast<float4*>(q)[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+        } else {
+            q[0] = f[0];
+        }
+    } else {
+        uint16_t* q = static_cast<uint16_t*>(p) + at;
+        if constexpr (VW == 8)
+            *reinterpret_cast<uint4*>(q) = make_uint4(norm_from_f2<BF>(f[0], f[1]), norm_from_f2<BF>(f[2], f[3]),
+                                                      norm_from_f2<BF>(f[4], f[5]), norm_from_f2<BF>(f[6], f[7]));
+        else if constexpr (VW == 4)
+            *reinterpret_cast<uint2*>(q) = make_uint2(norm_from_f2<BF>(f[0], f[1]), norm_from_f2<BF>(f[2], f[3]));
+        else
+            q[0] = norm_from_f<BF>(f[0]);
     }
 }
 template <bool BF, bool F32>
@@ -86,8 +142,10 @@ __device__ __forceinline__ void row_store(void* p, int64_t at, float f) {
     else
         static_cast<uint16_t*>(p)[at] = norm_from_f<BF>(f);
 }
+// (the fast exponential and reciprocal are off by a few units of 2^-22 for
+// gates of ordinary size, far below any output's rounding)
 __device__ __forceinline__ float gate_value(float g, int act) {
-    return act == MOE_GATE_SIGMOID ? 1.f / (1.f + expf(-g)) : g;
+    return act == MOE_GATE_SIGMOID ? __fdividef(1.f, 1.f + __expf(-g)) : g;
 }
 
 // Sum over the WARPS warps that hold a row; scratch[2][32] alternates so that
@@ -102,46 +160,52 @@ __device__ __forceinline__ float row_sum(float v, float (*scratch)[32], int& pha
     __syncthreads();
     v = lane < WARPS ? scratch[phase][lane] : 0.f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(FULL_MASK, v, o);
+    for (int o = WARPS / 2; o > 0; o >>= 1) v += __shfl_xor_sync(FULL_MASK, v, o);
+    v = __shfl_sync(FULL_MASK, v, 0);
     phase ^= 1;
     return v;
 }
 
-// The norm of a row held as NV vectors per thread.
-template <int WARPS, int NV, bool BF>
-__device__ __forceinline__ void norm_row(float (&f)[NV][8], const NormSpec& s, int d, int first, int stride,
+// The norm of a row held as NV vectors per thread (zeros beyond d).
+template <int WARPS, int NV, int VW, bool BF>
+__device__ __forceinline__ void norm_row(float (&f)[NV][VW], const NormSpec& s, int d, int first,
                                          float (*scratch)[32], int& phase) {
-    float mean = 0.f;
+    constexpr int stride = WARPS * 32;
     if (s.kind == MOE_NORM_LAYER) {
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum += f[i][j];
-        mean = row_sum<WARPS>(sum, scratch, phase) / d;
+            for (int j = 0; j < VW; ++j) sum += f[i][j];
+        const float mean = row_sum<WARPS>(sum, scratch, phase) / d;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if ((first + i * stride) * VW < d)
+#pragma unroll
+                for (int j = 0; j < VW; ++j) f[i][j] -= mean;
     }
     float sq = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-        if ((first + i * stride) * 8 < d)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                f[i][j] -= mean;
-                sq += f[i][j] * f[i][j];
-            }
+        for (int j = 0; j < VW; ++j) sq += f[i][j] * f[i][j];
     const float inv = 1.f / sqrtf(row_sum<WARPS>(sq, scratch, phase) / d + s.eps);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int at = (first + i * stride) * 8;
+        const int at = (first + i * stride) * VW;
         if (at < d) {
-            float w[8];
-            if (s.w) row_load8<BF, false>(s.w, at, w);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) f[i][j] *= s.w ? inv * w[j] : inv;
+            for (int j = 0; j < VW; ++j) f[i][j] *= inv;
+            float w[VW];
+            if (s.w) {
+                raw_floats<VW, BF, false>(raw_load<VW, false>(s.w, at), w);
+#pragma unroll
+                for (int j = 0; j < VW; ++j) f[i][j] *= w[j];
+            }
             if (s.b) {
-                row_load8<BF, false>(s.b, at, w);
+                raw_floats<VW, BF, false>(raw_load<VW, false>(s.b, at), w);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) f[i][j] += w[j];
+                for (int j = 0; j < VW; ++j) f[i][j] += w[j];
             }
         }
     }
@@ -149,57 +213,74 @@ __device__ __forceinline__ void norm_row(float (&f)[NV][8], const NormSpec& s, i
 
 }  // namespace
 
-// WARPS warps hold a row, NV vectors per thread (WARPS = 1: four rows per
-// block, one per warp).
-template <int WARPS, int NV, bool BF, bool RF>
-__global__ void __launch_bounds__(WARPS == 1 ? 128 : WARPS * 32) norm_rows_kernel(const NormArgs a) {
+// Blocks per SM that the registers are cut for: as many as do not spill.
+constexpr int norm_min_blocks(int warps, int nv, int vw) {
+    const bool heavy = nv * vw > 16 || nv >= 16;
+    return warps == 16 ? (heavy ? 1 : 2) : warps == 8 ? 4 : heavy ? 4 : 8;
+}
+
+// WARPS warps hold a row, NV vectors of VW elements per thread (WARPS = 1:
+// four rows per block, one per warp).
+template <int WARPS, int NV, int VW, bool BF, bool RF>
+__global__ void __launch_bounds__(WARPS == 1 ? 128 : WARPS * 32, norm_min_blocks(WARPS, NV, VW))
+    norm_rows_kernel(const NormArgs a) {
     __shared__ float scratch[2][32];
-    const int warp = threadIdx.x >> 5;
-    const int row = WARPS == 1 ? blockIdx.x * 4 + warp : blockIdx.x;
+    const int64_t row = WARPS == 1 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5) : blockIdx.x;
     if (row >= a.T) return;  // (WARPS = 1 has no barriers)
     const int first = WARPS == 1 ? threadIdx.x & 31 : threadIdx.x;
     constexpr int stride = WARPS * 32;
+    const bool gate_full = a.gate && a.gate_col;
     int phase = 0;
-    float f[NV][8];
+    float f[NV][VW];
+    Raw<VW, RF> r[NV];
+    Raw<VW, false> gt[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int at = (first + i * stride) * 8;
-        if (at < a.d)
-            row_load8<BF, false>(a.y, row * a.y_stride + at, f[i]);
-        else
-#pragma unroll
-            for (int j = 0; j < 8; ++j) f[i][j] = 0.f;
-    }
-    // the residual and the gate are on their way while the first norm reduces
-    float r[NV][8], gt[NV][8];
-    const float row_gate = a.gate && a.gate_col == 0
-                               ? gate_value(row_load<BF, false>(a.gate, row * a.gate_row), a.gate_act) : 1.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int at = (first + i * stride) * 8;
-        if (at < a.d && a.resid) row_load8<BF, RF>(a.resid, row * a.r_stride + at, r[i]);
-        if (at < a.d && a.gate && a.gate_col) row_load8<BF, false>(a.gate, row * a.gate_row + at, gt[i]);
-    }
-    if (a.post.kind >= 0) norm_row<WARPS, NV, BF>(f, a.post, a.d, first, stride, scratch, phase);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int at = (first + i * stride) * 8;
+        const int at = (first + i * stride) * VW;
         if (at < a.d) {
+            raw_floats<VW, BF, false>(raw_load<VW, false>(a.y, row * a.y_stride + at), f[i]);
+            if (a.resid) r[i] = raw_load<VW, RF>(a.resid, row * a.r_stride + at);
+            if (gate_full) gt[i] = raw_load<VW, false>(a.gate, row * a.gate_row + at);
+        } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float gv = a.gate && a.gate_col ? gate_value(gt[i][j], a.gate_act) : row_gate;
-                const float u = a.alpha * (a.gate ? f[i][j] * gv : f[i][j]);
-                f[i][j] = a.resid ? r[i][j] + u : u;
+            for (int j = 0; j < VW; ++j) f[i][j] = 0.f;
+        }
+    }
+    const float scale = a.alpha * (a.gate && !gate_full
+                                       ? gate_value(row_load<BF, false>(a.gate, row * a.gate_row), a.gate_act) : 1.f);
+    if (a.post.kind >= 0) norm_row<WARPS, NV, VW, BF>(f, a.post, a.d, first, scratch, phase);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int at = (first + i * stride) * VW;
+        if (at < a.d) {
+            if (gate_full) {
+                float g[VW];
+                raw_floats<VW, BF, false>(gt[i], g);
+                if (a.gate_act == MOE_GATE_SIGMOID) {
+#pragma unroll
+                    for (int j = 0; j < VW; ++j) g[j] = gate_value(g[j], MOE_GATE_SIGMOID);
+                }
+#pragma unroll
+                for (int j = 0; j < VW; ++j) f[i][j] *= g[j];
             }
-            if (a.resid_out) row_store8<BF, RF>(a.resid_out, (int64_t)row * a.d + at, f[i]);
+            if (a.resid) {
+                float v[VW];
+                raw_floats<VW, BF, RF>(r[i], v);
+#pragma unroll
+                for (int j = 0; j < VW; ++j) f[i][j] = v[j] + scale * f[i][j];
+            } else {
+#pragma unroll
+                for (int j = 0; j < VW; ++j) f[i][j] *= scale;
+            }
+            if (a.resid_out) raw_store<VW, BF, RF>(a.resid_out, row * a.d + at, f[i]);
         }
     }
     if (!a.out) return;
-    if (a.pre.kind >= 0) norm_row<WARPS, NV, BF>(f, a.pre, a.d, first, stride, scratch, phase);
+    if (a.pre.kind >= 0) norm_row<WARPS, NV, VW, BF>(f, a.pre, a.d, first, scratch, phase);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int at = (first + i * stride) * 8;
-        if (at < a.d) row_store8<BF, false>(a.out, (int64_t)row * a.d + at, f[i]);
+        const int at = (first + i * stride) * VW;
+        if (at < a.d) raw_store<VW, BF, false>(a.out, row * a.d + at, f[i]);
     }
 }
 
@@ -248,35 +329,61 @@ __global__ void __launch_bounds__(NORM_ANY_WARPS * 32) norm_any_kernel(const Nor
     for (int i = tid; i < a.d; i += TH) row_store<BF, false>(a.out, row * a.d + i, sm_row[i]);
 }
 
+template <int WARPS, int NV, int VW, bool BF, bool RF>
+static void norm_rows(const NormArgs& a, cudaStream_t st) {
+    constexpr int rows = WARPS == 1 ? 4 : 1;
+    norm_rows_kernel<WARPS, NV, VW, BF, RF><<<(a.T + rows - 1) / rows, WARPS == 1 ? 128 : WARPS * 32, 0, st>>>(a);
+}
+
 template <bool BF, bool RF>
-static cudaError_t launch_norm(const NormArgs& a, cudaStream_t st) {
-    auto al = [](const void* p, int64_t stride) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride % 8 == 0; };
-    const bool vec = a.d % 8 == 0 && a.d <= 16384 && al(a.y, a.y_stride) && al(a.resid, a.r_stride) &&
-                     (a.gate_col == 0 || al(a.gate, a.gate_row)) && al(a.post.w, 0) && al(a.post.b, 0) &&
-                     al(a.pre.w, 0) && al(a.pre.b, 0) && al(a.resid_out, 0) && al(a.out, 0);
-    if (!vec) {
+static cudaError_t launch_norm(const NormArgs& a, const DeviceInfo& di, cudaStream_t st) {
+    // the widest vector that d and every address allow
+    auto fits = [&](int vw) {
+        auto al = [&](const void* p, int64_t stride, int es) {
+            return reinterpret_cast<uintptr_t>(p) % std::min(vw * es, 16) == 0 && stride % vw == 0;
+        };
+        const int rs = RF ? 4 : 2;
+        return a.d % vw == 0 && al(a.y, a.y_stride, 2) && al(a.resid, a.r_stride, rs) &&
+               (a.gate_col == 0 || al(a.gate, a.gate_row, 2)) && al(a.post.w, 0, 2) && al(a.post.b, 0, 2) &&
+               al(a.pre.w, 0, 2) && al(a.pre.b, 0, 2) && al(a.resid_out, 0, rs) && al(a.out, 0, 2);
+    };
+    // a warp per row once the rows fill the GPU's warps; several for fewer rows, for latency
+    const bool many = a.T >= di.sm_count * 8;
+    if (a.d > 16384) {
         static SmemOnce once;
         const cudaError_t e = once.set(reinterpret_cast<const void*>(norm_any_kernel<BF, RF>), MOE_NORM_MAX_DIM * 4);
         if (e != cudaSuccess) return e;
         norm_any_kernel<BF, RF><<<a.T, NORM_ANY_WARPS * 32, (size_t)a.d * 4, st>>>(a);
-    } else if (a.d <= 256) {
-        norm_rows_kernel<1, 1, BF, RF><<<(a.T + 3) / 4, 128, 0, st>>>(a);
-    } else if (a.d <= 2048) {
-        norm_rows_kernel<8, 1, BF, RF><<<a.T, 256, 0, st>>>(a);
-    } else if (a.d <= 4096) {
-        norm_rows_kernel<16, 1, BF, RF><<<a.T, 512, 0, st>>>(a);
-    } else if (a.d <= 8192) {
-        norm_rows_kernel<16, 2, BF, RF><<<a.T, 512, 0, st>>>(a);
+    } else if (fits(8)) {
+        if (a.d <= 256) norm_rows<1, 1, 8, BF, RF>(a, st);
+        else if (a.d <= 512 && many) norm_rows<1, 2, 8, BF, RF>(a, st);
+        else if (a.d <= 1024 && many) norm_rows<1, 4, 8, BF, RF>(a, st);
+        else if (a.d <= 1024) norm_rows<4, 1, 8, BF, RF>(a, st);
+        else if (a.d <= 2048) norm_rows<8, 1, 8, BF, RF>(a, st);
+        else if (a.d <= 4096) norm_rows<16, 1, 8, BF, RF>(a, st);
+        else if (a.d <= 8192) norm_rows<16, 2, 8, BF, RF>(a, st);
+        else norm_rows<16, 4, 8, BF, RF>(a, st);
+    } else if (fits(4)) {
+        if (a.d <= 512) norm_rows<1, 4, 4, BF, RF>(a, st);
+        else if (a.d <= 2048) norm_rows<4, 4, 4, BF, RF>(a, st);
+        else if (a.d <= 8192) norm_rows<16, 4, 4, BF, RF>(a, st);
+        else norm_rows<16, 8, 4, BF, RF>(a, st);
     } else {
-        norm_rows_kernel<16, 4, BF, RF><<<a.T, 512, 0, st>>>(a);
+        if (a.d <= 512) norm_rows<1, 16, 1, BF, RF>(a, st);
+        else if (a.d <= 2048) norm_rows<4, 16, 1, BF, RF>(a, st);
+        else if (a.d <= 8192) norm_rows<16, 16, 1, BF, RF>(a, st);
+        else norm_rows<16, 32, 1, BF, RF>(a, st);
     }
     return cudaGetLastError();
 }
 
 cudaError_t launch_norm_residual(const NormArgs& a, int dtype, int resid_dtype, cudaStream_t st) {
+    DeviceInfo di;
+    const cudaError_t e = device_info(&di);
+    if (e != cudaSuccess) return e;
     const bool rf = resid_dtype == MOE_F32;
-    if (dtype == MOE_BF16) return rf ? launch_norm<true, true>(a, st) : launch_norm<true, false>(a, st);
-    return rf ? launch_norm<false, true>(a, st) : launch_norm<false, false>(a, st);
+    if (dtype == MOE_BF16) return rf ? launch_norm<true, true>(a, di, st) : launch_norm<true, false>(a, di, st);
+    return rf ? launch_norm<false, true>(a, di, st) : launch_norm<false, false>(a, di, st);
 }
 
 }  // namespace moedec
