@@ -450,7 +450,7 @@ int moe_paged_attention(const void* q, int64_t q_stride, int64_t q_head_stride, 
  * Arguments
  *   q [T][Hq][D], k and v [T][Hkv][D], q_out [T][Hq][D]: dtype MOE_BF16 or
  *   MOE_F16, strides in elements, D contiguous; q_out may be q itself.  The
- *   cache's dtype is dtype or MOE_E4M3 (value / scale, nearest even,
+ *   cache's dtype is dtype or MOE_E4M3 (value * (1 / scale), nearest even,
  *   saturated at 448).  positions int32 [T], slots int64 [T], freqs float64
  *   [rot/2] in radians per position (see moe_rope_freqs).
  *   1 <= D <= MOE_ROPE_MAX_DIM, rot even, 0 <= rot <= D.

@@ -157,6 +157,7 @@ struct RopeArgs {
     const double* freqs;
     int T, Hq, Hkv, D, rot, interleaved, num_pages, page;
     float mscale, k_scale, v_scale;
+    float k_inv, v_inv;  // filled by the launch
     int* err;
 };
 cudaError_t launch_rope_append(RopeArgs a, int dtype, int cache_dtype, cudaStream_t st);
