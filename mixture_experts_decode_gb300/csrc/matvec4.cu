@@ -59,7 +59,7 @@ __device__ __forceinline__ uint32_t code_pair(uint32_t w) {
 
 // GB: blocks of 32 k per group (1, 2, 4).
 template <int MT, int NT, int GB, bool BF>
-__global__ void __launch_bounds__(MV_WARPS * 32) matvec4_kernel(const Matvec4Args a, int tiles, int steps) {
+__global__ void __launch_bounds__(MV_WARPS * 32, NT <= 2 ? 2 : 1) matvec4_kernel(const __grid_constant__ Matvec4Args a, int tiles, int steps) {
     constexpr int NST = MT == 1 ? 4 : 3;
     constexpr int STAGE = MT * 16 * MV_ROW;
     constexpr int NGS = 8 / GB;              // groups of a step
@@ -75,31 +75,39 @@ __global__ void __launch_bounds__(MV_WARPS * 32) matvec4_kernel(const Matvec4Arg
     const int kg = a.K / a.group;
     const int per_warp = (steps + MV_WARPS - 1) / MV_WARPS;  // steps of a warp and tile
     const int my_tiles = ((int)blockIdx.x < tiles) ? (tiles - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
+    // Rows beyond T read the first row of x again: their columns of the
+    // products are not stored, and no column depends on another.
     const uint16_t* xrow[NT];
-    uint32_t x_on[NT];  // all ones for a real row of x
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         const int tk = nt * 8 + g;
-        x_on[nt] = tk < toks ? 0xffffffffu : 0u;
-        xrow[nt] = static_cast<const uint16_t*>(a.x) + (int64_t)(tok0 + (x_on[nt] ? tk : 0)) * a.x_stride;
+        xrow[nt] = static_cast<const uint16_t*>(a.x) + (int64_t)(tok0 + (tk < toks ? tk : 0)) * a.x_stride;
     }
 
     // Nothing below branches per lane, because the matrix instructions need
-    // the whole warp together: rows and columns beyond the end are read at the
-    // last valid place instead (x is zero there, and their rows not stored).
+    // the whole warp together: weight rows beyond N read the last row again
+    // (not stored), columns beyond K the last ones (their scale is zero).
     // The pipeline runs over (tile, step) pairs, issue side and use side.
+    const int64_t row_bytes = a.K / 2;
     const int last_kb = a.K / 2 - 16;
     int is_tile = 0, is_step = 0, is_stage = 0;
     auto issue = [&]() {
         if (is_tile < my_tiles) {
-            const int64_t row0 = (int64_t)(blockIdx.x + (int64_t)is_tile * gridDim.x) * (MT * 16) + (lane >> 3);
+            const int64_t row0 = (int64_t)(blockIdx.x + (int64_t)is_tile * gridDim.x) * (MT * 16);
+            const int r = lane >> 3;
             const int kb = min((is_step * MV_WARPS + warp) * MV_ROW + (lane & 7) * 16, last_kb);
-            uint8_t* s = ring + is_stage * STAGE + (lane >> 3) * MV_ROW;
+            uint8_t* s = ring + is_stage * STAGE + r * MV_ROW;
+            const int sw0 = ((lane & 7) ^ r) << 4, sw1 = sw0 ^ 64;  // row & 7 is r or r + 4
+            if (row0 + MT * 16 <= a.N) {
+                const uint8_t* p = a.codes + (row0 + r) * row_bytes + kb;
 #pragma unroll
-            for (int i = 0; i < MT * 4; ++i) {
-                const int64_t row = min(row0 + i * 4, (int64_t)a.N - 1);
-                const int sw = (lane & 7) ^ ((i * 4 + (lane >> 3)) & 7);
-                cp_async_16_zfill(s + i * 4 * MV_ROW + (sw << 4), a.codes + row * (a.K / 2) + kb, 16);
+                for (int i = 0; i < MT * 4; ++i, p += 4 * row_bytes)
+                    cp_async_16_zfill(s + i * 4 * MV_ROW + (i & 1 ? sw1 : sw0), p, 16);
+            } else {
+#pragma unroll
+                for (int i = 0; i < MT * 4; ++i)
+                    cp_async_16_zfill(s + i * 4 * MV_ROW + (i & 1 ? sw1 : sw0),
+                                      a.codes + min(row0 + r + i * 4, (int64_t)a.N - 1) * row_bytes + kb, 16);
             }
             if (++is_step == per_warp) {
                 is_step = 0;
@@ -109,29 +117,32 @@ __global__ void __launch_bounds__(MV_WARPS * 32) matvec4_kernel(const Matvec4Arg
         }
         cp_async_commit();
     };
-    // scale | zero << 16 of the lane's groups, one step ahead
+    // The lane's groups' scale | FP16 of 16 + zero << 16, one step ahead.
     uint32_t next_sz[MT][2][SLOTS];
     int sz_tile = 0, sz_step = 0;
     auto fetch_sz = [&]() {
         const int64_t row0 = (int64_t)(blockIdx.x + (int64_t)sz_tile * gridDim.x) * (MT * 16) + g;
         const int gi0 = (sz_step * MV_WARPS + warp) * NGS + (SLOTS == 1 && NGS < 4 ? t & (NGS - 1) : t);
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int s = 0; s < SLOTS; ++s) {
+            const int gi = min(gi0 + s * 4, kg - 1);
+            const uint32_t keep = gi0 + s * 4 < kg ? 0xffffffffu : 0xffff0000u;
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                for (int s = 0; s < SLOTS; ++s) {
-                    const int64_t row = min(row0 + mt * 16 + h * 8, (int64_t)a.N - 1);
-                    const int64_t at = row * kg + min(gi0 + s * 4, kg - 1);
-                    const uint32_t z = a.zeros ? a.zeros[at] : 8u;
-                    next_sz[mt][h][s] = static_cast<const uint16_t*>(a.scales)[at] | z << 16;
+                for (int h = 0; h < 2; ++h) {
+                    const int64_t at = min(row0 + mt * 16 + h * 8, (int64_t)a.N - 1) * kg + gi;
+                    const uint32_t z = a.zeros ? __ldg(a.zeros + at) : 8u;
+                    const uint32_t zz = __half_as_ushort(__uint2half_rn(16u + z));
+                    next_sz[mt][h][s] = (__ldg(static_cast<const uint16_t*>(a.scales) + at) | zz << 16) & keep;
                 }
+        }
         if (++sz_step == per_warp) {
             sz_step = 0;
             ++sz_tile;
         }
     };
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < NST - 1; ++i) issue();
     fetch_sz();
 
@@ -156,6 +167,13 @@ __global__ void __launch_bounds__(MV_WARPS * 32) matvec4_kernel(const Matvec4Arg
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int s = 0; s < SLOTS; ++s) sz[mt][h][s] = next_sz[mt][h][s];
+            // x of the step first (L1 or L2), under the wait for the codes
+            constexpr bool AHEAD = NT == 1;
+            uint4 xv[AHEAD ? 8 : 1];
+            if (AHEAD)
+#pragma unroll
+                for (int blk = 0; blk < 8; ++blk)
+                    xv[blk % (AHEAD ? 8 : 1)] = ld_cached_128(xrow[0] + min(step * MV_STEP + blk * 32 + 8 * t, a.K - 8));
             cp_async_wait<NST - 2>();
             __syncwarp();
             issue();
@@ -176,14 +194,11 @@ __global__ void __launch_bounds__(MV_WARPS * 32) matvec4_kernel(const Matvec4Arg
 #pragma unroll
                 for (int bb = 0; bb < GB; ++bb) {
                     const int blk = grp * GB + bb;
-                    const int k0 = step * MV_STEP + blk * 32 + 8 * t;
-                    const int kx = min(k0, a.K - 8);
                     uint32_t xb[NT][4];
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        uint4 v = ld_cached_128(xrow[nt] + kx);
-                        const uint32_t on = k0 < a.K ? x_on[nt] : 0u;
-                        v.x &= on, v.y &= on, v.z &= on, v.w &= on;
+                        const uint4 v = AHEAD ? xv[blk % (AHEAD ? 8 : 1)]
+                                              : ld_cached_128(xrow[nt] + min(step * MV_STEP + blk * 32 + 8 * t, a.K - 8));
                         xb[nt][0] = __byte_perm(v.x, v.z, 0x5410);  // x0, x4
                         xb[nt][1] = __byte_perm(v.x, v.z, 0x7632);  // x1, x5
                         xb[nt][2] = __byte_perm(v.y, v.w, 0x5410);  // x2, x6
@@ -226,7 +241,7 @@ __global__ void __launch_bounds__(MV_WARPS * 32) matvec4_kernel(const Matvec4Arg
                             memcpy(&hh, &q, 2);
                             sc = __half2float(hh);
                         }
-                        const float zz = 16.f + (float)(v >> 16);
+                        const float zz = __half2float(__ushort_as_half((uint16_t)(v >> 16)));
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -293,7 +308,7 @@ static cudaError_t launch_mv_group(const Matvec4Args& a, const DeviceInfo& di, c
 
 template <bool BF>
 static cudaError_t launch_mv_rows(const Matvec4Args& a, const DeviceInfo& di, cudaStream_t st) {
-    const bool two = (a.N + 31) / 32 >= 2 * di.sm_count;
+    const bool two = (a.N + 31) / 32 >= di.sm_count;
     if (a.T <= 8) return two ? launch_mv_group<2, 1, BF>(a, di, st) : launch_mv_group<1, 1, BF>(a, di, st);
     if (a.T <= 16) return two ? launch_mv_group<2, 2, BF>(a, di, st) : launch_mv_group<1, 2, BF>(a, di, st);
     return two ? launch_mv_group<2, 4, BF>(a, di, st) : launch_mv_group<1, 4, BF>(a, di, st);
