@@ -46,6 +46,9 @@ constexpr int ATT_WARPS = 4;
 constexpr int ATT_THREADS = ATT_WARPS * 32;
 constexpr int ATT_STEP = 16;                     // keys per warp step
 constexpr int ATT_UNIT = ATT_STEP * ATT_WARPS;   // keys per unit of work
+// What beginning a piece costs, in units: filling the ring and combining the
+// warps take as long as about two units of keys.
+constexpr int ATT_BEGIN = 2;
 constexpr int KV_BF16 = 0, KV_F16 = 1, KV_E4M3 = 2;
 
 // Stages per warp: what two resident blocks per SM can hold (about 96 KB
@@ -268,13 +271,13 @@ __global__ void __launch_bounds__(ATT_THREADS) paged_attention_kernel(const __gr
     float* sm_l = sm_m + ATT_WARPS * NH;
     float2* head_ml = reinterpret_cast<float2*>(sm_l + ATT_WARPS * NH);      // [NH]
     int64_t* sm_warp = reinterpret_cast<int64_t*>(head_ml + NH);            // [warps] + carry
-    int64_t* prefix = sm_warp + 8;                                         // [B] units up to and with b
+    int64_t* prefix = sm_warp + 8;                                          // [B] cost up to and with b
 
     const int nk = a.D / 16;
     const int chunks16 = a.D * ES / 16;
     const int64_t cap = (int64_t)a.max_pages * a.page;
 
-    // units of each sequence, scanned over the batch
+    // cost of an item of each sequence, scanned over the batch
     int64_t carry = 0;
     for (int b0 = 0; b0 < a.B; b0 += ATT_THREADS) {
         const int b = b0 + tid;
@@ -287,6 +290,7 @@ __global__ void __launch_bounds__(ATT_THREADS) paged_attention_kernel(const __gr
             const int nn = (int)(n < 0 ? 0 : (n > cap ? cap : n));
             const Visible v = visible_keys(nn, a.window, a.sinks);
             u = ((int64_t)v.vis + ATT_UNIT - 1) / ATT_UNIT;
+            if (u) u += ATT_BEGIN;
         }
         int64_t s = u;
 #pragma unroll
@@ -314,6 +318,9 @@ __global__ void __launch_bounds__(ATT_THREADS) paged_attention_kernel(const __gr
     const int64_t total = carry * items;
     const int64_t blocks = total < gridDim.x ? total : gridDim.x;
     if ((int64_t)blockIdx.x >= blocks) return;
+    // Block c takes the costs [total c / blocks, total (c + 1) / blocks), but
+    // an item is not cut within the cost of beginning it: a border there moves
+    // to the item's start.
     int64_t u = total * blockIdx.x / blocks;
     const int64_t u_end = total * (blockIdx.x + 1) / blocks;
     int b = 0;
@@ -332,11 +339,14 @@ __global__ void __launch_bounds__(ATT_THREADS) paged_attention_kernel(const __gr
     while (u < u_end) {
         while (prefix[b] * items <= u) ++b;
         const int64_t before = b ? prefix[b - 1] : 0;
-        const int64_t units = prefix[b] - before;
+        const int64_t cost = prefix[b] - before;
         const int64_t rel = u - before * items;
-        const int item = (int)(rel / units);
-        const int64_t t0 = rel - (int64_t)item * units;
-        const int64_t t1 = min(units, t0 + (u_end - u));
+        const int item = (int)(rel / cost);
+        const int64_t first_u = before * items + (int64_t)item * cost;
+        if (u_end - first_u <= ATT_BEGIN) break;  // it begins in the next block
+        const int64_t units = cost - ATT_BEGIN;
+        const int64_t t0 = max((int64_t)0, u - first_u - ATT_BEGIN);
+        const int64_t t1 = min(units, u_end - first_u - ATT_BEGIN);
         const int kvh = item / a.chunks, chunk = item - kvh * a.chunks;
         const int head0 = kvh * a.G + chunk * a.hpi;
         const int heads = min(a.hpi, a.G - chunk * a.hpi);
@@ -676,15 +686,15 @@ __global__ void __launch_bounds__(ATT_THREADS) paged_attention_kernel(const __gr
         }
         if (!whole) {
             if (tid < heads) reinterpret_cast<float2*>(a.ws_ml)[(int64_t)slot * a.hpi + tid] = head_ml[tid];
-            // the pieces of this item belong to blocks c1 .. c2
-            const int64_t first_u = before * items + (int64_t)item * units, last_u = first_u + units - 1;
-            const int c1 = (int)(((first_u + 1) * blocks - 1) / total);
-            const int c2 = (int)(((last_u + 1) * blocks - 1) / total);
+            // the pieces of this item belong to blocks c1 .. c2, the last ones
+            // whose costs start before its first key and before its end
+            const int c1 = (int)(((first_u + ATT_BEGIN + 1) * blocks - 1) / total);
+            const int c2 = (int)(((first_u + cost) * blocks - 1) / total);
             join_pieces<QBF>(a, c1, c2, b, head0, heads, P_SHIFT, head_ml, reinterpret_cast<float*>(smem),
                              reinterpret_cast<int*>(sm_warp));
         }
         __syncthreads();  // the ring and the flags are free again
-        u += t1 - t0;
+        u = first_u + ATT_BEGIN + t1;
     }
 }
 
