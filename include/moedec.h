@@ -428,7 +428,7 @@ int moe_mx_requant(const void* in, void* out, int64_t rows, int K, moe_stream_t 
  * Limits: B <= MOE_ATTN_MAX_BATCH, D a multiple of 16 up to MOE_ATTN_MAX_DIM,
  * Hq a multiple of Hkv.
  */
-#define MOE_ATTN_COUNTER_BYTES 2048
+#define MOE_ATTN_COUNTER_BYTES 4096
 int moe_paged_attention_workspace_bytes(int Hq, int Hkv, int D, size_t* bytes);
 int moe_paged_attention(const void* q, int64_t q_stride, int64_t q_head_stride, int B, int Hq, int Hkv, int D,
                         int dtype, moe_cache_t k, moe_cache_t v, int cache_dtype, int num_pages, int page_size,

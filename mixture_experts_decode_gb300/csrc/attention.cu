@@ -23,7 +23,7 @@
 // takes 16-bit operands; p is given to it as hi + lo (two 16-bit values, an
 // error near 2^-17 of p in BF16 and 2^-22 in FP16), because one 16-bit
 // rounding of p would cost as much as rounding the output.  FP16 operands
-// hold 2^14 p (at most 2^14), so that a long tail of keys far below the
+// hold 2^14 p (at most 2^15), so that a long tail of keys far below the
 // maximum is kept down to p = 2^-38; l carries the same factor.  E4M3 codes widen to FP16 exactly; a
 // BF16 q then goes to FP16 after a power-of-two scaling of its head's row
 // (the largest element in [2^9, 2^10]), exact for elements within 2^-23 of
@@ -51,11 +51,15 @@ constexpr int ATT_UNIT = ATT_STEP * ATT_WARPS;   // keys per unit of work
 constexpr int ATT_BEGIN = 2;
 constexpr int KV_BF16 = 0, KV_F16 = 1, KV_E4M3 = 2;
 
-// Stages per warp: what two resident blocks per SM can hold (about 96 KB
-// each), at least three.
-constexpr int att_stages(int dp, int es) {
-    const int s = 98304 / (ATT_WARPS * 2 * ATT_STEP * dp * es);
-    return s < 3 ? 3 : (s > 6 ? 6 : s);
+// Blocks per SM that the registers are cut for, and stages per warp in their
+// share of the 228 KB: three blocks of two stages of D = 128 BF16 beat two of
+// three (the warps' fixed latencies, not the loads, are what is waited for).
+constexpr int att_blocks(int dp, int nt) { return dp == 64 && nt == 1 ? 4 : dp == 256 || nt == 2 ? 2 : 3; }
+constexpr int att_stages(int dp, int es, int nt) {
+    const int s = (att_blocks(dp, nt) == 4 ? 49152 : att_blocks(dp, nt) == 3 ? 66000 : 98304) /
+                  (ATT_WARPS * 2 * ATT_STEP * dp * es);
+    const int least = es == 1 ? 3 : 2;  // (the sums of two N tiles take three E4M3 stages)
+    return s < least ? least : (s > 6 ? 6 : s);
 }
 
 __device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t addr) {
@@ -218,7 +222,7 @@ __device__ __forceinline__ bool arrive_last(int* counter, int n, int* err, int* 
 // The pieces of an item cut over blocks c1 .. c2 (this block's is written):
 // the last block of each eight joins theirs into the first one's place, the
 // last of those joins the groups (one level where eight blocks suffice), so
-// no block reads more than 41 pieces.  Counters: an item's first group by c1
+// no block reads more than 81 pieces.  Counters: an item's first group by c1
 // (no other item begins in that block and goes on), its later groups and the
 // item itself by block / 8 (an item of more than eight blocks is the only one
 // with a later group, or an end, in such a place).
@@ -250,16 +254,18 @@ __device__ __noinline__ void join_pieces(const AttnArgs& a, int c1, int c2, int 
 }
 
 template <int DP, int NT, int KV, bool QBF>
-__global__ void __launch_bounds__(ATT_THREADS) paged_attention_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(ATT_THREADS, att_blocks(DP, NT)) paged_attention_kernel(const __grid_constant__ AttnArgs a) {
     constexpr int ES = KV == KV_E4M3 ? 1 : 2;
     constexpr bool BF = KV == KV_BF16;  // operand type of the products
     constexpr int ROW = DP * ES;        // bytes of a key's row in shared memory
     constexpr int CHP = ROW / 16;
-    constexpr int NST = att_stages(DP, ES);
+    constexpr int NST = att_stages(DP, ES, NT);
     constexpr int HALF = ATT_STEP * ROW;  // bytes of K (or V) in a stage
     constexpr int NK = DP / 16;
     constexpr int NH = NT * 8;
     constexpr float P_SHIFT = BF ? 0.f : 14.f;
+    constexpr float SLACK = BF ? 8.f : 1.f;  // FP16 holds 2^15 p
+    constexpr int SO = DP + 4;               // floats of a head's row of o in shared memory
 
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 31, warp = warp_index();
@@ -363,43 +369,44 @@ __global__ void __launch_bounds__(ATT_THREADS) paged_attention_kernel(const __gr
 
         // Nothing from here to the sums' end branches per lane, because the
         // matrix instructions need the whole warp together.
-        // Lanes 0..15 (and again 16..31) find the page of one key each, one
-        // step ahead of its use; beyond the last key they look the last one up
-        // again and drop it.  page < 0: nothing to read.
-        int page = -1, off = 0;
+        // Lanes 0..15 find the row of one key each in the K cache, lanes 16..31
+        // the same keys' in the V cache, one step ahead of its use; beyond the
+        // last key they look the last one up again and drop it.
+        bool have = false;
+        int64_t row_at = 0;  // bytes from the head's first row
         auto find = [&](int i) {
             if (i >= steps) return;
-            const int64_t k64 = ((int64_t)step0 + (int64_t)i * ATT_WARPS) * ATT_STEP + (lane & 15);
-            const int key = (int)min(k64, (int64_t)key_end - 1);
+            const uint32_t key0 = (uint32_t)(step0 + i * ATT_WARPS) * ATT_STEP + (lane & 15);
+            const int key = (int)min(key0, (uint32_t)key_end - 1u);
             const int tok = key < vis.head ? key : key + vis.skip;
-            const int pi = tok / a.page;
-            off = tok - pi * a.page;
+            const int pi = (int)(((uint64_t)(uint32_t)tok * a.page_mul) >> a.page_shift);
+            const int off = tok - pi * a.page;
             const int pg = table[pi];
             const bool known = pg >= 0 && pg < a.num_pages;
             if (__any_sync(FULL_MASK, !known)) atomicOr(a.err, known ? 0 : MOE_DEVERR_PAGE);
-            page = known && k64 < key_end ? pg : -1;
+            have = known && key0 < (uint32_t)key_end;
+            row_at = have ? (pg * (lane < 16 ? a.k_sp : a.v_sp) + off * (lane < 16 ? a.k_st : a.v_st)) * ES : 0;
         };
-        auto issue = [&](int i) {
-            const int st = i % NST;
+        constexpr int ROWS = 32 / CHP;  // rows that the warp copies at once
+        const int col = lane % CHP, row0 = lane / CHP;
+        const uint8_t* kcol = kbase + (col < chunks16 ? col * 16 : 0);
+        const uint8_t* vcol = vbase + (col < chunks16 ? col * 16 : 0);
+        auto issue = [&](int i, int st) {
             if (i < steps) {
-                const uint32_t mask = __ballot_sync(FULL_MASK, page >= 0) & 0xffffu;
+                const uint32_t mask = __ballot_sync(FULL_MASK, have) & 0xffffu;
                 live[st] = mask;
+                const uint32_t copied = col < chunks16 ? mask : 0u;  // 0 bytes write zeros
                 uint8_t* sk = ring + st * 2 * HALF;
 #pragma unroll
-                for (int it = 0; it < ATT_STEP * CHP / 32; ++it) {
-                    const int c = it * 32 + lane;
-                    const int row = c / CHP, col = c % CHP;
-                    const int pg = __shfl_sync(FULL_MASK, page, row);
-                    const int of = __shfl_sync(FULL_MASK, off, row);
-                    // 0 bytes write zeros: a key that is not there, or columns beyond D
-                    const bool on = pg >= 0 && col < chunks16;
-                    const int bytes = on ? 16 : 0;
-                    const int64_t p = on ? pg : 0, o = on ? of : 0, at = on ? col * 16 : 0;
+                for (int it = 0; it < ATT_STEP / ROWS; ++it) {
+                    const int row = it * ROWS + row0;
+                    const int64_t ka = __shfl_sync(FULL_MASK, row_at, row), va = __shfl_sync(FULL_MASK, row_at, row + 16);
+                    const int bytes = (copied >> row & 1u) << 4;
                     const int ck = KV == KV_E4M3 ? (CHP >= 8 ? col ^ ((row & 1) << 2) : col) : col ^ (row & 7);
                     const int cv = KV == KV_E4M3 ? (CHP >= 8 ? col ^ (((row >> 1) & 3) << 1) : col ^ (((row >> 1) & 1) << 1))
                                                  : col ^ (row & 7);
-                    cp_async_16_zfill(sk + row * ROW + ck * 16, kbase + (p * a.k_sp + o * a.k_st) * ES + at, bytes);
-                    cp_async_16_zfill(sk + HALF + row * ROW + cv * 16, vbase + (p * a.v_sp + o * a.v_st) * ES + at, bytes);
+                    cp_async_16_zfill(sk + row * ROW + ck * 16, kcol + ka, bytes);
+                    cp_async_16_zfill(sk + HALF + row * ROW + cv * 16, vcol + va, bytes);
                 }
             }
             cp_async_commit();
@@ -407,7 +414,7 @@ __global__ void __launch_bounds__(ATT_THREADS) paged_attention_kernel(const __gr
         find(0);
 #pragma unroll 1
         for (int i = 0; i < NST - 1; ++i) {
-            issue(i);
+            issue(i, i);
             find(i + 1);
         }
 
@@ -476,14 +483,17 @@ __global__ void __launch_bounds__(ATT_THREADS) paged_attention_kernel(const __gr
                 for (int i = 0; i < 4; ++i) o[kk][nt][i] = 0.f;
         }
 
+        int use = 0;  // stage of step i
+#pragma unroll 1
         for (int i = 0; i < steps; ++i) {
             cp_async_wait<NST - 2>();
             __syncwarp();
-            issue(i + NST - 1);  // into the stage that step i - 1 has left
+            issue(i + NST - 1, use == 0 ? NST - 1 : use - 1);  // into the stage that step i - 1 has left
             find(i + NST);
-            const uint8_t* sk = ring + (i % NST) * 2 * HALF;
+            const uint8_t* sk = ring + use * 2 * HALF;
             const uint8_t* sv = sk + HALF;
-            const uint32_t mask = live[i % NST];
+            const uint32_t mask = live[use];
+            if (++use == NST) use = 0;
 
             float s[NT][4];
             {
@@ -531,25 +541,45 @@ __global__ void __launch_bounds__(ATT_THREADS) paged_attention_kernel(const __gr
                     }
             }
 
-            // running maximum and sum, p as hi + lo operands
-            uint32_t ph[NT][2], pl[NT][2];
-            float scale_o[NT][2];
+            // The reference m of the exponents only has to stay near the running
+            // maximum: it moves, and o and l with it, when some score passes it
+            // by more than SLACK (p <= 2^SLACK), which is rare after the first
+            // steps and spares the other steps the reduction over the keys.
             bool grew = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) grew |= fmaxf(s[nt][c], s[nt][c + 2]) > m[nt][c] + SLACK;
+            if (__any_sync(FULL_MASK, grew)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float scale_o[2];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float mx = fmaxf(s[nt][c], s[nt][c + 2]);
+                        mx = fmaxf(mx, __shfl_xor_sync(FULL_MASK, mx, 4));
+                        mx = fmaxf(mx, __shfl_xor_sync(FULL_MASK, mx, 8));
+                        mx = fmaxf(mx, __shfl_xor_sync(FULL_MASK, mx, 16));
+                        const float mn = fmaxf(m[nt][c], mx);
+                        scale_o[c] = exp2_fast(m[nt][c] - finite_or_zero(mn));
+                        m[nt][c] = mn;
+                        l[nt][c] *= scale_o[c];
+                    }
+#pragma unroll
+                    for (int kk = 0; kk < NK; ++kk)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) o[kk][nt][j] *= scale_o[j & 1];
+                }
+            }
+            // p as hi + lo operands of the second product
+            uint32_t ph[NT][2], pl[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    float mx = fmaxf(s[nt][c], s[nt][c + 2]);
-                    mx = fmaxf(mx, __shfl_xor_sync(FULL_MASK, mx, 4));
-                    mx = fmaxf(mx, __shfl_xor_sync(FULL_MASK, mx, 8));
-                    mx = fmaxf(mx, __shfl_xor_sync(FULL_MASK, mx, 16));
-                    const float mn = fmaxf(m[nt][c], mx);
-                    grew |= mn > m[nt][c];
-                    const float mu = finite_or_zero(mn);
-                    scale_o[nt][c] = exp2_fast(m[nt][c] - mu);
-                    m[nt][c] = mn;
-                    s[nt][c] = exp2_fast(s[nt][c] - mu + P_SHIFT);
-                    s[nt][c + 2] = exp2_fast(s[nt][c + 2] - mu + P_SHIFT);
+                    const float mu = finite_or_zero(m[nt][c]) - P_SHIFT;
+                    s[nt][c] = exp2_fast(s[nt][c] - mu);
+                    s[nt][c + 2] = exp2_fast(s[nt][c + 2] - mu);
                 }
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
@@ -558,17 +588,6 @@ __global__ void __launch_bounds__(ATT_THREADS) paged_attention_kernel(const __gr
                     const uint32_t lo = pack2<BF>(s[nt][2 * r] - back.x, s[nt][2 * r + 1] - back.y);
                     ph[nt][r] = transpose_8x8(hi);
                     pl[nt][r] = transpose_8x8(lo);
-                }
-            }
-            if (__any_sync(FULL_MASK, grew)) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    l[nt][0] *= scale_o[nt][0];
-                    l[nt][1] *= scale_o[nt][1];
-#pragma unroll
-                    for (int kk = 0; kk < NK; ++kk)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) o[kk][nt][j] *= scale_o[nt][j & 1];
                 }
             }
 #pragma unroll
@@ -639,7 +658,7 @@ __global__ void __launch_bounds__(ATT_THREADS) paged_attention_kernel(const __gr
                 }
             }
         __syncwarp();
-        float* so = reinterpret_cast<float*>(ring);  // [NH][DP]
+        float* so = reinterpret_cast<float*>(ring);  // [NH][SO]
 #pragma unroll
         for (int kk = 0; kk < NK; ++kk)
 #pragma unroll
@@ -649,7 +668,7 @@ __global__ void __launch_bounds__(ATT_THREADS) paged_attention_kernel(const __gr
                     const int h = nt * 8 + 2 * t + (j & 1);
                     const int dim = KV == KV_E4M3 ? (kk >> 1) * 32 + 4 * g + (kk & 1) * 2 + (j >> 1)
                                                   : kk * 16 + g + (j >> 1) * 8;
-                    so[h * DP + dim] = o[kk][nt][j];
+                    so[h * SO + dim] = o[kk][nt][j];
                 }
         __syncthreads();
 
@@ -678,7 +697,7 @@ __global__ void __launch_bounds__(ATT_THREADS) paged_attention_kernel(const __gr
 #pragma unroll
             for (int w = 0; w < ATT_WARPS; ++w)
                 add_scaled(sum, sm_m[w * NH + h],
-                           *reinterpret_cast<const float4*>(smem + (size_t)w * NST * 2 * HALF + (h * DP + dim) * 4));
+                           *reinterpret_cast<const float4*>(smem + (size_t)w * NST * 2 * HALF + (h * SO + dim) * 4));
             if (whole)
                 store_head4<QBF>(a, b, head0 + h, dim, sum, head_ml[h], P_SHIFT);
             else
@@ -698,19 +717,25 @@ __global__ void __launch_bounds__(ATT_THREADS) paged_attention_kernel(const __gr
     }
 }
 
+// Blocks that a launch may have (pieces in the workspace): 160 SMs' worth.
+static int attn_max_blocks(int D, int hpi) {
+    const int nt = hpi > 8 ? 2 : 1;
+    return 160 * att_blocks(D <= 64 ? 64 : D <= 128 ? 128 : 256, nt);
+}
+
 template <int DP, int NT, int KV, bool QBF>
 static cudaError_t launch_attn(const AttnArgs& a, const DeviceInfo& di, cudaStream_t st) {
     constexpr int ES = KV == KV_E4M3 ? 1 : 2;
-    const size_t smem = (size_t)ATT_WARPS * att_stages(DP, ES) * 2 * ATT_STEP * DP * ES +
-                        ATT_WARPS * att_stages(DP, ES) * 4 + 2 * ATT_WARPS * NT * 8 * 4 + NT * 8 * 8 + 64 + (size_t)a.B * 8;
+    const size_t smem = (size_t)ATT_WARPS * att_stages(DP, ES, NT) * 2 * ATT_STEP * DP * ES +
+                        ATT_WARPS * att_stages(DP, ES, NT) * 4 + 2 * ATT_WARPS * NT * 8 * 4 + NT * 8 * 8 + 64 + (size_t)a.B * 8;
     auto kernel = paged_attention_kernel<DP, NT, KV, QBF>;
     static SmemOnce once;
     cudaError_t e = once.set(reinterpret_cast<const void*>(kernel), di.max_smem_optin);
     if (e != cudaSuccess) return e;
     if (smem > (size_t)di.max_smem_optin) return cudaErrorInvalidValue;
     int per_sm = (int)((size_t)di.smem_per_sm / (smem + 1024));
-    per_sm = per_sm < 1 ? 1 : (per_sm > 2 ? 2 : per_sm);
-    const int grid = min(di.sm_count * per_sm, ATTN_MAX_BLOCKS);
+    per_sm = per_sm < 1 ? 1 : min(per_sm, att_blocks(DP, NT));
+    const int grid = min(di.sm_count * per_sm, attn_max_blocks(a.D, a.hpi));
     kernel<<<grid, ATT_THREADS, smem, st>>>(a);
     return cudaGetLastError();
 }
@@ -732,7 +757,7 @@ int attn_heads_per_item(int G) {
 
 size_t attn_workspace_bytes(int Hq, int Hkv, int D) {
     const size_t hpi = attn_heads_per_item(Hq / Hkv);
-    return ATTN_COUNTER_BYTES + (size_t)2 * ATTN_MAX_BLOCKS * hpi * (D + 2) * 4;
+    return ATTN_COUNTER_BYTES + (size_t)2 * attn_max_blocks(D, (int)hpi) * hpi * (D + 2) * 4;
 }
 
 cudaError_t launch_paged_attention(AttnArgs a, int dtype, int cache_dtype, void* ws, cudaStream_t st) {
@@ -743,10 +768,14 @@ cudaError_t launch_paged_attention(AttnArgs a, int dtype, int cache_dtype, void*
     a.G = a.Hq / a.Hkv;
     a.hpi = attn_heads_per_item(a.G);
     a.chunks = (a.G + a.hpi - 1) / a.hpi;
+    int log2_page = 0;  // tok / page as a product: exact for tok < 2^31
+    while ((int64_t(1) << log2_page) < a.page) ++log2_page;
+    a.page_shift = 31 + log2_page;
+    a.page_mul = (uint32_t)((uint64_t(1) << a.page_shift) / a.page + 1);
     a.out_aligned = reinterpret_cast<uintptr_t>(a.out) % 8 == 0;
     a.counters = static_cast<int*>(ws);
     a.ws_ml = reinterpret_cast<float*>(static_cast<char*>(ws) + ATTN_COUNTER_BYTES);
-    a.ws_o = a.ws_ml + (size_t)2 * ATTN_MAX_BLOCKS * a.hpi * 2;
+    a.ws_o = a.ws_ml + (size_t)2 * attn_max_blocks(a.D, a.hpi) * a.hpi * 2;
     if (cache_dtype == MOE_E4M3)
         return dtype == MOE_BF16 ? launch_attn_kv<KV_E4M3, true>(a, di, st) : launch_attn_kv<KV_E4M3, false>(a, di, st);
     return dtype == MOE_BF16 ? launch_attn_kv<KV_BF16, true>(a, di, st) : launch_attn_kv<KV_F16, false>(a, di, st);

@@ -111,8 +111,8 @@ struct SmemOnce {
 
 // Paged attention: blocks of a launch at most (a join counter and two pieces
 // of workspace each), and the counters' bytes at the start of the workspace.
-constexpr int ATTN_MAX_BLOCKS = 320;
-constexpr size_t ATTN_COUNTER_BYTES = 2048;  // MOE_ATTN_COUNTER_BYTES
+constexpr int ATTN_MAX_BLOCKS = 640;
+constexpr size_t ATTN_COUNTER_BYTES = 4096;  // MOE_ATTN_COUNTER_BYTES
 static_assert((ATTN_MAX_BLOCKS + 2 * (ATTN_MAX_BLOCKS / 8 + 1)) * 4 <= ATTN_COUNTER_BYTES, "a counter per block, two per eight");
 struct AttnArgs {
     const void* q;
@@ -130,6 +130,8 @@ struct AttnArgs {
     float* lse;
     // filled by the launch
     bool out_aligned;    // to 8 bytes
+    uint32_t page_mul;
+    int page_shift;
     int G, hpi, chunks;  // query heads of a key-value head, of an item; items of a group
     int* counters;
     float* ws_ml;  // [2 * blocks][hpi][2] maximum and sum of a piece

@@ -49,8 +49,8 @@ def test_attention_of_no_sequences_launches_nothing(lib):
 def test_attention_workspace_bytes(lib):
     n = ctypes.c_size_t()
     assert lib.moe_paged_attention_workspace_bytes(32, 4, 128, ctypes.byref(n)) == 0
-    # a counter page, and two pieces of 8 heads x (128 + 2) floats per block
-    assert n.value == -(-(2048 + 2 * 320 * 8 * 130 * 4) // 256) * 256
+    # a counter page, and two pieces of 8 heads x (128 + 2) floats for each of 480 blocks
+    assert n.value == -(-(4096 + 2 * 480 * 8 * 130 * 4) // 256) * 256
     assert lib.moe_paged_attention_workspace_bytes(32, 4, 128, None) == ARG
     assert lib.moe_paged_attention_workspace_bytes(33, 4, 128, ctypes.byref(n)) == SHAPE
     assert lib.moe_paged_attention_workspace_bytes(32, 4, 512, ctypes.byref(n)) == LIMIT
