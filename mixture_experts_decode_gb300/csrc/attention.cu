@@ -49,6 +49,10 @@ constexpr int ATT_UNIT = ATT_STEP * ATT_WARPS;   // keys per unit of work
 // What beginning a piece costs, in units: filling the ring and combining the
 // warps take as long as about two units of keys.
 constexpr int ATT_BEGIN = 2;
+// A block takes at least this much, one unit and its beginning: cutting finer
+// only adds joins, and coarser lets a block do items one after the other
+// (777 keys of one sequence: 13.0 us at 1, 10.1 at 3, 12.0 at 5).
+constexpr int ATT_LEAST = 3;
 constexpr int KV_BF16 = 0, KV_F16 = 1, KV_E4M3 = 2;
 
 // Blocks per SM that the registers are cut for, and stages per warp in their
@@ -158,47 +162,45 @@ __device__ __forceinline__ void store_head4(const AttnArgs& a, int b, int h, int
 }
 
 // Joins n pieces of an item, piece i at slot(i), in their order: the sums go
-// to `put` four dims at a time with the joined (maximum, l).  Called by a
-// whole block; factors live in sm_f [n][heads] (n <= ATT_JOIN_MOST).
+// to `put` four dims at a time with the joined (maximum, l).  Every thread
+// joins its own dims with eight pieces' loads in flight at a time, the maxima
+// and sums among them, so a join of eight is one round trip to L2.
 constexpr int ATT_JOIN = 8;                                     // pieces of a group
 constexpr int ATT_JOIN_MOST = ATTN_MAX_BLOCKS / ATT_JOIN + 1;   // groups of an item
 template <class Slot, class Put>
-__device__ __forceinline__ void join_slots(const AttnArgs& a, int n, int heads, float2* head_ml, float* sm_f, Slot slot,
-                                           Put put) {
+__device__ __forceinline__ void join_slots(const AttnArgs& a, int n, int heads, Slot slot, Put put) {
     const float2* mls = reinterpret_cast<const float2*>(a.ws_ml);
-    for (int i = threadIdx.x; i < n * heads; i += ATT_THREADS) {
-        const int p = i / heads, h = i - p * heads;
-        const float2 v = __ldcg(mls + (int64_t)slot(p) * a.hpi + h);
-        sm_f[2 * i] = v.x;
-        sm_f[2 * i + 1] = v.y;
-    }
-    __syncthreads();
-    if ((int)threadIdx.x < heads) {
-        const int h = threadIdx.x;
-        float mm = -INFINITY, ll = 0.f;
-        for (int p = 0; p < n; ++p) mm = fmaxf(mm, sm_f[2 * (p * heads + h)]);
-        const float mu = finite_or_zero(mm);
-        for (int p = 0; p < n; ++p) {
-            const float f = exp2_fast(sm_f[2 * (p * heads + h)] - mu);
-            ll += f * sm_f[2 * (p * heads + h) + 1];
-            sm_f[2 * (p * heads + h)] = f;
-        }
-        head_ml[h] = make_float2(mm, ll);
-    }
-    __syncthreads();
     for (int e = threadIdx.x; e < heads * (a.D / 4); e += ATT_THREADS) {
         const int h = e / (a.D / 4), dim = (e - h * (a.D / 4)) * 4;
         float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        float m = -INFINITY, l = 0.f;
+#pragma unroll 1
         for (int p0 = 0; p0 < n; p0 += 8) {
             float4 v[8];
+            float2 ml[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)  // the last piece again beyond the end
-                v[i] = __ldcg(reinterpret_cast<const float4*>(a.ws_o + ((int64_t)slot(min(p0 + i, n - 1)) * a.hpi + h) * a.D + dim));
+            for (int i = 0; i < 8; ++i) {  // beyond the end the last piece again, with weight 0
+                const int64_t at = (int64_t)slot(min(p0 + i, n - 1)) * a.hpi + h;
+                ml[i] = __ldcg(mls + at);
+                v[i] = __ldcg(reinterpret_cast<const float4*>(a.ws_o + at * a.D + dim));
+            }
+            float mn = m;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) mn = fmaxf(mn, ml[i].x);
+            const float mu = finite_or_zero(mn);
+            const float old = exp2_fast(m - mu);
+            m = mn;
+            l *= old;
+            sum.x *= old, sum.y *= old, sum.z *= old, sum.w *= old;
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                if (p0 + i < n) add_scaled(sum, sm_f[2 * ((p0 + i) * heads + h)], v[i]);
+                if (p0 + i < n) {
+                    const float f = exp2_fast(ml[i].x - mu);
+                    l += f * ml[i].y;
+                    add_scaled(sum, f, v[i]);
+                }
         }
-        put(h, dim, sum);
+        put(h, dim, sum, make_float2(m, l));
     }
 }
 
@@ -228,7 +230,7 @@ __device__ __forceinline__ bool arrive_last(int* counter, int n, int* err, int* 
 // with a later group, or an end, in such a place).
 template <bool QBF>
 __device__ __noinline__ void join_pieces(const AttnArgs& a, int c1, int c2, int b, int head0, int heads, float shift,
-                                         float2* head_ml, float* sm_f, int* flag) {
+                                         float2* head_ml, int* flag) {
     const int pieces = c2 - c1 + 1;
     const int grp = ((int)blockIdx.x - c1) / ATT_JOIN;
     const int g0 = c1 + grp * ATT_JOIN;
@@ -236,21 +238,25 @@ __device__ __noinline__ void join_pieces(const AttnArgs& a, int c1, int c2, int 
     int* const later = a.counters + ATTN_MAX_BLOCKS;
     int* const ends = later + ATT_JOIN_MOST;
     auto slot = [&](int c) { return 2 * c + (c == c1 ? 1 : 0); };
-    auto finish = [&](int h, int dim, const float4& sum) { store_head4<QBF>(a, b, head0 + h, dim, sum, head_ml[h], shift); };
+    auto finish = [&](int h, int dim, const float4& sum, float2 ml) { store_head4<QBF>(a, b, head0 + h, dim, sum, ml, shift); };
     if (!arrive_last(grp == 0 ? a.counters + c1 : later + g0 / ATT_JOIN, in_group, a.err, flag)) return;
     if (pieces <= ATT_JOIN) {
-        join_slots(a, pieces, heads, head_ml, sm_f, [&](int p) { return slot(c1 + p); }, finish);
+        join_slots(a, pieces, heads, [&](int p) { return slot(c1 + p); }, finish);
         return;
     }
+    // The group takes its first piece's place: each thread has read its own
+    // dims of it by then, and the maxima and sums, which all threads read, are
+    // put there after a barrier.
     const int64_t to = (int64_t)slot(g0) * a.hpi;
-    join_slots(a, in_group, heads, head_ml, sm_f, [&](int p) { return slot(g0 + p); }, [&](int h, int dim, const float4& sum) {
-        // (each thread has read its own place of every piece by now)
+    join_slots(a, in_group, heads, [&](int p) { return slot(g0 + p); }, [&](int h, int dim, const float4& sum, float2 ml) {
         *reinterpret_cast<float4*>(a.ws_o + (to + h) * a.D + dim) = sum;
+        if (dim == 0) head_ml[h] = ml;
     });
+    __syncthreads();
     if ((int)threadIdx.x < heads) reinterpret_cast<float2*>(a.ws_ml)[to + threadIdx.x] = head_ml[threadIdx.x];
     const int groups = (pieces + ATT_JOIN - 1) / ATT_JOIN;
     if (!arrive_last(ends + c1 / ATT_JOIN, groups, a.err, flag)) return;
-    join_slots(a, groups, heads, head_ml, sm_f, [&](int p) { return slot(c1 + p * ATT_JOIN); }, finish);
+    join_slots(a, groups, heads, [&](int p) { return slot(c1 + p * ATT_JOIN); }, finish);
 }
 
 template <int DP, int NT, int KV, bool QBF>
@@ -322,7 +328,7 @@ __global__ void __launch_bounds__(ATT_THREADS, att_blocks(DP, NT)) paged_attenti
         }
     const int items = a.Hkv * a.chunks;  // items of one sequence
     const int64_t total = carry * items;
-    const int64_t blocks = total < gridDim.x ? total : gridDim.x;
+    const int64_t blocks = min((int64_t)gridDim.x, (total + ATT_LEAST - 1) / ATT_LEAST);
     if ((int64_t)blockIdx.x >= blocks) return;
     // Block c takes the costs [total c / blocks, total (c + 1) / blocks), but
     // an item is not cut within the cost of beginning it: a border there moves
@@ -709,8 +715,7 @@ __global__ void __launch_bounds__(ATT_THREADS, att_blocks(DP, NT)) paged_attenti
             // whose costs start before its first key and before its end
             const int c1 = (int)(((first_u + ATT_BEGIN + 1) * blocks - 1) / total);
             const int c2 = (int)(((first_u + cost) * blocks - 1) / total);
-            join_pieces<QBF>(a, c1, c2, b, head0, heads, P_SHIFT, head_ml, reinterpret_cast<float*>(smem),
-                             reinterpret_cast<int*>(sm_warp));
+            join_pieces<QBF>(a, c1, c2, b, head0, heads, P_SHIFT, head_ml, reinterpret_cast<int*>(sm_warp));
         }
         __syncthreads();  // the ring and the flags are free again
         u = first_u + ATT_BEGIN + t1;
