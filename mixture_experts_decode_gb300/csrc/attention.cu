@@ -378,20 +378,17 @@ __global__ void __launch_bounds__(ATT_THREADS, att_blocks(DP, NT)) paged_attenti
         // Lanes 0..15 find the row of one key each in the K cache, lanes 16..31
         // the same keys' in the V cache, one step ahead of its use; beyond the
         // last key they look the last one up again and drop it.
-        bool have = false;
-        int64_t row_at = 0;  // bytes from the head's first row
+        int pg = 0, off = 0;
+        bool in_range = false;
         auto find = [&](int i) {
             if (i >= steps) return;
             const uint32_t key0 = (uint32_t)(step0 + i * ATT_WARPS) * ATT_STEP + (lane & 15);
             const int key = (int)min(key0, (uint32_t)key_end - 1u);
             const int tok = key < vis.head ? key : key + vis.skip;
             const int pi = (int)(((uint64_t)(uint32_t)tok * a.page_mul) >> a.page_shift);
-            const int off = tok - pi * a.page;
-            const int pg = table[pi];
-            const bool known = pg >= 0 && pg < a.num_pages;
-            if (__any_sync(FULL_MASK, !known)) atomicOr(a.err, known ? 0 : MOE_DEVERR_PAGE);
-            have = known && key0 < (uint32_t)key_end;
-            row_at = have ? (pg * (lane < 16 ? a.k_sp : a.v_sp) + off * (lane < 16 ? a.k_st : a.v_st)) * ES : 0;
+            off = tok - pi * a.page;
+            in_range = key0 < (uint32_t)key_end;
+            pg = table[pi];  // (used by the next issue)
         };
         constexpr int ROWS = 32 / CHP;  // rows that the warp copies at once
         const int col = lane % CHP, row0 = lane / CHP;
@@ -399,6 +396,11 @@ __global__ void __launch_bounds__(ATT_THREADS, att_blocks(DP, NT)) paged_attenti
         const uint8_t* vcol = vbase + (col < chunks16 ? col * 16 : 0);
         auto issue = [&](int i, int st) {
             if (i < steps) {
+                const bool known = pg >= 0 && pg < a.num_pages;
+                if (__any_sync(FULL_MASK, !known)) atomicOr(a.err, known ? 0 : MOE_DEVERR_PAGE);
+                const bool have = known && in_range;
+                const int64_t row_at =  // bytes from the head's first row
+                    have ? (pg * (lane < 16 ? a.k_sp : a.v_sp) + off * (lane < 16 ? a.k_st : a.v_st)) * ES : 0;
                 const uint32_t mask = __ballot_sync(FULL_MASK, have) & 0xffffu;
                 live[st] = mask;
                 const uint32_t copied = col < chunks16 ? mask : 0u;  // 0 bytes write zeros
