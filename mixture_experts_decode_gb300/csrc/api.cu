@@ -605,7 +605,7 @@ int moe_matvec4(const void* x, int64_t x_stride, int T, int K, int dtype, const 
     if (!x || !codes || !scales || !y) return MOE_ERR_ARG;
     if (!aligned(x, 16) || x_stride % 8 || !aligned(codes, 16) || !aligned(scales, 2) || !aligned(y, 2))
         return MOE_ERR_ALIGN;
-    const Matvec4Args a{x, x_stride, codes, scales, zeros, y, y_stride, T, N, K, group};
+    const Matvec4Args a{x, x_stride, codes, scales, zeros, y, y_stride, T, N, K, group, false};
     return cuda_status(launch_matvec4(a, dtype, (cudaStream_t)stream));
 }
 

@@ -195,7 +195,8 @@ struct Matvec4Args {
     void* y;
     int64_t y_stride;
     int T, N, K, group;
+    bool scales_aligned;  // filled by the launch
 };
-cudaError_t launch_matvec4(const Matvec4Args& a, int dtype, cudaStream_t st);
+cudaError_t launch_matvec4(Matvec4Args a, int dtype, cudaStream_t st);
 
 }  // namespace moedec

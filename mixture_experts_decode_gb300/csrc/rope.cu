@@ -10,14 +10,15 @@
 // to 2^-34 turns, where an FP32 product would be off by radians.  The top 32
 // bits, as a signed fraction of half a turn, go to sincospif.
 //
-// Bound: HBM, each element in and out once.  One block takes one token at a
-// time (blocks stride over the tokens): its rot/2 sines go to shared memory
+// Bound: HBM, each element in and out once (16384 tokens of 64 + 8 + 8 heads
+// of 128: 671 MB, 106 us, 6.3 TB/s).  One block takes one or a few tokens at a
+// time (blocks stride over the tokens): their rot/2 sines go to shared memory
 // once and serve every head.  A thread keeps one place within a head (a
-// 16-byte vector, or the two vectors of eight rotated pairs) for all the heads
-// it visits, so that its sines sit in registers and the addresses of a head
-// cost one multiplication; the first heads' loads are on their way before the
-// sines are ready.  All arithmetic is FP32; each output is rounded once (E4M3:
-// times the reciprocal of the cache's scale, nearest even, saturated at 448).
+// 16-byte vector, or the two vectors of eight rotated pairs) of the same heads
+// throughout, so that addresses only move on, and the heads' loads are on
+// their way before the sines are made.  All arithmetic is FP32; each output is
+// rounded once (E4M3: times the reciprocal of the cache's scale, nearest even,
+// saturated at 448).
 #include <algorithm>
 
 #include "common.cuh"
@@ -82,21 +83,20 @@ __device__ __forceinline__ void floats8(const uint4& v, float (&f)[8]) {
 
 // What a token needs before its heads: the sines of its pairs (by pair) and
 // its cache row, by the block's threads into shared memory.
+__device__ __forceinline__ float2 rope_sine(int position, uint64_t turns, float mscale) {
+    const uint64_t phase = (uint64_t)(int64_t)position * turns;
+    float s, c;
+    sincospif((float)(int32_t)(phase >> 32) * 4.656612873077393e-10f, &s, &c);  // 2^-31: half turns
+    return make_float2(c * mscale, s * mscale);
+}
 struct RopeToken {
     float2 cs[MOE_ROPE_MAX_DIM / 2];
     int64_t page, row;  // page -1: not written
 };
-__device__ __forceinline__ void rope_token(const RopeArgs& a, int tok, const uint64_t* F, RopeToken& s) {
+__device__ __forceinline__ void rope_token(const RopeArgs& a, int position, int64_t slot, const uint64_t* F, RopeToken& s) {
     const int half = a.rot / 2;
-    const uint64_t pos = (uint64_t)(int64_t)a.positions[tok];
-    for (int i = threadIdx.x; i < half; i += blockDim.x) {
-        const float x = (float)(int32_t)((pos * F[i]) >> 32) * 4.656612873077393e-10f;  // 2^-31: half turns
-        float sn, c;
-        sincospif(x, &sn, &c);
-        s.cs[i] = make_float2(c * a.mscale, sn * a.mscale);
-    }
+    for (int i = threadIdx.x; i < half; i += blockDim.x) s.cs[i] = rope_sine(position, F[i], a.mscale);
     if (threadIdx.x == blockDim.x - 1) {
-        const int64_t slot = a.slots[tok];
         int64_t page = -1, row = 0;
         if (slot >= 0) {
             page = slot / a.page;
@@ -145,83 +145,281 @@ __device__ __forceinline__ RopeHead rope_head(const RopeArgs& a, int tok, int h,
 
 }  // namespace
 
-// Rows 16-byte aligned, D and the rotated halves (or pairs) in whole vectors
-// of 8.  units: places of a head -- rot/16 of eight pairs (i, i + rot/2), or
-// rot/8 of four adjacent pairs (INTER), then the vectors beyond rot.
+// The two vector kernels want rows 16-byte aligned, D and the rotated halves
+// (or pairs) in whole vectors of 8.  units: places of a head -- rot/16 of
+// eight pairs (i, i + rot/2), or rot/8 of four adjacent pairs (INTER), then
+// the vectors beyond rot.
+
+// One place of a head: eight elements, and their pairs' other halves (half
+// layout: Place::two), rotated by the sines of its pairs.
+template <bool BF, bool INTER>
+struct Place {
+    static constexpr int PAIRS = INTER ? 4 : 8;
+    uint4 x, y;
+    __device__ __forceinline__ void load(const uint16_t* p, bool two, int half) {
+        x = *reinterpret_cast<const uint4*>(p);
+        if (two) y = *reinterpret_cast<const uint4*>(p + half);
+    }
+    __device__ __forceinline__ void floats(float (&f)[8], float (&e)[8], bool two) const {
+        floats8<BF>(x, f);
+        if (two) floats8<BF>(y, e);
+    }
+    static __device__ __forceinline__ void rotate(float (&f)[8], float (&e)[8], const float2* cs) {
+        if (INTER) {
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const float s = f[2 * p], t = f[2 * p + 1];
+                f[2 * p] = s * cs[p].x - t * cs[p].y;
+                f[2 * p + 1] = t * cs[p].x + s * cs[p].y;
+            }
+        } else {
+#pragma unroll
+            for (int p = 0; p < 8; ++p) {
+                const float s = f[p], t = e[p];
+                f[p] = s * cs[p % PAIRS].x - t * cs[p % PAIRS].y;
+                e[p] = t * cs[p % PAIRS].x + s * cs[p % PAIRS].y;
+            }
+        }
+    }
+};
+template <bool BF>
+__device__ __forceinline__ void put_half(uint16_t* p, const float (&f)[8], const float (&e)[8], bool two, int half) {
+    store8<BF>(p, f);
+    if (two) store8<BF>(p + half, e);
+}
+template <bool BF, bool E4>
+__device__ __forceinline__ void put_cache(uint8_t* p, const float (&f)[8], const float (&e)[8], bool two, int half, float inv) {
+    if (E4) {
+        store8_e4m3(p, f, inv);
+        if (two) store8_e4m3(p + half, e, inv);
+    } else {
+        put_half<BF>(reinterpret_cast<uint16_t*>(p), f, e, two, half);
+    }
+}
+
+// Many heads: one token at a time, each thread in one place of every
+// (256 / units)-th head, its sines in registers.
 template <bool BF, bool E4, bool INTER>
-__global__ void __launch_bounds__(ROPE_THREADS, 3) rope_append_kernel(const __grid_constant__ RopeArgs a, int units) {
+__global__ void __launch_bounds__(ROPE_THREADS, INTER ? 3 : 2)
+    rope_heads_kernel(const __grid_constant__ RopeArgs a, int units) {
     __shared__ RopeToken sm_tok[2];
     __shared__ uint64_t sm_turns[MOE_ROPE_MAX_DIM / 2];
+    using P = Place<BF, INTER>;
     constexpr int CES = E4 ? 1 : 2;
-    constexpr int PAIRS = INTER ? 4 : 8;
-    constexpr int AHEAD = INTER ? 4 : 2;  // heads whose loads (64 bytes of them) are issued together
+    constexpr int AHEAD = INTER ? 4 : 2;  // query heads whose loads are issued together
     const int half = a.rot / 2;
     const int rot_units = INTER ? a.rot / 8 : a.rot / 16;
     const int group = threadIdx.x / units, unit = threadIdx.x - group * units;
-    const int groups = blockDim.x / units;
+    const int groups = ROPE_THREADS / units;
     const bool turns = unit < rot_units, two = turns && !INTER;
     const int dim = turns ? unit * 8 : a.rot + (unit - rot_units) * 8;
-    const int heads = group < groups ? a.Hq + 2 * a.Hkv : 0;
+    const int nq = group < groups ? a.Hq : 0, nkv = group < groups ? a.Hkv : 0;
+    // this thread's place in its first head, and steps to its next one
+    const uint16_t* q = static_cast<const uint16_t*>(a.q) + blockIdx.x * a.q_st + group * a.q_sh + dim;
+    const uint16_t* k = static_cast<const uint16_t*>(a.k) + blockIdx.x * a.k_st + group * a.k_sh + dim;
+    const uint16_t* v = static_cast<const uint16_t*>(a.v) + blockIdx.x * a.v_st + group * a.v_sh + dim;
+    uint16_t* qo = static_cast<uint16_t*>(a.q_out) + blockIdx.x * a.qo_st + group * a.qo_sh + dim;
+    const int64_t q_step = groups * a.q_sh, qo_step = groups * a.qo_sh;
+    float2 cs[P::PAIRS];
+
+    // a token's position and slot are loaded while the one before is worked on
+    int position = a.positions[blockIdx.x];
+    int64_t slot = a.slots[blockIdx.x];
     rope_turns(a, sm_turns);
     __syncthreads();
     int buf = 0;
     for (int tok = blockIdx.x; tok < a.T; tok += gridDim.x, buf ^= 1) {
-        uint4 x[AHEAD], y[AHEAD];
-        auto load = [&](int h0) {
+        // the first heads are on their way while the sines are made
+        P pq[AHEAD], pk, pv;
 #pragma unroll
-            for (int i = 0; i < AHEAD; ++i) {
-                const int h = h0 + i * groups;
-                if (h < heads) {
-                    const uint16_t* src = rope_head<CES>(a, tok, h, -1, 0).src + dim;
-                    x[i] = *reinterpret_cast<const uint4*>(src);
-                    if (two) y[i] = *reinterpret_cast<const uint4*>(src + half);
-                }
-            }
-        };
-        load(group);
-        rope_token(a, tok, sm_turns, sm_tok[buf]);
+        for (int i = 0; i < AHEAD; ++i)
+            if (group + i * groups < nq) pq[i].load(q + i * q_step, two, half);
+        if (group < nkv) {
+            pk.load(k, two, half);
+            pv.load(v, two, half);
+        }
+        rope_token(a, position, slot, sm_turns, sm_tok[buf]);
+        if (tok + gridDim.x < a.T) {
+            position = a.positions[tok + gridDim.x];
+            slot = a.slots[tok + gridDim.x];
+        }
         __syncthreads();  // (the other buffer's readers are past: one token apart)
         const int64_t page = sm_tok[buf].page, row = sm_tok[buf].row;
-        float2 cs[PAIRS];
         if (turns)
 #pragma unroll
-            for (int p = 0; p < PAIRS; ++p) cs[p] = sm_tok[buf].cs[unit * PAIRS + p];
-        for (int h0 = group; h0 < heads; h0 += AHEAD * groups) {
-            if (h0 != group) load(h0);
+            for (int p = 0; p < P::PAIRS; ++p) cs[p] = sm_tok[buf].cs[unit * P::PAIRS + p];
+        const uint16_t* qh = q;
+        uint16_t* qoh = qo;
+        float f[8], e[8];
+        for (int h = group; h < nq; h += AHEAD * groups) {
+            if (h != group)
 #pragma unroll
-            for (int i = 0; i < AHEAD; ++i) {
-                const int h = h0 + i * groups;
-                if (h >= heads) continue;
-                const RopeHead hd = rope_head<CES>(a, tok, h, page, row);
-                if (!hd.dst) continue;
-                float f[8], e[8];
-                floats8<BF>(x[i], f);
-                if (two) floats8<BF>(y[i], e);
-                if (turns && hd.turn) {
-                    if (INTER) {
+                for (int i = 0; i < AHEAD; ++i)
+                    if (h + i * groups < nq) pq[i].load(qh + i * q_step, two, half);
 #pragma unroll
-                        for (int p = 0; p < 4; ++p) {
-                            const float u = f[2 * p], v = f[2 * p + 1];
-                            f[2 * p] = u * cs[p].x - v * cs[p].y;
-                            f[2 * p + 1] = v * cs[p].x + u * cs[p].y;
-                        }
-                    } else {
-#pragma unroll
-                        for (int p = 0; p < 8; ++p) {
-                            const float u = f[p], v = e[p];
-                            f[p] = u * cs[p % PAIRS].x - v * cs[p % PAIRS].y;
-                            e[p] = v * cs[p % PAIRS].x + u * cs[p % PAIRS].y;
-                        }
-                    }
+            for (int i = 0; i < AHEAD; ++i)
+                if (h + i * groups < nq) {
+                    pq[i].floats(f, e, two);
+                    if (turns) P::rotate(f, e, cs);
+                    put_half<BF>(qoh + i * qo_step, f, e, two, half);
                 }
-                if (E4 && hd.cache) {
-                    store8_e4m3(hd.dst + dim, f, hd.inv);
-                    if (two) store8_e4m3(hd.dst + dim + half, e, hd.inv);
+            qh += AHEAD * q_step;
+            qoh += AHEAD * qo_step;
+        }
+        if (page >= 0) {
+            for (int h = group; h < nkv; h += groups) {
+                if (h != group) {
+                    pk.load(k + (h - group) * a.k_sh, two, half);
+                    pv.load(v + (h - group) * a.v_sh, two, half);
+                }
+                pk.floats(f, e, two);
+                if (turns) P::rotate(f, e, cs);
+                put_cache<BF, E4>(static_cast<uint8_t*>(a.kc) + (page * a.kc_sp + row * a.kc_st + h * a.kc_sh + dim) * CES, f, e,
+                                  two, half, a.k_inv);
+                pv.floats(f, e, two);
+                put_cache<BF, E4>(static_cast<uint8_t*>(a.vc) + (page * a.vc_sp + row * a.vc_st + h * a.vc_sh + dim) * CES, f, e,
+                                  two, half, a.v_inv);
+            }
+        }
+        q += gridDim.x * a.q_st;
+        k += gridDim.x * a.k_st;
+        v += gridDim.x * a.v_st;
+        qo += gridDim.x * a.qo_st;
+    }
+}
+
+// Fewer heads: `toks` tokens at a time, whose heads (queries, keys, values)
+// are dealt to groups of `units` threads, JOBS to each at most.  A thread's
+// jobs stay the same heads of the block's first, second .. token throughout.
+constexpr int ROPE_SINES = 512;  // pairs of a block's tokens at most
+constexpr int ROPE_TOKS = 8;
+constexpr int rope_jobs(bool inter) { return inter ? 4 : 2; }  // 64 bytes of loads
+template <bool BF, bool E4, bool INTER>
+__global__ void __launch_bounds__(ROPE_THREADS, 3)
+    rope_tokens_kernel(const __grid_constant__ RopeArgs a, int units, int toks) {
+    using P = Place<BF, INTER>;
+    constexpr int JOBS = rope_jobs(INTER);
+    constexpr int CES = E4 ? 1 : 2;
+    __shared__ __align__(16) float2 sm_cs[2][ROPE_SINES];
+    __shared__ uint64_t sm_turns[MOE_ROPE_MAX_DIM / 2];
+    __shared__ int64_t sm_row[2][ROPE_TOKS][2];  // offsets of the token's row in the K and V caches; -1: none
+    __shared__ int sm_pos[2][ROPE_TOKS];
+    const int tid = threadIdx.x;
+    const int half = a.rot / 2;
+    const int rot_units = INTER ? a.rot / 8 : a.rot / 16;
+    const int group = tid / units, unit = tid - group * units;
+    const int groups = ROPE_THREADS / units;
+    const bool turns = unit < rot_units, two = turns && !INTER;
+    const int dim = turns ? unit * 8 : a.rot + (unit - rot_units) * 8;
+    const int heads = a.Hq + 2 * a.Hkv;
+
+    const int64_t stride = (int64_t)gridDim.x * toks;
+    // a token's position and slot: loaded two rounds ahead, put into shared memory one ahead
+    auto put_token = [&](int b, int64_t tok, int position, int64_t slot) {
+        int64_t kr = -1, vr = -1;
+        if (tok < a.T && slot >= 0) {
+            const int64_t page = slot / a.page, row = slot - page * a.page;
+            if (page < a.num_pages) {
+                kr = page * a.kc_sp + row * a.kc_st;
+                vr = page * a.vc_sp + row * a.vc_st;
+            } else {
+                atomicOr(a.err, MOE_DEVERR_PAGE);
+            }
+        }
+        sm_row[b][tid][0] = kr;
+        sm_row[b][tid][1] = vr;
+        sm_pos[b][tid] = position;
+    };
+    int position = 0;
+    int64_t slot = -1;
+    auto load_token = [&](int64_t tok) {
+        if (tok < a.T) {
+            position = a.positions[tok];
+            slot = a.slots[tok];
+        }
+    };
+    const int64_t first = (int64_t)blockIdx.x * toks;
+    if (tid < toks) {
+        load_token(first + tid);
+        put_token(0, first + tid, position, slot);
+        load_token(first + stride + tid);
+    }
+    const uint16_t* src[JOBS];
+    uint8_t* dst[JOBS];         // the query's place (moving on); the head's place in a cache row
+    int64_t src_step[JOBS];
+    int kind[JOBS], tokl[JOBS];  // 0 query, 1 key, 2 value, 3 nothing
+#pragma unroll
+    for (int j = 0; j < JOBS; ++j) {
+        const int hh = group + j * groups;
+        const int tl = hh / heads, h = hh - tl * heads;
+        tokl[j] = tl;
+        kind[j] = group >= groups || tl >= toks ? 3 : h < a.Hq ? 0 : h < a.Hq + a.Hkv ? 1 : 2;
+        const int64_t tok = first + tl;
+        if (kind[j] == 0) {
+            src[j] = static_cast<const uint16_t*>(a.q) + tok * a.q_st + h * a.q_sh + dim;
+            dst[j] = static_cast<uint8_t*>(a.q_out) + (tok * a.qo_st + h * a.qo_sh + dim) * 2;
+            src_step[j] = stride * a.q_st;
+        } else if (kind[j] == 1) {
+            src[j] = static_cast<const uint16_t*>(a.k) + tok * a.k_st + (h - a.Hq) * a.k_sh + dim;
+            dst[j] = static_cast<uint8_t*>(a.kc) + ((h - a.Hq) * a.kc_sh + dim) * CES;
+            src_step[j] = stride * a.k_st;
+        } else {
+            src[j] = static_cast<const uint16_t*>(a.v) + tok * a.v_st + (h - a.Hq - a.Hkv) * a.v_sh + dim;
+            dst[j] = static_cast<uint8_t*>(a.vc) + ((h - a.Hq - a.Hkv) * a.vc_sh + dim) * CES;
+            src_step[j] = stride * a.v_st;
+        }
+    }
+    const int64_t qo_step = stride * a.qo_st * 2;
+    rope_turns(a, sm_turns);
+    __syncthreads();
+
+    int buf = 0;
+    for (int64_t t0 = first; t0 < a.T; t0 += stride, buf ^= 1) {
+        P place[JOBS];
+#pragma unroll
+        for (int j = 0; j < JOBS; ++j)
+            if (kind[j] != 3 && t0 + tokl[j] < a.T) place[j].load(src[j], two, half);
+        // (half layout: two pairs of one unit, then of the next, so that a warp's
+        // reads of 16 bytes by consecutive units are consecutive; 90 -> 82 us at
+        // 16384 tokens of 32 / 4 heads of 128.  The four pairs of an interleaved
+        // unit meet two-way conflicts as they lie, which costs less than the
+        // registers of the other order: 59 against 65 us at 85836 of 4 / 1.)
+        for (int i = tid; i < toks * half; i += ROPE_THREADS) {
+            const int tl = i / half, pair = i - tl * half, r = pair % P::PAIRS;
+            sm_cs[buf][tl * half + (INTER ? pair : (r >> 1) * 2 * rot_units + pair / P::PAIRS * 2 + (r & 1))] =
+                rope_sine(sm_pos[buf][tl], sm_turns[pair], a.mscale);
+        }
+        if (tid < toks) {
+            put_token(buf ^ 1, t0 + stride + tid, position, slot);
+            load_token(t0 + 2 * stride + tid);
+        }
+        __syncthreads();  // (the other buffer's readers are past: one round apart)
+#pragma unroll
+        for (int j = 0; j < JOBS; ++j) {
+            if (kind[j] != 3 && t0 + tokl[j] < a.T) {
+                float f[8], e[8];
+                place[j].floats(f, e, two);
+                if (INTER && turns && kind[j] != 2) P::rotate(f, e, sm_cs[buf] + tokl[j] * half + unit * P::PAIRS);
+                if (!INTER && turns && kind[j] != 2) {
+                    float2 cs[P::PAIRS];
+#pragma unroll
+                    for (int p = 0; p < P::PAIRS / 2; ++p) {
+                        const float4 c =
+                            *reinterpret_cast<const float4*>(&sm_cs[buf][tokl[j] * half + (p * rot_units + unit) * 2]);
+                        cs[2 * p] = make_float2(c.x, c.y);
+                        cs[2 * p + 1] = make_float2(c.z, c.w);
+                    }
+                    P::rotate(f, e, cs);
+                }
+                if (kind[j] == 0) {
+                    put_half<BF>(reinterpret_cast<uint16_t*>(dst[j]), f, e, two, half);
+                    dst[j] += qo_step;
                 } else {
-                    store8<BF>(reinterpret_cast<uint16_t*>(hd.dst) + dim, f);
-                    if (two) store8<BF>(reinterpret_cast<uint16_t*>(hd.dst) + dim + half, e);
+                    const int64_t row = sm_row[buf][tokl[j]][kind[j] - 1];
+                    if (row >= 0) put_cache<BF, E4>(dst[j] + row * CES, f, e, two, half, kind[j] == 1 ? a.k_inv : a.v_inv);
                 }
             }
+            src[j] += src_step[j];
         }
     }
 }
@@ -238,7 +436,7 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_append_any_kernel(const __g
     __syncthreads();
     int buf = 0;
     for (int tok = blockIdx.x; tok < a.T; tok += gridDim.x, buf ^= 1) {
-        rope_token(a, tok, sm_turns, sm_tok[buf]);
+        rope_token(a, a.positions[tok], a.slots[tok], sm_turns, sm_tok[buf]);
         __syncthreads();
         for (int i = threadIdx.x; i < total; i += blockDim.x) {
             const int h = i / units, unit = i - h * units;
@@ -273,15 +471,26 @@ static cudaError_t launch_rope(const RopeArgs& a, const DeviceInfo& di, cudaStre
                      al(a.k, a.k_st, a.k_sh, 0) && al(a.v, a.v_st, a.v_sh, 0) && al(a.q_out, a.qo_st, a.qo_sh, 0) &&
                      al(a.kc, a.kc_sp, a.kc_st, a.kc_sh) && al(a.vc, a.vc_sp, a.vc_st, a.vc_sh);
     if (vec) {
-        // threads for all the heads at once, between 64 and 256
         const int units = (a.interleaved ? a.rot / 8 : a.rot / 16) + (a.D - a.rot) / 8;
-        const int64_t want = (int64_t)units * (a.Hq + 2 * a.Hkv);
-        const int threads = want <= 64 ? 64 : want <= 128 ? 128 : ROPE_THREADS;
-        const int grid = std::min(a.T, di.sm_count * (3 * ROPE_THREADS / threads));
-        if (a.interleaved)
-            rope_append_kernel<BF, E4, true><<<grid, threads, 0, st>>>(a, units);
-        else
-            rope_append_kernel<BF, E4, false><<<grid, threads, 0, st>>>(a, units);
+        const int jobs = ROPE_THREADS / units * rope_jobs(a.interleaved), heads = a.Hq + 2 * a.Hkv;
+        if (heads > jobs) {
+            const int grid = std::min(a.T, di.sm_count * (a.interleaved ? 3 : 2));
+            if (a.interleaved)
+                rope_heads_kernel<BF, E4, true><<<grid, ROPE_THREADS, 0, st>>>(a, units);
+            else
+                rope_heads_kernel<BF, E4, false><<<grid, ROPE_THREADS, 0, st>>>(a, units);
+        } else {
+            // as many tokens as the threads have jobs for, once every block has some
+            const int blocks = di.sm_count * 3;
+            int toks = std::min(jobs / heads, std::min(ROPE_TOKS, a.T / blocks));
+            if (a.rot) toks = std::min(toks, 2 * ROPE_SINES / a.rot);
+            toks = std::max(toks, 1);
+            const int grid = std::min((a.T + toks - 1) / toks, blocks);
+            if (a.interleaved)
+                rope_tokens_kernel<BF, E4, true><<<grid, ROPE_THREADS, 0, st>>>(a, units, toks);
+            else
+                rope_tokens_kernel<BF, E4, false><<<grid, ROPE_THREADS, 0, st>>>(a, units, toks);
+        }
     } else {
         rope_append_any_kernel<BF, E4><<<std::min(a.T, di.sm_count * 8), ROPE_THREADS, 0, st>>>(a);
     }

@@ -285,3 +285,79 @@ def test_matvec_strided_x_and_graph(cuda_device):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(y, want) and math.isfinite(float(y.float().sum()))
+
+
+@pytest.mark.parametrize("dtype,T", [(BF, 1), (BF, 3), (BF, 8), (HF, 1), (HF, 2), (HF, 4)])
+def test_matvec_few_rows_single_weights(cuda_device, dtype, T):
+    """One element of x per row, all its significant bits set: each output is one weight times it, rounded once."""
+    K, N = 96, 256
+    codes = torch.arange(256, dtype=torch.uint8, device=cuda_device)[:, None].expand(256, K // 2).contiguous()
+    z = (torch.arange(256, device=cuda_device) % 16).to(torch.uint8)[:, None].expand(256, 3).contiguous()
+    scales = torch.ones(256, 3, dtype=dtype, device=cuda_device)
+    full = 2 - torch.finfo(dtype).eps     # every bit of the significand
+    for k in (0, 1, 31, 32, 77, 95):
+        x = torch.zeros(T, K, dtype=dtype, device=cuda_device)
+        for t in range(T):
+            x[t, (k + 5 * t) % K] = full * 2.0 ** (3 * t - 9) * (-1) ** t
+        y = moe.matvec4(x, moe.W4(codes, scales, z))
+        for t in range(T):
+            kk = (k + 5 * t) % K
+            w = (codes[:, 0] >> (4 * (kk % 2)) & 15).double() - z[:, 0].double()
+            assert torch.equal(y[t], (w * x[t, kk].double()).to(dtype)), (k, t)
+    assert int((moe.matvec4(torch.zeros(T, K, dtype=dtype, device=cuda_device), moe.W4(codes, scales, z)) != 0).sum()) == 0
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_matvec_few_rows_of_wide_range(cuda_device, dtype):
+    """Elements over 24 binades in one row, and rows of very different size.  An element's parts are exact down to
+    2^-13 of its row's largest and within 2^-22 of the largest below: that much, times the weights, beside FP32."""
+    g = torch.Generator(device=cuda_device).manual_seed(3)
+    N, K, group = 130, 1024, 64
+    for rows in ((1.0,), (1.0, 2.0 ** -8), (2.0 ** 6, 2.0 ** -2, 1.0, 2.0 ** -6)):
+        x = torch.randn(len(rows), K, generator=g, device=cuda_device) * torch.tensor(rows, device=cuda_device)[:, None]
+        x = (x * 2.0 ** -torch.randint(0, 25, x.shape, generator=g, device=cuda_device).float()).to(dtype)
+        codes = torch.randint(0, 256, (N, K // 2), generator=g, device=cuda_device, dtype=torch.uint8)
+        scales = torch.rand(N, K // group, generator=g, device=cuda_device).to(dtype)
+        y = moe.matvec4(x, moe.W4(codes, scales))
+        want, bound = refs.matvec4(x, codes, scales, None, group)
+        weights = 15 * scales.double().repeat_interleave(group, 1).sum(1)
+        within(y, want, bound + 2.0 ** -22 * x.double().abs().amax(1, keepdim=True) * weights, dtype, "wide range")
+
+
+@pytest.mark.parametrize("K,group", [(32, 32), (96, 32), (128, 64), (128, 128), (1184, 32), (2176, 64), (4224, 128), (20000, 32)])
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_matvec_one_row_many_weights(cuda_device, K, group, dtype):
+    mv_check(cuda_device, 1, 9729, K, group, dtype, K % 64 == 0, seed=K, what=f"K={K}")
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_matvec_one_row_single_weights_and_wide_range(cuda_device, dtype):
+    """As the tests of few rows, with the weight rows for which a single row of x is split into 8-bit parts."""
+    K, N = 96, 9984
+    codes = torch.arange(N, device=cuda_device).to(torch.uint8)[:, None].expand(N, K // 2).contiguous()
+    z = (torch.arange(N, device=cuda_device) % 16).to(torch.uint8)[:, None].expand(N, 3).contiguous()
+    scales = torch.ones(N, 3, dtype=dtype, device=cuda_device)
+    full = 2 - torch.finfo(dtype).eps
+    for k, size in ((0, 1.0), (31, 2.0 ** -9), (32, -2.0 ** 12), (95, 3 * 2.0 ** -14)):
+        x = torch.zeros(1, K, dtype=dtype, device=cuda_device)
+        x[0, k] = full * size if size != 3 * 2.0 ** -14 else size
+        w = (codes[:, 0] >> (4 * (k % 2)) & 15).double() - z[:, 0].double()
+        y = moe.matvec4(x, moe.W4(codes, scales, z))
+        assert torch.equal(y[0], (w * x[0, k].double()).to(dtype)), k
+    assert int((moe.matvec4(torch.zeros(1, K, dtype=dtype, device=cuda_device), moe.W4(codes, scales, z)) != 0).sum()) == 0
+    g = torch.Generator(device=cuda_device).manual_seed(4)
+    K, group = 1024, 64
+    codes = torch.randint(0, 256, (N, K // 2), generator=g, device=cuda_device, dtype=torch.uint8)
+    scales = torch.rand(N, K // group, generator=g, device=cuda_device).to(dtype)
+    weights = 15 * scales.double().repeat_interleave(group, 1).sum(1)
+    for top in (1.0, 2.0 ** 10, 2.0 ** -4):
+        x = torch.randn(1, K, generator=g, device=cuda_device)
+        x = (x * top * 2.0 ** -torch.randint(0, 25, x.shape, generator=g, device=cuda_device).float()).to(dtype)
+        want, bound = refs.matvec4(x, codes, scales, None, group)
+        bound = bound + 2.0 ** -22 * x.double().abs().max() * weights
+        y = moe.matvec4(x, moe.W4(codes, scales))
+        # (FP16 at the largest size passes the type's range in places: infinite there)
+        most = torch.finfo(dtype).max
+        inside, beyond = want.abs() + bound < most, want.abs() - bound > most * (1 + refs.half_step(dtype))
+        within(y[inside], want[inside], bound[inside], dtype, "wide")
+        assert torch.equal(y[beyond].double(), want[beyond].sign() * math.inf)
