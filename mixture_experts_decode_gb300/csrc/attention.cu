@@ -35,7 +35,7 @@
 // an equal contiguous run of units (so ragged batches stay balanced), and the
 // last block to finish an item that was cut joins its pieces in order, which
 // keeps the result independent of timing.
-#include "common.cuh"
+#include "block_common.cuh"
 #include "internal.h"
 
 namespace moedec {

@@ -22,7 +22,7 @@
 // running on across them.
 #include <algorithm>
 
-#include "common.cuh"
+#include "block_common.cuh"
 #include "internal.h"
 
 namespace moedec {
