@@ -408,7 +408,8 @@ int moe_mx_requant(const void* in, void* out, int64_t rows, int K, moe_stream_t 
  * Arguments
  *   q          [B][Hq][D] of dtype MOE_BF16 or MOE_F16; strides in elements,
  *              multiples of 8, 16-byte aligned.  out [B][Hq][D] contiguous of
- *              the same dtype.  lse float32 [B][Hq] or NULL.
+ *              the same dtype, which may be a contiguous q.  lse float32
+ *              [B][Hq] or NULL.
  *   k, v       the cache, of cache_dtype = dtype or MOE_E4M3; rows 16-byte
  *              aligned (data and strides).  Token j of sequence b is row
  *              j % page_size of page block_table[b][j / page_size].

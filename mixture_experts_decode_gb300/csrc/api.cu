@@ -495,7 +495,7 @@ int moe_paged_attention(const void* q, int64_t q_stride, int64_t q_head_stride, 
     if (B > MOE_ATTN_MAX_BATCH || (int64_t)Hq * D > (1 << 24)) return MOE_ERR_LIMIT;
     if (B == 0) return MOE_OK;
     if (!q || !seq_lens || !out) return MOE_ERR_ARG;
-    if (num_pages > 0 && max_pages > 0 && (!k.data || !v.data || !block_table)) return MOE_ERR_ARG;
+    if ((max_pages > 0 && !block_table) || (num_pages > 0 && max_pages > 0 && (!k.data || !v.data))) return MOE_ERR_ARG;
     if (!workspace || workspace_bytes < need) return MOE_ERR_WORKSPACE;
     const int es = cache_dtype == MOE_E4M3 ? 1 : 2;
     if (!aligned(q, 16) || !strides_aligned(2, 16, q_stride, q_head_stride, 0) || !aligned(k.data, 16) ||
@@ -510,7 +510,8 @@ int moe_paged_attention(const void* q, int64_t q_stride, int64_t q_head_stride, 
     a.v = v.data, a.v_sp = v.page_stride, a.v_st = v.token_stride, a.v_sh = v.head_stride;
     a.table = block_table, a.table_stride = table_stride, a.lens = seq_lens;
     a.B = B, a.Hq = Hq, a.Hkv = Hkv, a.D = D;
-    a.num_pages = num_pages, a.page = page_size, a.max_pages = max_pages;
+    a.num_pages = num_pages, a.page = page_size;
+    a.max_pages = num_pages > 0 ? max_pages : 0;  // a cache without pages holds no token
     a.window = window, a.sinks = sinks;
     a.scale_log2 = scale * (e4 ? k.scale : 1.f) * 1.44269504088896341f;
     a.v_scale = e4 ? v.scale : 1.f;

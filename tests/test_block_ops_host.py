@@ -174,3 +174,8 @@ def test_binding_refuses_mismatched_tensors(lib):
         moe.matvec4(y, moe.W4(codes, scales.bfloat16()))
     with pytest.raises(ValueError):
         moe.matvec4(y, moe.W4(codes, scales, torch.zeros(8, 1, dtype=torch.uint8)))
+
+
+def test_attention_needs_a_table_even_without_pages(lib):
+    assert _attn(lib, pages=0, table=None) == ARG
+    assert _attn(lib, pages=0, k=_kv(None), v=_kv(None), table=None) == ARG

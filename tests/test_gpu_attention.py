@@ -274,3 +274,20 @@ def test_empty_batch(cuda_device):
     c = make(cuda_device, [5], 4, 2, 64, 16, BF, seed=18)
     out = moe.paged_attention(c["q"][:0], c["k"], c["v"], c["table"][:0], c["lens"][:0])
     assert out.shape == (0, 4, 64)
+
+
+def test_cache_without_pages(cuda_device):
+    q = torch.randn(2, 4, 64, device=cuda_device).to(BF)
+    empty = torch.zeros(0, 16, 2, 64, dtype=BF, device=cuda_device)
+    table = torch.zeros(2, 3, dtype=torch.int32, device=cuda_device)
+    lens = torch.tensor([5, 0], dtype=torch.int32, device=cuda_device)
+    out, lse = moe.paged_attention(q, empty, empty, table, lens, return_lse=True)
+    assert int((out != 0).sum()) == 0 and bool((lse == -math.inf).all())
+    assert moe.device_error(cuda_device) & 0x8
+
+
+def test_output_over_the_query(cuda_device):
+    c = make(cuda_device, [3000, 40, 0, 700], 20, 1, 128, 64, BF, seed=19)
+    want, _ = check(c)
+    moe.paged_attention(c["q"], c["k"], c["v"], c["table"], c["lens"], out=c["q"])
+    assert torch.equal(c["q"], want)
