@@ -293,6 +293,7 @@ __global__ void __launch_bounds__(ATT_THREADS, att_blocks(DP, NT)) paged_attenti
     int64_t* sm_warp = reinterpret_cast<int64_t*>(head_ml + NH);            // [warps] + carry
     int64_t* prefix = sm_warp + 8;                                          // [B] cost up to and with b
 
+    after_previous();
     const int nk = a.D / 16;
     const int chunks16 = a.D * ES / 16;
     const int64_t cap = (int64_t)a.max_pages * a.page;
@@ -751,8 +752,7 @@ static cudaError_t launch_attn(const AttnArgs& a, const DeviceInfo& di, cudaStre
     int per_sm = (int)((size_t)di.smem_per_sm / (smem + 1024));
     per_sm = per_sm < 1 ? 1 : min(per_sm, att_blocks(DP, NT));
     const int grid = min(di.sm_count * per_sm, attn_max_blocks(a.D, a.hpi));
-    kernel<<<grid, ATT_THREADS, smem, st>>>(a);
-    return cudaGetLastError();
+    return launch_after(kernel, dim3(grid), ATT_THREADS, smem, st, a);
 }
 
 template <int KV, bool QBF>

@@ -120,7 +120,7 @@ constexpr int MV_ONE_STAGES = 2;
 
 // GB: blocks of 32 k per group (1, 2, 4).
 template <int MT, int NT, int GB, bool BF>
-__global__ void __launch_bounds__(MV_WARPS * 32, mv_blocks(NT)) matvec4_kernel(const __grid_constant__ Matvec4Args a, int tiles, int steps) {
+__global__ void __launch_bounds__(MV_WARPS * 32, mv_blocks(NT)) matvec4_kernel(const __grid_constant__ Matvec4Args a, int tiles, int steps, int kw_log) {
     constexpr int NST = mv_stages(MT);
     constexpr int STAGE = MT * 16 * MV_ROW;
     constexpr int NGS = 8 / GB;              // groups of a step
@@ -133,8 +133,12 @@ __global__ void __launch_bounds__(MV_WARPS * 32, mv_blocks(NT)) matvec4_kernel(c
     float* sm_sum = reinterpret_cast<float*>(smem + MV_WARPS * NST * STAGE);  // [warps][OUT][32]
     const int tok0 = blockIdx.y * (NT * 8);
     const int toks = min(a.T - tok0, NT * 8);
+    after_previous();
     const int kg = a.K / a.group;
-    const int per_warp = (steps + MV_WARPS - 1) / MV_WARPS;  // steps of a warp and tile
+    // 2^kw_log warps share K (step = i * that + kw), the others take further rows
+    const int kws = 1 << kw_log, kw = warp & (kws - 1), rw = warp >> kw_log;
+    const int tile_rows = (MV_WARPS >> kw_log) * (MT * 16);
+    const int per_warp = (steps + kws - 1) >> kw_log;  // steps of a warp and tile
     const int my_tiles = ((int)blockIdx.x < tiles) ? (tiles - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
     // Rows beyond T read the first row of x again: their columns of the
     // products are not stored, and no column depends on another.
@@ -154,9 +158,9 @@ __global__ void __launch_bounds__(MV_WARPS * 32, mv_blocks(NT)) matvec4_kernel(c
     int is_tile = 0, is_step = 0, is_stage = 0;
     auto issue = [&]() {
         if (is_tile < my_tiles) {
-            const int64_t row0 = (int64_t)(blockIdx.x + (int64_t)is_tile * gridDim.x) * (MT * 16);
+            const int64_t row0 = (int64_t)(blockIdx.x + (int64_t)is_tile * gridDim.x) * tile_rows + rw * (MT * 16);
             const int r = lane >> 3;
-            const int kb = min((is_step * MV_WARPS + warp) * MV_ROW + (lane & 7) * 16, last_kb);
+            const int kb = min((is_step * kws + kw) * MV_ROW + (lane & 7) * 16, last_kb);
             uint8_t* s = ring + is_stage * STAGE + r * MV_ROW;
             const int sw0 = ((lane & 7) ^ r) << 4, sw1 = sw0 ^ 64;  // row & 7 is r or r + 4
             if (row0 + MT * 16 <= a.N) {
@@ -184,9 +188,9 @@ __global__ void __launch_bounds__(MV_WARPS * 32, mv_blocks(NT)) matvec4_kernel(c
     int sz_tile = 0, sz_step = 0;
     const bool whole_groups = kg % NGS == 0 && a.scales_aligned;
     auto fetch_sz = [&]() {
-        const int64_t row = min((int64_t)(blockIdx.x + (int64_t)sz_tile * gridDim.x) * (MT * 16) + (lane & (MT * 16 - 1)),
+        const int64_t row = min((int64_t)(blockIdx.x + (int64_t)sz_tile * gridDim.x) * tile_rows + rw * (MT * 16) + (lane & (MT * 16 - 1)),
                                 (int64_t)a.N - 1);
-        const int gi0 = (sz_step * MV_WARPS + warp) * NGS;
+        const int gi0 = (sz_step * kws + kw) * NGS;
         if (whole_groups && gi0 < kg) {
             const int64_t at = row * kg + gi0;
             const uint16_t* sp = static_cast<const uint16_t*>(a.scales) + at;
@@ -226,7 +230,7 @@ __global__ void __launch_bounds__(MV_WARPS * 32, mv_blocks(NT)) matvec4_kernel(c
 
     int use_stage = 0;
     for (int tile = 0; tile < my_tiles; ++tile) {
-        const int64_t row0 = (int64_t)(blockIdx.x + (int64_t)tile * gridDim.x) * (MT * 16);
+        const int64_t row0 = (int64_t)(blockIdx.x + (int64_t)tile * gridDim.x) * tile_rows;
         float tot[MT][NT][4];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
@@ -237,7 +241,7 @@ __global__ void __launch_bounds__(MV_WARPS * 32, mv_blocks(NT)) matvec4_kernel(c
 
 #pragma unroll 1
         for (int si = 0; si < per_warp; ++si) {
-            const int step = si * MV_WARPS + warp;
+            const int step = si * kws + kw;
             uint32_t sz[NGS];  // scale | FP16 of 16 + zero << 16
             // 1024 + z by its bits, less 1008: 16 + z, exact
 #pragma unroll
@@ -343,14 +347,14 @@ __global__ void __launch_bounds__(MV_WARPS * 32, mv_blocks(NT)) matvec4_kernel(c
                 for (int j = 0; j < 4; ++j) sm_sum[(warp * OUT + (mt * NT + nt) * 4 + j) * 32 + lane] = tot[mt][nt][j];
         __syncthreads();
         // consecutive threads take consecutive rows of a token
-        for (int e = tid; e < MT * 16 * toks; e += MV_WARPS * 32) {
-            const int r = e % (MT * 16), tk = e / (MT * 16);
-            const int mt = r >> 4, rg = r & 7, h = (r >> 3) & 1;
+        for (int e = tid; e < tile_rows * toks; e += MV_WARPS * 32) {
+            const int tk = e / tile_rows, r = e - tk * tile_rows;
+            const int mt = (r >> 4) % MT, rg = r & 7, h = (r >> 3) & 1;
             const int nt = tk >> 3, tt = (tk & 7) >> 1, c = tk & 1;
             const int at = ((mt * NT + nt) * 4 + 2 * h + c) * 32 + rg * 4 + tt;
+            const float* first = sm_sum + ((r / (MT * 16)) << kw_log) * OUT * 32 + at;
             float v = 0.f;
-#pragma unroll
-            for (int w = 0; w < MV_WARPS; ++w) v += sm_sum[w * OUT * 32 + at];
+            for (int w = 0; w < kws; ++w) v += first[w * OUT * 32];
             const int64_t row = row0 + r;
             if (row < a.N) {
                 const int64_t o = (int64_t)(tok0 + tk) * a.y_stride + row;
@@ -381,7 +385,7 @@ __global__ void __launch_bounds__(MV_WARPS * 32, mv_blocks(NT)) matvec4_kernel(c
 // splitting of x costs more (4864 x 1024, 5 rows: 7.7 against 4.5), and more
 // rows fill more columns with parts (14336 x 4096, 4 rows: 18.5 against 14.7).
 template <int MT, int GB, bool BF>
-__global__ void __launch_bounds__(MV_WARPS * 32, 2) matvec4_one_kernel(const __grid_constant__ Matvec4Args a, int tiles, int steps) {
+__global__ void __launch_bounds__(MV_WARPS * 32, 2) matvec4_one_kernel(const __grid_constant__ Matvec4Args a, int tiles, int steps, int kw_log) {
     constexpr int NST = MV_ONE_STAGES;
     constexpr int STAGE = MT * 16 * MV_ROW;
     constexpr int NGS = 8 / GB;              // groups of a step
@@ -393,8 +397,12 @@ __global__ void __launch_bounds__(MV_WARPS * 32, 2) matvec4_one_kernel(const __g
     float* sm_sum = reinterpret_cast<float*>(smem + MV_WARPS * NST * STAGE);  // [warps][MT][16][2]
     uint32_t* sm_amax = reinterpret_cast<uint32_t*>(sm_sum + MV_WARPS * MT * 32);  // FP32 bits
     uint8_t* sm_x = reinterpret_cast<uint8_t*>(sm_amax + 4);  // [K / 32][PARTS][4][8]
+    after_previous();
     const int kg = a.K / a.group;
-    const int per_warp = (steps + MV_WARPS - 1) / MV_WARPS;  // steps of a warp and tile
+    // 2^kw_log warps share K (step = i * that + kw), the others take further rows
+    const int kws = 1 << kw_log, kw = warp & (kws - 1), rw = warp >> kw_log;
+    const int tile_rows = (MV_WARPS >> kw_log) * (MT * 16);
+    const int per_warp = (steps + kws - 1) >> kw_log;  // steps of a warp and tile
     const int my_tiles = ((int)blockIdx.x < tiles) ? (tiles - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
     // Nothing below branches per lane, because the matrix instructions need
     // the whole warp together: weight rows beyond N read the last row again
@@ -405,9 +413,9 @@ __global__ void __launch_bounds__(MV_WARPS * 32, 2) matvec4_one_kernel(const __g
     int is_tile = 0, is_step = 0, is_stage = 0;
     auto issue = [&]() {
         if (is_tile < my_tiles) {
-            const int64_t row0 = (int64_t)(blockIdx.x + (int64_t)is_tile * gridDim.x) * (MT * 16);
+            const int64_t row0 = (int64_t)(blockIdx.x + (int64_t)is_tile * gridDim.x) * tile_rows + rw * (MT * 16);
             const int r = lane >> 3;
-            const int kb = min((is_step * MV_WARPS + warp) * MV_ROW + (lane & 7) * 16, last_kb);
+            const int kb = min((is_step * kws + kw) * MV_ROW + (lane & 7) * 16, last_kb);
             uint8_t* s = ring + is_stage * STAGE + r * MV_ROW;
             const int sw0 = ((lane & 7) ^ r) << 4, sw1 = sw0 ^ 64;  // row & 7 is r or r + 4
             if (row0 + MT * 16 <= a.N) {
@@ -435,9 +443,9 @@ __global__ void __launch_bounds__(MV_WARPS * 32, 2) matvec4_one_kernel(const __g
     int sz_tile = 0, sz_step = 0;
     const bool whole_groups = kg % NGS == 0 && a.scales_aligned;
     auto fetch_sz = [&]() {
-        const int64_t row = min((int64_t)(blockIdx.x + (int64_t)sz_tile * gridDim.x) * (MT * 16) + (lane & (MT * 16 - 1)),
+        const int64_t row = min((int64_t)(blockIdx.x + (int64_t)sz_tile * gridDim.x) * tile_rows + rw * (MT * 16) + (lane & (MT * 16 - 1)),
                                 (int64_t)a.N - 1);
-        const int gi0 = (sz_step * MV_WARPS + warp) * NGS;
+        const int gi0 = (sz_step * kws + kw) * NGS;
         if (whole_groups && gi0 < kg) {
             const int64_t at = row * kg + gi0;
             const uint16_t* sp = static_cast<const uint16_t*>(a.scales) + at;
@@ -520,7 +528,7 @@ __global__ void __launch_bounds__(MV_WARPS * 32, 2) matvec4_one_kernel(const __g
 
     int use_stage = 0;
     for (int tile = 0; tile < my_tiles; ++tile) {
-        const int64_t row0 = (int64_t)(blockIdx.x + (int64_t)tile * gridDim.x) * (MT * 16);
+        const int64_t row0 = (int64_t)(blockIdx.x + (int64_t)tile * gridDim.x) * tile_rows;
         float tot[MT][2];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
@@ -529,7 +537,7 @@ __global__ void __launch_bounds__(MV_WARPS * 32, 2) matvec4_one_kernel(const __g
 
 #pragma unroll 1
         for (int si = 0; si < per_warp; ++si) {
-            const int step = si * MV_WARPS + warp;
+            const int step = si * kws + kw;
             uint32_t sz[NGS];  // scale | FP16 of zero << 16
             // 1024 + z by its bits, less 1024: z, exact
 #pragma unroll
@@ -594,12 +602,13 @@ __global__ void __launch_bounds__(MV_WARPS * 32, 2) matvec4_one_kernel(const __g
             for (int h = 0; h < 2; ++h)
                 if (t < PARTS - 1) sm_sum[((warp * MT + mt) * 16 + h * 8 + g) * 2 + t] = tot[mt][h];
         __syncthreads();
-        for (int r = tid; r < MT * 16; r += MV_WARPS * 32) {
+        for (int r = tid; r < tile_rows; r += MV_WARPS * 32) {
+            const int g0 = r / (MT * 16);
+            const float* first = sm_sum + ((g0 << kw_log) * MT * 16 + r - g0 * (MT * 16)) * 2;
             float v = 0.f;
-#pragma unroll
-            for (int w = 0; w < MV_WARPS; ++w) {
-                v += sm_sum[(w * MT * 16 + r) * 2];
-                if (PARTS > 2) v += sm_sum[(w * MT * 16 + r) * 2 + 1];
+            for (int w = 0; w < kws; ++w) {
+                v += first[w * MT * 32];
+                if (PARTS > 2) v += first[w * MT * 32 + 1];
             }
             // codes in units of 2^-9, x times 2^(7 - exponent)
             v = v * 512.f * __uint_as_float((uint32_t)(127 - 7 + exponent) << 23);
@@ -615,10 +624,19 @@ __global__ void __launch_bounds__(MV_WARPS * 32, 2) matvec4_one_kernel(const __g
     cp_async_wait<0>();
 }
 
+// Warps that share K: all eight, or as many as there are steps (a power of
+// two), so that none is idle on short rows.
+static int mv_kw_log(int steps) { return steps >= 8 ? 3 : steps >= 4 ? 2 : steps >= 2 ? 1 : 0; }
+// Tiles of a block with two row tiles a warp.
+static int mv_tiles2(const Matvec4Args& a) {
+    const int rows = (MV_WARPS >> mv_kw_log((a.K + MV_STEP - 1) / MV_STEP)) * 32;
+    return (a.N + rows - 1) / rows;
+}
+
 // Enough weight rows to repay the splitting of x, whose parts fit shared
 // memory beside the ring.
 static bool one_row(const Matvec4Args& a, const DeviceInfo& di, bool bf) {
-    return a.T == 1 && (a.N + 31) / 32 >= 2 * di.sm_count && (int64_t)a.K * (bf ? 2 : 3) <= 65536;
+    return a.T == 1 && mv_tiles2(a) >= 2 * di.sm_count && (int64_t)a.K * (bf ? 2 : 3) <= 65536;
 }
 
 template <int MT, int GB, bool BF>
@@ -629,11 +647,11 @@ static cudaError_t launch_mv_one(const Matvec4Args& a, const DeviceInfo& di, cud
     static SmemOnce once;
     const cudaError_t e = once.set(reinterpret_cast<const void*>(kernel), (int)fixed + 65536);
     if (e != cudaSuccess) return e;
-    const int tiles = (a.N + MT * 16 - 1) / (MT * 16);
-    const int steps = (a.K + MV_STEP - 1) / MV_STEP;
+    const int steps = (a.K + MV_STEP - 1) / MV_STEP, kw_log = mv_kw_log(steps);
+    const int tile_rows = (MV_WARPS >> kw_log) * MT * 16;
+    const int tiles = (a.N + tile_rows - 1) / tile_rows;
     const int per_sm = std::max(1, std::min(2, (int)((size_t)di.smem_per_sm / (smem + 1024))));
-    kernel<<<std::min(tiles, di.sm_count * per_sm), MV_WARPS * 32, smem, st>>>(a, tiles, steps);
-    return cudaGetLastError();
+    return launch_after(kernel, dim3(std::min(tiles, di.sm_count * per_sm)), MV_WARPS * 32, smem, st, a, tiles, steps, kw_log);
 }
 
 template <int MT, bool BF>
@@ -651,12 +669,12 @@ static cudaError_t launch_mv(const Matvec4Args& a, const DeviceInfo& di, cudaStr
     static SmemOnce once;
     cudaError_t e = once.set(reinterpret_cast<const void*>(kernel), (int)smem);
     if (e != cudaSuccess) return e;
-    const int tiles = (a.N + MT * 16 - 1) / (MT * 16);
-    const int steps = (a.K + MV_STEP - 1) / MV_STEP;
+    const int steps = (a.K + MV_STEP - 1) / MV_STEP, kw_log = mv_kw_log(steps);
+    const int tile_rows = (MV_WARPS >> kw_log) * MT * 16;
+    const int tiles = (a.N + tile_rows - 1) / tile_rows;
     const int per_sm = std::max(1, std::min(3, (int)((size_t)di.smem_per_sm / (smem + 1024))));
     const dim3 grid(std::min(tiles, di.sm_count * per_sm), (a.T + NT * 8 - 1) / (NT * 8));
-    kernel<<<grid, MV_WARPS * 32, smem, st>>>(a, tiles, steps);
-    return cudaGetLastError();
+    return launch_after(kernel, grid, MV_WARPS * 32, smem, st, a, tiles, steps, kw_log);
 }
 
 template <int MT, int NT, bool BF>
@@ -668,7 +686,7 @@ static cudaError_t launch_mv_group(const Matvec4Args& a, const DeviceInfo& di, c
 
 template <bool BF>
 static cudaError_t launch_mv_rows(const Matvec4Args& a, const DeviceInfo& di, cudaStream_t st) {
-    const bool two = (a.N + 31) / 32 >= di.sm_count;
+    const bool two = mv_tiles2(a) >= di.sm_count;  // two row tiles a warp once they fill the SMs
     if (one_row(a, di, BF)) return launch_mv_one_group<2, BF>(a, di, st);
     if (a.T <= 8) return two ? launch_mv_group<2, 1, BF>(a, di, st) : launch_mv_group<1, 1, BF>(a, di, st);
     if (a.T <= 16) return two ? launch_mv_group<2, 2, BF>(a, di, st) : launch_mv_group<1, 2, BF>(a, di, st);

@@ -20,7 +20,7 @@
 // MB): 139 us, 5.9 TB/s; one row of 2048: 2.4 us.
 #include <algorithm>
 
-#include "common.cuh"
+#include "block_common.cuh"
 #include "internal.h"
 
 namespace moedec {
@@ -227,6 +227,7 @@ template <int WARPS, int NV, int VW, bool BF, bool RF>
 __global__ void __launch_bounds__(WARPS == 1 ? 128 : WARPS * 32, norm_min_blocks(WARPS, NV, VW))
     norm_rows_kernel(const NormArgs a) {
     __shared__ float scratch[2][32];
+    after_previous();
     const int64_t row = WARPS == 1 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5) : blockIdx.x;
     if (row >= a.T) return;  // (WARPS = 1 has no barriers)
     const int first = WARPS == 1 ? threadIdx.x & 31 : threadIdx.x;
@@ -293,6 +294,7 @@ __global__ void __launch_bounds__(NORM_ANY_WARPS * 32) norm_any_kernel(const Nor
     extern __shared__ float sm_row[];
     __shared__ float scratch[2][32];
     constexpr int TH = NORM_ANY_WARPS * 32;
+    after_previous();
     const int64_t row = blockIdx.x;
     const int tid = threadIdx.x;
     int phase = 0;
@@ -332,9 +334,10 @@ __global__ void __launch_bounds__(NORM_ANY_WARPS * 32) norm_any_kernel(const Nor
 }
 
 template <int WARPS, int NV, int VW, bool BF, bool RF>
-static void norm_rows(const NormArgs& a, cudaStream_t st) {
+static cudaError_t norm_rows(const NormArgs& a, cudaStream_t st) {
     constexpr int rows = WARPS == 1 ? 4 : 1;
-    norm_rows_kernel<WARPS, NV, VW, BF, RF><<<(a.T + rows - 1) / rows, WARPS == 1 ? 128 : WARPS * 32, 0, st>>>(a);
+    return launch_after(norm_rows_kernel<WARPS, NV, VW, BF, RF>, dim3((a.T + rows - 1) / rows), WARPS == 1 ? 128 : WARPS * 32, 0,
+                        st, a);
 }
 
 template <bool BF, bool RF>
@@ -355,28 +358,30 @@ static cudaError_t launch_norm(const NormArgs& a, const DeviceInfo& di, cudaStre
         static SmemOnce once;
         const cudaError_t e = once.set(reinterpret_cast<const void*>(norm_any_kernel<BF, RF>), MOE_NORM_MAX_DIM * 4);
         if (e != cudaSuccess) return e;
-        norm_any_kernel<BF, RF><<<a.T, NORM_ANY_WARPS * 32, (size_t)a.d * 4, st>>>(a);
-    } else if (fits(8)) {
-        if (a.d <= 256) norm_rows<1, 1, 8, BF, RF>(a, st);
-        else if (a.d <= 512 && many) norm_rows<1, 2, 8, BF, RF>(a, st);
-        else if (a.d <= 1024 && many) norm_rows<1, 4, 8, BF, RF>(a, st);
-        else if (a.d <= 1024) norm_rows<4, 1, 8, BF, RF>(a, st);
-        else if (a.d <= 2048) norm_rows<8, 1, 8, BF, RF>(a, st);
-        else if (a.d <= 4096) norm_rows<16, 1, 8, BF, RF>(a, st);
-        else if (a.d <= 8192) norm_rows<16, 2, 8, BF, RF>(a, st);
-        else norm_rows<16, 4, 8, BF, RF>(a, st);
-    } else if (fits(4)) {
-        if (a.d <= 512) norm_rows<1, 4, 4, BF, RF>(a, st);
-        else if (a.d <= 2048) norm_rows<4, 4, 4, BF, RF>(a, st);
-        else if (a.d <= 8192) norm_rows<16, 4, 4, BF, RF>(a, st);
-        else norm_rows<16, 8, 4, BF, RF>(a, st);
-    } else {
-        if (a.d <= 512) norm_rows<1, 16, 1, BF, RF>(a, st);
-        else if (a.d <= 2048) norm_rows<4, 16, 1, BF, RF>(a, st);
-        else if (a.d <= 8192) norm_rows<16, 16, 1, BF, RF>(a, st);
-        else norm_rows<16, 32, 1, BF, RF>(a, st);
+        return launch_after(norm_any_kernel<BF, RF>, dim3(a.T), NORM_ANY_WARPS * 32, (size_t)a.d * 4, st, a);
     }
-    return cudaGetLastError();
+    if (fits(8)) {
+        if (a.d <= 256) return norm_rows<1, 1, 8, BF, RF>(a, st);
+        if (a.d <= 512 && many) return norm_rows<1, 2, 8, BF, RF>(a, st);
+        if (a.d <= 1024 && many) return norm_rows<1, 4, 8, BF, RF>(a, st);
+        if (a.d <= 1024) return norm_rows<4, 1, 8, BF, RF>(a, st);
+        if (a.d <= 2048) return norm_rows<8, 1, 8, BF, RF>(a, st);
+        if (a.d <= 4096) return norm_rows<16, 1, 8, BF, RF>(a, st);
+        if (a.d <= 8192) return norm_rows<16, 2, 8, BF, RF>(a, st);
+        return norm_rows<16, 4, 8, BF, RF>(a, st);
+    }
+    if (fits(4)) {
+        if (a.d <= 128) return norm_rows<1, 1, 4, BF, RF>(a, st);
+        if (a.d <= 512) return norm_rows<1, 4, 4, BF, RF>(a, st);
+        if (a.d <= 2048) return norm_rows<4, 4, 4, BF, RF>(a, st);
+        if (a.d <= 8192) return norm_rows<16, 4, 4, BF, RF>(a, st);
+        return norm_rows<16, 8, 4, BF, RF>(a, st);
+    }
+    if (a.d <= 128) return norm_rows<1, 4, 1, BF, RF>(a, st);
+    if (a.d <= 512) return norm_rows<1, 16, 1, BF, RF>(a, st);
+    if (a.d <= 2048) return norm_rows<4, 16, 1, BF, RF>(a, st);
+    if (a.d <= 8192) return norm_rows<16, 16, 1, BF, RF>(a, st);
+    return norm_rows<16, 32, 1, BF, RF>(a, st);
 }
 
 cudaError_t launch_norm_residual(const NormArgs& a, int dtype, int resid_dtype, cudaStream_t st) {

@@ -21,7 +21,7 @@
 // saturated at 448).
 #include <algorithm>
 
-#include "common.cuh"
+#include "block_common.cuh"
 #include "internal.h"
 
 namespace moedec {
@@ -204,6 +204,7 @@ __global__ void __launch_bounds__(ROPE_THREADS, INTER ? 3 : 2)
     rope_heads_kernel(const __grid_constant__ RopeArgs a, int units) {
     __shared__ RopeToken sm_tok[2];
     __shared__ uint64_t sm_turns[MOE_ROPE_MAX_DIM / 2];
+    after_previous();
     using P = Place<BF, INTER>;
     constexpr int CES = E4 ? 1 : 2;
     constexpr int AHEAD = INTER ? 4 : 2;  // query heads whose loads are issued together
@@ -297,6 +298,7 @@ constexpr int rope_jobs(bool inter) { return inter ? 4 : 2; }  // 64 bytes of lo
 template <bool BF, bool E4, bool INTER>
 __global__ void __launch_bounds__(ROPE_THREADS, 3)
     rope_tokens_kernel(const __grid_constant__ RopeArgs a, int units, int toks) {
+    after_previous();
     using P = Place<BF, INTER>;
     constexpr int JOBS = rope_jobs(INTER);
     constexpr int CES = E4 ? 1 : 2;
@@ -429,6 +431,7 @@ template <bool BF, bool E4>
 __global__ void __launch_bounds__(ROPE_THREADS) rope_append_any_kernel(const __grid_constant__ RopeArgs a) {
     __shared__ RopeToken sm_tok[2];
     __shared__ uint64_t sm_turns[MOE_ROPE_MAX_DIM / 2];
+    after_previous();
     const int half = a.rot / 2;
     const int units = half + a.D - a.rot;
     const int total = (a.Hq + 2 * a.Hkv) * units;
@@ -476,25 +479,20 @@ static cudaError_t launch_rope(const RopeArgs& a, const DeviceInfo& di, cudaStre
         if (heads > jobs) {
             const int grid = std::min(a.T, di.sm_count * (a.interleaved ? 3 : 2));
             if (a.interleaved)
-                rope_heads_kernel<BF, E4, true><<<grid, ROPE_THREADS, 0, st>>>(a, units);
-            else
-                rope_heads_kernel<BF, E4, false><<<grid, ROPE_THREADS, 0, st>>>(a, units);
-        } else {
-            // as many tokens as the threads have jobs for, once every block has some
-            const int blocks = di.sm_count * 3;
-            int toks = std::min(jobs / heads, std::min(ROPE_TOKS, a.T / blocks));
-            if (a.rot) toks = std::min(toks, 2 * ROPE_SINES / a.rot);
-            toks = std::max(toks, 1);
-            const int grid = std::min((a.T + toks - 1) / toks, blocks);
-            if (a.interleaved)
-                rope_tokens_kernel<BF, E4, true><<<grid, ROPE_THREADS, 0, st>>>(a, units, toks);
-            else
-                rope_tokens_kernel<BF, E4, false><<<grid, ROPE_THREADS, 0, st>>>(a, units, toks);
+                return launch_after(rope_heads_kernel<BF, E4, true>, dim3(grid), ROPE_THREADS, 0, st, a, units);
+            return launch_after(rope_heads_kernel<BF, E4, false>, dim3(grid), ROPE_THREADS, 0, st, a, units);
         }
-    } else {
-        rope_append_any_kernel<BF, E4><<<std::min(a.T, di.sm_count * 8), ROPE_THREADS, 0, st>>>(a);
+        // as many tokens as the threads have jobs for, once every block has some
+        const int blocks = di.sm_count * 3;
+        int toks = std::min(jobs / heads, std::min(ROPE_TOKS, a.T / blocks));
+        if (a.rot) toks = std::min(toks, 2 * ROPE_SINES / a.rot);
+        toks = std::max(toks, 1);
+        const int grid = std::min((a.T + toks - 1) / toks, blocks);
+        if (a.interleaved)
+            return launch_after(rope_tokens_kernel<BF, E4, true>, dim3(grid), ROPE_THREADS, 0, st, a, units, toks);
+        return launch_after(rope_tokens_kernel<BF, E4, false>, dim3(grid), ROPE_THREADS, 0, st, a, units, toks);
     }
-    return cudaGetLastError();
+    return launch_after(rope_append_any_kernel<BF, E4>, dim3(std::min(a.T, di.sm_count * 8)), ROPE_THREADS, 0, st, a);
 }
 
 cudaError_t launch_rope_append(RopeArgs a, int dtype, int cache_dtype, cudaStream_t st) {
