@@ -361,6 +361,7 @@ static cudaError_t launch_norm(const NormArgs& a, const DeviceInfo& di, cudaStre
         return launch_after(norm_any_kernel<BF, RF>, dim3(a.T), NORM_ANY_WARPS * 32, (size_t)a.d * 4, st, a);
     }
     if (fits(8)) {
+        if (a.d <= 128) return norm_rows<1, 1, 4, BF, RF>(a, st);
         if (a.d <= 256) return norm_rows<1, 1, 8, BF, RF>(a, st);
         if (a.d <= 512 && many) return norm_rows<1, 2, 8, BF, RF>(a, st);
         if (a.d <= 1024 && many) return norm_rows<1, 4, 8, BF, RF>(a, st);
@@ -372,14 +373,16 @@ static cudaError_t launch_norm(const NormArgs& a, const DeviceInfo& di, cudaStre
     }
     if (fits(4)) {
         if (a.d <= 128) return norm_rows<1, 1, 4, BF, RF>(a, st);
+        if (a.d <= 256) return norm_rows<1, 2, 4, BF, RF>(a, st);
         if (a.d <= 512) return norm_rows<1, 4, 4, BF, RF>(a, st);
         if (a.d <= 2048) return norm_rows<4, 4, 4, BF, RF>(a, st);
         if (a.d <= 8192) return norm_rows<16, 4, 4, BF, RF>(a, st);
         return norm_rows<16, 8, 4, BF, RF>(a, st);
     }
     if (a.d <= 128) return norm_rows<1, 4, 1, BF, RF>(a, st);
-    if (a.d <= 512) return norm_rows<1, 16, 1, BF, RF>(a, st);
-    if (a.d <= 2048) return norm_rows<4, 16, 1, BF, RF>(a, st);
+    if (a.d <= 512) return norm_rows<4, 4, 1, BF, RF>(a, st);
+    if (a.d <= 2048) return norm_rows<8, 8, 1, BF, RF>(a, st);
+    if (a.d <= 4096) return norm_rows<16, 8, 1, BF, RF>(a, st);
     if (a.d <= 8192) return norm_rows<16, 16, 1, BF, RF>(a, st);
     return norm_rows<16, 32, 1, BF, RF>(a, st);
 }
