@@ -361,3 +361,23 @@ def test_matvec_one_row_single_weights_and_wide_range(cuda_device, dtype):
         inside, beyond = want.abs() + bound < most, want.abs() - bound > most * (1 + refs.half_step(dtype))
         within(y[inside], want[inside], bound[inside], dtype, "wide")
         assert torch.equal(y[beyond].double(), want[beyond].sign() * math.inf)
+
+
+@pytest.mark.parametrize("T,d", [(1, 9), (2, 1), (9, 15), (17, 85), (8, 255), (1300, 257), (5, 505), (1300, 511), (3, 1017), (4, 2041), (3, 4095),
+                                 (2, 8183), (3, 8185), (2, 16375), (2, 16377), (11, 340)])
+@pytest.mark.parametrize("gate", ["none", "full", "column", "row"])
+def test_norm_rows_between_vectors(cuda_device, T, d, gate):
+    for resid in (BF, F32):
+        norm_check(cuda_device, T, d, BF, resid, "layer", "rms", gate, "sigmoid", 0.5, bias=True, seed=d, what=f"{T}x{d} {gate}")
+    # nothing beyond the arrays' ends is written
+    y = torch.randn(T * d + 64, device=cuda_device).to(HF)
+    buf = [torch.full((T * d + 64,), 7.0, dtype=HF, device=cuda_device) for _ in range(2)]
+    inner = [b[32:32 + T * d].view(T, d) for b in buf]
+    moe.norm_residual(y[:T * d].view(T, d), y[:T * d].view(T, d), pre=moe.Norm(), resid_out=inner[0], out=inner[1])
+    for b in buf:
+        assert bool((b[:32] == 7).all()) and bool((b[32 + T * d:] == 7).all())
+    # in place, a row's end next to another row's beginning
+    r = y[:T * d].view(T, d).clone()
+    want, x = moe.norm_residual(y[:T * d].view(T, d), r, pre=moe.Norm())
+    moe.norm_residual(y[:T * d].view(T, d), r, pre=moe.Norm(), resid_out=r)
+    assert torch.equal(r, want)
