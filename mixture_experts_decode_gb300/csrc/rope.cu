@@ -292,15 +292,17 @@ __global__ void __launch_bounds__(ROPE_THREADS, INTER ? 3 : 2)
 // Fewer heads: `toks` tokens at a time, whose heads (queries, keys, values)
 // are dealt to groups of `units` threads, JOBS to each at most.  A thread's
 // jobs stay the same heads of the block's first, second .. token throughout.
+// (Half layout: four jobs of 32 bytes in two blocks per SM, 66 us at 16384
+// tokens of 32 / 4 heads of 128; two in three blocks 81, three in two 75.)
 constexpr int ROPE_SINES = 512;  // pairs of a block's tokens at most
-constexpr int ROPE_TOKS = 8;
-constexpr int rope_jobs(bool inter) { return inter ? 4 : 2; }  // 64 bytes of loads
+constexpr int ROPE_TOKS = 16;
+constexpr int ROPE_JOBS = 4;
 template <bool BF, bool E4, bool INTER>
-__global__ void __launch_bounds__(ROPE_THREADS, 3)
+__global__ void __launch_bounds__(ROPE_THREADS, INTER ? 3 : 2)
     rope_tokens_kernel(const __grid_constant__ RopeArgs a, int units, int toks) {
     after_previous();
     using P = Place<BF, INTER>;
-    constexpr int JOBS = rope_jobs(INTER);
+    constexpr int JOBS = ROPE_JOBS;
     constexpr int CES = E4 ? 1 : 2;
     __shared__ __align__(16) float2 sm_cs[2][ROPE_SINES];
     __shared__ uint64_t sm_turns[MOE_ROPE_MAX_DIM / 2];
@@ -382,8 +384,8 @@ __global__ void __launch_bounds__(ROPE_THREADS, 3)
         for (int j = 0; j < JOBS; ++j)
             if (kind[j] != 3 && t0 + tokl[j] < a.T) place[j].load(src[j], two, half);
         // (half layout: two pairs of one unit, then of the next, so that a warp's
-        // reads of 16 bytes by consecutive units are consecutive; 90 -> 82 us at
-        // 16384 tokens of 32 / 4 heads of 128.  The four pairs of an interleaved
+        // reads of 16 bytes by consecutive units are consecutive; it took 8 of 90
+        // us off 16384 tokens of 32 / 4 heads of 128.  The four pairs of an interleaved
         // unit meet two-way conflicts as they lie, which costs less than the
         // registers of the other order: 59 against 65 us at 85836 of 4 / 1.)
         for (int i = tid; i < toks * half; i += ROPE_THREADS) {
@@ -475,7 +477,7 @@ static cudaError_t launch_rope(const RopeArgs& a, const DeviceInfo& di, cudaStre
                      al(a.kc, a.kc_sp, a.kc_st, a.kc_sh) && al(a.vc, a.vc_sp, a.vc_st, a.vc_sh);
     if (vec) {
         const int units = (a.interleaved ? a.rot / 8 : a.rot / 16) + (a.D - a.rot) / 8;
-        const int jobs = ROPE_THREADS / units * rope_jobs(a.interleaved), heads = a.Hq + 2 * a.Hkv;
+        const int jobs = ROPE_THREADS / units * ROPE_JOBS, heads = a.Hq + 2 * a.Hkv;
         if (heads > jobs) {
             const int grid = std::min(a.T, di.sm_count * (a.interleaved ? 3 : 2));
             if (a.interleaved)
@@ -483,7 +485,7 @@ static cudaError_t launch_rope(const RopeArgs& a, const DeviceInfo& di, cudaStre
             return launch_after(rope_heads_kernel<BF, E4, false>, dim3(grid), ROPE_THREADS, 0, st, a, units);
         }
         // as many tokens as the threads have jobs for, once every block has some
-        const int blocks = di.sm_count * 3;
+        const int blocks = di.sm_count * (a.interleaved ? 3 : 2);
         int toks = std::min(jobs / heads, std::min(ROPE_TOKS, a.T / blocks));
         if (a.rot) toks = std::min(toks, 2 * ROPE_SINES / a.rot);
         toks = std::max(toks, 1);
