@@ -16,16 +16,17 @@
 // with mma.m16n8k16: 8 heads fill one N tile exactly, and the score
 // accumulator becomes the second product's B operand by one 8x8 transpose
 // (movmatrix).  A tcgen05 product needs 64 or 128 rows in M and moves its
-// accumulator through TMEM; here the products take a few percent of the issue
-// slots, so the warp-level instruction with registers is the shorter path.
+// accumulator through TMEM; here the products keep the tensor pipe busy for a
+// quarter of the time at most (E4M3), so the warp-level instruction with its
+// operands in registers is the shorter path.
 //
 // Rounding choices: scores, softmax and sums are FP32.  The second product
 // takes 16-bit operands; p is given to it as hi + lo (two 16-bit values, an
 // error near 2^-17 of p in BF16 and 2^-22 in FP16), because one 16-bit
 // rounding of p would cost as much as rounding the output.  FP16 operands
 // hold 2^14 p (at most 2^15), so that a long tail of keys far below the
-// maximum is kept down to p = 2^-38; l carries the same factor.  E4M3 codes widen to FP16 exactly; a
-// BF16 q then goes to FP16 after a power-of-two scaling of its head's row
+// maximum is kept down to p = 2^-38; l carries the same factor.  E4M3 codes
+// widen to FP16 exactly; a BF16 q then goes to FP16 after a power-of-two scaling of its head's row
 // (the largest element in [2^9, 2^10]), exact for elements within 2^-23 of
 // the row's largest, and smaller ones are off by less than FP32's own sum.
 //

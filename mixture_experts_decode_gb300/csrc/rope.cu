@@ -5,10 +5,11 @@
 // the half layout and (x_{2i}, x_{2i+1}) interleaved; with a = pos * f_i,
 //   (x, y) -> mscale * (x cos a - y sin a,  y cos a + x sin a).
 // The angle is reduced exactly: f_i / 2 pi is taken modulo 1 as a 64-bit
-// fraction F_i of a turn (FP64, once per thread), and pos * F_i wraps modulo
-// 2^64, that is modulo a whole turn, so a position of 2^31 still has its angle
-// to 2^-34 turns, where an FP32 product would be off by radians.  The top 32
-// bits, as a signed fraction of half a turn, go to sincospif.
+// fraction F_i of a turn (FP64, once per block), and pos * F_i wraps modulo
+// 2^64, that is modulo a whole turn: a position of 2^20 has its angle to 2^-33
+// turns, one of 2^31 to 2^-24 (FP64's rounding of F_i), where an FP32 product
+// would be off by radians.  The top 32 bits, as a signed fraction of half a
+// turn, go to sincospif.
 //
 // Bound: HBM, each element in and out once (16384 tokens of 64 + 8 + 8 heads
 // of 128: 671 MB, 106 us, 6.3 TB/s).  One block takes one or a few tokens at a
@@ -28,7 +29,7 @@ namespace moedec {
 
 namespace {
 
-constexpr int ROPE_THREADS = 256;  // at most
+constexpr int ROPE_THREADS = 256;
 
 template <bool BF>
 __device__ __forceinline__ float to_f(uint16_t v) {
