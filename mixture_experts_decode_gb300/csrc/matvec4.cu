@@ -624,19 +624,27 @@ __global__ void __launch_bounds__(MV_WARPS * 32, 2) matvec4_one_kernel(const __g
     cp_async_wait<0>();
 }
 
-// Warps that share K: all eight, or as many as there are steps (a power of
-// two), so that none is idle on short rows.
-static int mv_kw_log(int steps) { return steps >= 8 ? 3 : steps >= 4 ? 2 : steps >= 2 ? 1 : 0; }
+// Warps that share K, as a power of two: as many as there are steps, up to
+// eight, so that none is idle on short rows (28672 x 512: 13.7 -> 4.8 us); four
+// where eight would be idle for an eighth of their steps or more and half the
+// blocks still fill the SMs (14336 x 2304, 8 rows: 17.7 -> 12.4 us; but 1152 x
+// 4736 5.3 -> 7.4).
+static int mv_kw_log(const Matvec4Args& a, const DeviceInfo& di) {
+    const int steps = (a.K + MV_STEP - 1) / MV_STEP;
+    if (steps < 8) return steps >= 4 ? 2 : steps >= 2 ? 1 : 0;
+    const int by_eight = (steps + 7) / 8 * 8, by_four = (steps + 3) / 4 * 4;
+    return by_four <= by_eight / 8 * 7 && a.N >= 32 * di.sm_count ? 2 : 3;
+}
 // Tiles of a block with two row tiles a warp.
-static int mv_tiles2(const Matvec4Args& a) {
-    const int rows = (MV_WARPS >> mv_kw_log((a.K + MV_STEP - 1) / MV_STEP)) * 32;
+static int mv_tiles2(const Matvec4Args& a, const DeviceInfo& di) {
+    const int rows = (MV_WARPS >> mv_kw_log(a, di)) * 32;
     return (a.N + rows - 1) / rows;
 }
 
 // Enough weight rows to repay the splitting of x, whose parts fit shared
 // memory beside the ring.
 static bool one_row(const Matvec4Args& a, const DeviceInfo& di, bool bf) {
-    return a.T == 1 && mv_tiles2(a) >= 2 * di.sm_count && (int64_t)a.K * (bf ? 2 : 3) <= 65536;
+    return a.T == 1 && mv_tiles2(a, di) >= 2 * di.sm_count && (int64_t)a.K * (bf ? 2 : 3) <= 65536;
 }
 
 template <int MT, int GB, bool BF>
@@ -647,7 +655,7 @@ static cudaError_t launch_mv_one(const Matvec4Args& a, const DeviceInfo& di, cud
     static SmemOnce once;
     const cudaError_t e = once.set(reinterpret_cast<const void*>(kernel), (int)fixed + 65536);
     if (e != cudaSuccess) return e;
-    const int steps = (a.K + MV_STEP - 1) / MV_STEP, kw_log = mv_kw_log(steps);
+    const int steps = (a.K + MV_STEP - 1) / MV_STEP, kw_log = mv_kw_log(a, di);
     const int tile_rows = (MV_WARPS >> kw_log) * MT * 16;
     const int tiles = (a.N + tile_rows - 1) / tile_rows;
     const int per_sm = std::max(1, std::min(2, (int)((size_t)di.smem_per_sm / (smem + 1024))));
@@ -669,7 +677,7 @@ static cudaError_t launch_mv(const Matvec4Args& a, const DeviceInfo& di, cudaStr
     static SmemOnce once;
     cudaError_t e = once.set(reinterpret_cast<const void*>(kernel), (int)smem);
     if (e != cudaSuccess) return e;
-    const int steps = (a.K + MV_STEP - 1) / MV_STEP, kw_log = mv_kw_log(steps);
+    const int steps = (a.K + MV_STEP - 1) / MV_STEP, kw_log = mv_kw_log(a, di);
     const int tile_rows = (MV_WARPS >> kw_log) * MT * 16;
     const int tiles = (a.N + tile_rows - 1) / tile_rows;
     const int per_sm = std::max(1, std::min(3, (int)((size_t)di.smem_per_sm / (smem + 1024))));
@@ -686,7 +694,7 @@ static cudaError_t launch_mv_group(const Matvec4Args& a, const DeviceInfo& di, c
 
 template <bool BF>
 static cudaError_t launch_mv_rows(const Matvec4Args& a, const DeviceInfo& di, cudaStream_t st) {
-    const bool two = mv_tiles2(a) >= di.sm_count;  // two row tiles a warp once they fill the SMs
+    const bool two = mv_tiles2(a, di) >= di.sm_count;  // two row tiles a warp once they fill the SMs
     if (one_row(a, di, BF)) return launch_mv_one_group<2, BF>(a, di, st);
     if (a.T <= 8) return two ? launch_mv_group<2, 1, BF>(a, di, st) : launch_mv_group<1, 1, BF>(a, di, st);
     if (a.T <= 16) return two ? launch_mv_group<2, 2, BF>(a, di, st) : launch_mv_group<1, 2, BF>(a, di, st);

@@ -381,3 +381,12 @@ def test_norm_rows_between_vectors(cuda_device, T, d, gate):
     want, x = moe.norm_residual(y[:T * d].view(T, d), r, pre=moe.Norm())
     moe.norm_residual(y[:T * d].view(T, d), r, pre=moe.Norm(), resid_out=r)
     assert torch.equal(r, want)
+
+
+@pytest.mark.parametrize("N,K,group", [(77900, 256, 128), (77825, 32, 32), (38950, 512, 64), (38920, 416, 32), (19470, 1024, 128),
+                                       (19457, 800, 32), (19500, 2304, 64), (9730, 2048, 32), (9731, 6016, 128)])
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_matvec_one_row_short_and_uneven_depths(cuda_device, N, K, group, dtype):
+    """Block tiles of several warps' rows (fewer than eight steps of K, or steps that do not divide by eight)."""
+    mv_check(cuda_device, 1, N, K, group, dtype, True, seed=K, what=f"{N}x{K}")
+    mv_check(cuda_device, 3, N // 4 + 1, K, group, dtype, False, seed=K, what=f"3 rows, {N // 4 + 1}x{K}")
