@@ -307,7 +307,10 @@ __global__ void __launch_bounds__(ROPE_THREADS, INTER ? 3 : 2)
     constexpr int CES = E4 ? 1 : 2;
     __shared__ __align__(16) float2 sm_cs[2][ROPE_SINES];
     __shared__ uint64_t sm_turns[MOE_ROPE_MAX_DIM / 2];
-    __shared__ int64_t sm_row[2][ROPE_TOKS][2];  // offsets of the token's row in the K and V caches; -1: none
+    // Offsets of the token's row in the K and V caches; -1: none.  Three places:
+    // a round's are read after its barrier, the next round's are written before
+    // it, and the round after that is written while slower warps still read.
+    __shared__ int64_t sm_row[3][ROPE_TOKS][2];
     __shared__ int sm_pos[2][ROPE_TOKS];
     const int tid = threadIdx.x;
     const int half = a.rot / 2;
@@ -320,7 +323,7 @@ __global__ void __launch_bounds__(ROPE_THREADS, INTER ? 3 : 2)
 
     const int64_t stride = (int64_t)gridDim.x * toks;
     // a token's position and slot: loaded two rounds ahead, put into shared memory one ahead
-    auto put_token = [&](int b, int64_t tok, int position, int64_t slot) {
+    auto put_token = [&](int b, int at, int64_t tok, int position, int64_t slot) {
         int64_t kr = -1, vr = -1;
         if (tok < a.T && slot >= 0) {
             const int64_t page = slot / a.page, row = slot - page * a.page;
@@ -331,8 +334,8 @@ __global__ void __launch_bounds__(ROPE_THREADS, INTER ? 3 : 2)
                 atomicOr(a.err, MOE_DEVERR_PAGE);
             }
         }
-        sm_row[b][tid][0] = kr;
-        sm_row[b][tid][1] = vr;
+        sm_row[at][tid][0] = kr;
+        sm_row[at][tid][1] = vr;
         sm_pos[b][tid] = position;
     };
     int position = 0;
@@ -346,7 +349,7 @@ __global__ void __launch_bounds__(ROPE_THREADS, INTER ? 3 : 2)
     const int64_t first = (int64_t)blockIdx.x * toks;
     if (tid < toks) {
         load_token(first + tid);
-        put_token(0, first + tid, position, slot);
+        put_token(0, 0, first + tid, position, slot);
         load_token(first + stride + tid);
     }
     const uint16_t* src[JOBS];
@@ -378,8 +381,9 @@ __global__ void __launch_bounds__(ROPE_THREADS, INTER ? 3 : 2)
     rope_turns(a, sm_turns);
     __syncthreads();
 
-    int buf = 0;
+    int buf = 0, at = 0;  // places of this round's sines and positions, and of its rows
     for (int64_t t0 = first; t0 < a.T; t0 += stride, buf ^= 1) {
+        const int at_next = at == 2 ? 0 : at + 1;
         P place[JOBS];
 #pragma unroll
         for (int j = 0; j < JOBS; ++j)
@@ -395,10 +399,16 @@ __global__ void __launch_bounds__(ROPE_THREADS, INTER ? 3 : 2)
                 rope_sine(sm_pos[buf][tl], sm_turns[pair], a.mscale);
         }
         if (tid < toks) {
-            put_token(buf ^ 1, t0 + stride + tid, position, slot);
+            put_token(buf ^ 1, at_next, t0 + stride + tid, position, slot);
             load_token(t0 + 2 * stride + tid);
         }
-        __syncthreads();  // (the other buffer's readers are past: one round apart)
+        // One barrier a round.  Sines: written before it and read after it, so
+        // the readers of this place, two rounds back, are past the barrier
+        // between.  Positions: read before it, written for the next round
+        // before it, in the place that was read before the last one.  Rows:
+        // written for the next round before it, in the place that was read
+        // two rounds back, before the last barrier.
+        __syncthreads();
 #pragma unroll
         for (int j = 0; j < JOBS; ++j) {
             if (kind[j] != 3 && t0 + tokl[j] < a.T) {
@@ -420,12 +430,13 @@ __global__ void __launch_bounds__(ROPE_THREADS, INTER ? 3 : 2)
                     put_half<BF>(reinterpret_cast<uint16_t*>(dst[j]), f, e, two, half);
                     dst[j] += qo_step;
                 } else {
-                    const int64_t row = sm_row[buf][tokl[j]][kind[j] - 1];
+                    const int64_t row = sm_row[at][tokl[j]][kind[j] - 1];
                     if (row >= 0) put_cache<BF, E4>(dst[j] + row * CES, f, e, two, half, kind[j] == 1 ? a.k_inv : a.v_inv);
                 }
             }
             src[j] += src_step[j];
         }
+        at = at_next;
     }
 }
 
