@@ -55,3 +55,16 @@ def test_prompt_equals_its_slices(cuda_device, T, Hq, Hkv, D, rot, interleaved, 
 def test_prompt_of_few_heads(cuda_device, T, Hq, Hkv, D, rot, interleaved, cache):
     rope_check(pad_some(rope_case(cuda_device, T, Hq, Hkv, D, rot, dtype=HF, cache=cache, seed=T), T), interleaved,
                what=f"T={T}")
+
+
+# More heads than a block's threads have jobs for (four for each of 256 / units
+# groups): heads are then taken one token at a time.  Head counts that no group
+# count divides, whole and partial rotation, several tokens a block.
+@pytest.mark.parametrize("T,Hq,Hkv,D,rot,interleaved", [
+    (1000, 61, 5, 256, 256, False), (1900, 71, 3, 128, 32, False), (700, 131, 7, 128, 128, False),
+    (1, 67, 3, 128, 128, True), (2001, 67, 3, 128, 128, True), (1500, 129, 4, 64, 16, True), (900, 64, 8, 128, 64, True),
+    (500, 127, 127, 128, 128, False)])
+@pytest.mark.parametrize("dtype,cache", [(BF, BF), (HF, HF), (BF, E4), (HF, E4)])
+def test_prompt_of_many_heads(cuda_device, T, Hq, Hkv, D, rot, interleaved, dtype, cache):
+    c = pad_some(rope_case(cuda_device, T, Hq, Hkv, D, rot, dtype=dtype, cache=cache, seed=T + Hq), T)
+    rope_check(c, interleaved, mscale=1.25, what=f"T={T} heads={Hq}/{Hkv}")
