@@ -11,6 +11,13 @@ __device__ __forceinline__ void cp_async_16_zfill(void* smem, const void* gmem, 
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(a), "l"(gmem), "r"(src_bytes) : "memory");
 }
 
+// 16 bytes by an ordinary load.
+__device__ __forceinline__ uint4 ld_128(const void* p) {
+    uint4 r;
+    asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p) : "memory");
+    return r;
+}
+
 // The warp's index in its block as a value the compiler knows to be the same
 // in all lanes: branches on it do not split the warp.
 __device__ __forceinline__ int warp_index() { return __shfl_sync(FULL_MASK, (int)threadIdx.x >> 5, 0); }
@@ -21,7 +28,10 @@ __device__ __forceinline__ int warp_index() { return __shfl_sync(FULL_MASK, (int
 // completed and its writes are visible.  A step is a chain of kernels of a few
 // microseconds; this takes about 2 us off the gap between two calls (attention
 // of 777 keys in a loop of calls 12.4 -> 9.9 us, 4-bit 16 x 4096 -> 7169 14.4
-// -> 12.3 us).
+// -> 12.3 us).  A block of such a kernel may be resident while its inputs are
+// still being written, so they are not read-only for the kernel's duration and
+// are read by ordinary loads, never through the non-coherent path
+// (ld.global.nc, __ldg): the wait orders the writes before the former only.
 __device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 template <class... Params, class... Args>

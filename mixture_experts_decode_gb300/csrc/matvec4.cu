@@ -195,17 +195,17 @@ __global__ void __launch_bounds__(MV_WARPS * 32, mv_blocks(NT)) matvec4_kernel(c
             const int64_t at = row * kg + gi0;
             const uint16_t* sp = static_cast<const uint16_t*>(a.scales) + at;
             if constexpr (NGS == 8) {
-                const uint4 v = __ldg(reinterpret_cast<const uint4*>(sp));
+                const uint4 v = *reinterpret_cast<const uint4*>(sp);
                 sc[0] = v.x, sc[1] = v.y, sc[2] = v.z, sc[3] = v.w;
-                const uint2 z = a.zeros ? __ldg(reinterpret_cast<const uint2*>(a.zeros + at)) : make_uint2(0x08080808u, 0x08080808u);
+                const uint2 z = a.zeros ? *reinterpret_cast<const uint2*>(a.zeros + at) : make_uint2(0x08080808u, 0x08080808u);
                 zb[0] = z.x, zb[1] = z.y;
             } else if constexpr (NGS == 4) {
-                const uint2 v = __ldg(reinterpret_cast<const uint2*>(sp));
+                const uint2 v = *reinterpret_cast<const uint2*>(sp);
                 sc[0] = v.x, sc[1] = v.y;
-                zb[0] = a.zeros ? __ldg(reinterpret_cast<const uint32_t*>(a.zeros + at)) : 0x08080808u;
+                zb[0] = a.zeros ? *reinterpret_cast<const uint32_t*>(a.zeros + at) : 0x08080808u;
             } else {
-                sc[0] = __ldg(reinterpret_cast<const uint32_t*>(sp));
-                zb[0] = a.zeros ? __ldg(reinterpret_cast<const uint16_t*>(a.zeros + at)) : 0x0808u;
+                sc[0] = *reinterpret_cast<const uint32_t*>(sp);
+                zb[0] = a.zeros ? *reinterpret_cast<const uint16_t*>(a.zeros + at) : 0x0808u;
             }
         } else {  // one by one; groups beyond K get scale 0
 #pragma unroll
@@ -213,10 +213,10 @@ __global__ void __launch_bounds__(MV_WARPS * 32, mv_blocks(NT)) matvec4_kernel(c
 #pragma unroll
             for (int i = 0; i < NGS; ++i) {
                 const int gi = min(gi0 + i, kg - 1);
-                uint32_t v = __ldg(static_cast<const uint16_t*>(a.scales) + row * kg + gi);
+                uint32_t v = static_cast<const uint16_t*>(a.scales)[row * kg + gi];
                 v = gi0 + i < kg ? v : 0u;
                 sc[i / 2] = i % 2 ? sc[i / 2] | v << 16 : v;
-                zb[i / 4] |= (a.zeros ? (uint32_t)__ldg(a.zeros + row * kg + gi) : 8u) << (8 * (i % 4));
+                zb[i / 4] |= (a.zeros ? (uint32_t)a.zeros[row * kg + gi] : 8u) << (8 * (i % 4));
             }
         }
         if (++sz_step == per_warp) {
@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(MV_WARPS * 32, mv_blocks(NT)) matvec4_kernel(c
                 for (int i = 0; i < W; ++i)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
-                        xv[i][nt] = ld_cached_128(xrow[nt] + min(step * MV_STEP + (blk0 + i) * 32 + 8 * t, a.K - 8));
+                        xv[i][nt] = ld_128(xrow[nt] + min(step * MV_STEP + (blk0 + i) * 32 + 8 * t, a.K - 8));
             };
             load_x(0);
             cp_async_wait<NST - 2>();
@@ -450,17 +450,17 @@ __global__ void __launch_bounds__(MV_WARPS * 32, 2) matvec4_one_kernel(const __g
             const int64_t at = row * kg + gi0;
             const uint16_t* sp = static_cast<const uint16_t*>(a.scales) + at;
             if constexpr (NGS == 8) {
-                const uint4 v = __ldg(reinterpret_cast<const uint4*>(sp));
+                const uint4 v = *reinterpret_cast<const uint4*>(sp);
                 sc[0] = v.x, sc[1] = v.y, sc[2] = v.z, sc[3] = v.w;
-                const uint2 z = a.zeros ? __ldg(reinterpret_cast<const uint2*>(a.zeros + at)) : make_uint2(0x08080808u, 0x08080808u);
+                const uint2 z = a.zeros ? *reinterpret_cast<const uint2*>(a.zeros + at) : make_uint2(0x08080808u, 0x08080808u);
                 zb[0] = z.x, zb[1] = z.y;
             } else if constexpr (NGS == 4) {
-                const uint2 v = __ldg(reinterpret_cast<const uint2*>(sp));
+                const uint2 v = *reinterpret_cast<const uint2*>(sp);
                 sc[0] = v.x, sc[1] = v.y;
-                zb[0] = a.zeros ? __ldg(reinterpret_cast<const uint32_t*>(a.zeros + at)) : 0x08080808u;
+                zb[0] = a.zeros ? *reinterpret_cast<const uint32_t*>(a.zeros + at) : 0x08080808u;
             } else {
-                sc[0] = __ldg(reinterpret_cast<const uint32_t*>(sp));
-                zb[0] = a.zeros ? __ldg(reinterpret_cast<const uint16_t*>(a.zeros + at)) : 0x0808u;
+                sc[0] = *reinterpret_cast<const uint32_t*>(sp);
+                zb[0] = a.zeros ? *reinterpret_cast<const uint16_t*>(a.zeros + at) : 0x0808u;
             }
         } else {  // one by one; groups beyond K get scale 0
 #pragma unroll
@@ -468,10 +468,10 @@ __global__ void __launch_bounds__(MV_WARPS * 32, 2) matvec4_one_kernel(const __g
 #pragma unroll
             for (int i = 0; i < NGS; ++i) {
                 const int gi = min(gi0 + i, kg - 1);
-                uint32_t v = __ldg(static_cast<const uint16_t*>(a.scales) + row * kg + gi);
+                uint32_t v = static_cast<const uint16_t*>(a.scales)[row * kg + gi];
                 v = gi0 + i < kg ? v : 0u;
                 sc[i / 2] = i % 2 ? sc[i / 2] | v << 16 : v;
-                zb[i / 4] |= (a.zeros ? (uint32_t)__ldg(a.zeros + row * kg + gi) : 8u) << (8 * (i % 4));
+                zb[i / 4] |= (a.zeros ? (uint32_t)a.zeros[row * kg + gi] : 8u) << (8 * (i % 4));
             }
         }
         if (++sz_step == per_warp) {
@@ -490,7 +490,7 @@ __global__ void __launch_bounds__(MV_WARPS * 32, 2) matvec4_one_kernel(const __g
     __syncthreads();
     for (int i0 = 0; i0 < vecs; i0 += MV_WARPS * 32) {
         float f[8], m = 0.f;
-        x_floats<BF>(ld_cached_128(static_cast<const uint16_t*>(a.x) + min(i0 + tid, vecs - 1) * 8), f);
+        x_floats<BF>(ld_128(static_cast<const uint16_t*>(a.x) + min(i0 + tid, vecs - 1) * 8), f);
 #pragma unroll
         for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(f[j]));
         // (the bits of non-negative floats compare as they do)
@@ -502,7 +502,7 @@ __global__ void __launch_bounds__(MV_WARPS * 32, 2) matvec4_one_kernel(const __g
     const float fwd = __uint_as_float((uint32_t)(127 + 7 - exponent) << 23);
     for (int i = tid; i < vecs; i += MV_WARPS * 32) {
         float f[8];
-        x_floats<BF>(ld_cached_128(static_cast<const uint16_t*>(a.x) + i * 8), f);
+        x_floats<BF>(ld_128(static_cast<const uint16_t*>(a.x) + i * 8), f);
 #pragma unroll
         for (int j = 0; j < 8; ++j) f[j] *= fwd;
         uint8_t* to = sm_x + ((i >> 2) * PARTS * 4 + (i & 3)) * 8;
