@@ -504,15 +504,21 @@ int moe_norm_residual(const void* y, int64_t y_stride, int T, int d, int dtype, 
  * moe_matvec4 -- products of few activation rows with 4-bit weights:
  *     y[t,n] = sum_k (c[n,k] - z[n,k/group]) * s[n,k/group] * x[t,k]
  * Arguments
- *   x       [T][K] of dtype MOE_BF16 / MOE_F16, finite, row stride x_stride
- *           (a multiple of 8), 16-byte aligned.
+ *   x       [T][K] of dtype MOE_BF16 / MOE_F16, row stride x_stride (a multiple
+ *           of 8), 16-byte aligned.  A row that holds an infinity or a NaN, or
+ *           whose sum of |x| over some group, times 16 + the largest code or
+ *           zero point, passes FP32's range, gives no reliable finite value:
+ *           with an infinity or a NaN, none at all.
  *   codes   [N][K/2] bytes, two unsigned codes 0..15 each, the lower k in the
  *           low nibble; 16-byte aligned.
  *   scales  [N][K/group] of dtype.  zeros uint8 [N][K/group], or NULL for 8.
  *   group   32, 64 or 128; K a multiple of group.
  *   y       [T][N] of dtype, row stride y_stride.
  *   T <= MOE_MATVEC_MAX_TOKENS (the codes are read once per 32 rows of x), K <= 2^24.
- * Products are exact, sums FP32, the weights are not rounded; y is rounded once.
+ * The weights are not rounded, sums are FP32, y is rounded once.  Products are
+ * exact, but with one row of x on many weight rows (about 9700 where K is 2048
+ * or more) elements of x are held to 2^-25 of the largest element of their
+ * group, below the rounding of an FP32 sum that has that element in it.
  */
 int moe_matvec4(const void* x, int64_t x_stride, int T, int K, int dtype, const uint8_t* codes, const void* scales,
                 const uint8_t* zeros, int N, int group, void* y, int64_t y_stride, moe_stream_t stream);

@@ -10,12 +10,13 @@
 //   s * ( sum (16 + c) x - (16 + z) sum x ),
 // products exact, sums FP32.  The offset makes the two sums about five times
 // larger than their difference for spread codes, which costs two or three of
-// FP32's bits; the weights themselves are never rounded.
+// FP32's bits; the weights themselves are never rounded.  (One row of x on many
+// weight rows: products of 8-bit parts of x, to the same accuracy, below.)
 //
 // Bound: HBM on the codes for few rows of x (half a byte per weight; scales
 // and zero points add 3 bytes per group), then instruction issue: about 25
 // instructions per eight codes of a thread, all told (28672 x 8192, one row:
-// 129 MB in 33 us, 3.9 TB/s, 2.5 instructions per cycle of 4).  A warp takes 16 * MT weight rows
+// 129 MB in 34.7 us, 3.7 TB/s, 2.5 instructions per cycle of 4).  A warp takes 16 * MT weight rows
 // (M of mma.m16n8k16) by 256 k per step through its own cp.async ring, eight
 // rows of x are the N side, and the eight warps of a block split K, so a
 // single token still has every warp of the GPU loading; their sums meet in
@@ -100,8 +101,8 @@ __device__ __forceinline__ uint32_t e4m3_four(float a, float b, float c, float d
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
     return (uint32_t)lo | (uint32_t)hi << 16;
 }
-// Exponent e of a row's largest element, 2^e <= amax < 2^(e + 1), within what
-// keeps 2^(7 - e) and its inverse normal numbers.
+// Exponent e of a group's largest element, 2^e <= amax < 2^(e + 1), within what
+// keeps 2^(7 - e) and its inverse normal numbers (128 for an infinity or NaN).
 __device__ __forceinline__ int x_exponent(uint32_t amax) { return max((int)(amax >> 23) - 127, -112); }
 
 __device__ __forceinline__ void e4m3_mma(float (&c)[4], const uint32_t (&a)[4], uint2 b, bool first) {
@@ -115,6 +116,7 @@ __device__ __forceinline__ void e4m3_mma(float (&c)[4], const uint32_t (&a)[4], 
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b.x), "r"(b.y));
 }
 constexpr int MV_ONE_STAGES = 2;
+constexpr int MV_PARTS = 3;
 
 }  // namespace
 
@@ -373,30 +375,37 @@ __global__ void __launch_bounds__(MV_WARPS * 32, mv_blocks(NT)) matvec4_kernel(c
 //
 // An unsigned code 0..15 in a byte is the E4M3 number code * 2^-9 (the
 // subnormals and the first binade are one linear scale), so four codes of a
-// word become an operand register by one AND.  x is scaled by a power of two
-// (its largest element to [2^7, 2^8)) and split, when the block starts, into
-// two (BF16) or three (FP16) E4M3 parts of four bits each,
-// x = p0 + p1 / 16 (+ p2 / 256): exact for elements down to 2^-13 of the
-// largest, within 2^-22 of the largest below that.  The parts are columns of
+// word become an operand register by one AND.  x is scaled, group by group, by
+// a power of two (the group's largest element to [2^7, 2^8)) and split, when
+// the block starts, into three E4M3 parts of four bits each,
+// x = p0 + p1 / 16 + p2 / 256: exact for elements down to 2^-14 (FP16) or
+// 2^-17 (BF16) of the group's largest, and off by at most 2^-18 where the
+// largest is 2^7, that is 2^-25 of it, below that -- less than the half step of
+// 2^-24 by which an FP32 sum of the group with that element in it is rounded.  (Relative to the whole
+// row's largest, an outlier would cost other groups their bits, also for the
+// weight rows whose code at the outlier is the zero point.)  An infinity or a
+// NaN makes its group's factor NaN, and so every output.  The parts are columns of
 // the N side, and the products are added in FP32 by mma.m16n8k32 (checked:
 // 24-bit sums, no shorter accumulator).
-// Taken from two row tiles per block slot on: 28672 x 8192 in 32.9 us against
-// 43.4 with 16-bit products, 14336 x 4096 in 12.9 against 14.7; below that the
+// Taken from two row tiles per block slot on: 28672 x 8192 in 34.7 us against
+// 43.9 with 16-bit products, 14336 x 4096 in 13.0 against 14.7; below that the
 // splitting of x costs more (4864 x 1024, 5 rows: 7.7 against 4.5), and more
 // rows fill more columns with parts (14336 x 4096, 4 rows: 18.5 against 14.7).
+// One block per SM from K of about 15400 on still wins while the parts fit 64
+// KB (20000 x 16384: 60.5 us against 64.5, x 20480: 75.2 against 79.7).
 template <int MT, int GB, bool BF>
 __global__ void __launch_bounds__(MV_WARPS * 32, 2) matvec4_one_kernel(const __grid_constant__ Matvec4Args a, int tiles, int steps, int kw_log) {
     constexpr int NST = MV_ONE_STAGES;
     constexpr int STAGE = MT * 16 * MV_ROW;
     constexpr int NGS = 8 / GB;              // groups of a step
-    constexpr int PARTS = BF ? 2 : 3;
+    constexpr int PARTS = MV_PARTS;
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 31, warp = warp_index();
     const int g = lane >> 2, t = lane & 3;
     uint8_t* ring = smem + warp * NST * STAGE;
     float* sm_sum = reinterpret_cast<float*>(smem + MV_WARPS * NST * STAGE);  // [warps][MT][16][2]
-    uint32_t* sm_amax = reinterpret_cast<uint32_t*>(sm_sum + MV_WARPS * MT * 32);  // FP32 bits
-    uint8_t* sm_x = reinterpret_cast<uint8_t*>(sm_amax + 4);  // [K / 32][PARTS][4][8]
+    uint8_t* sm_x = reinterpret_cast<uint8_t*>(sm_sum + MV_WARPS * MT * 32);  // [K / 32][PARTS][4][8]
+    float* sm_unit = reinterpret_cast<float*>(sm_x + a.K * PARTS);            // [per_warp * warps][NGS] what a group's parts count
     after_previous();
     const int kg = a.K / a.group;
     // 2^kw_log warps share K (step = i * that + kw), the others take further rows
@@ -484,41 +493,42 @@ __global__ void __launch_bounds__(MV_WARPS * 32, 2) matvec4_one_kernel(const __g
     fetch_sz();
 
     // x in parts, while the first codes are on their way: the k of a word's
-    // low nibbles (0, 2, 4, 6), then of its high nibbles
+    // low nibbles (0, 2, 4, 6), then of its high nibbles.  A group's vectors
+    // lie in 4 * GB neighbouring lanes; those beyond K are whole groups, which
+    // work on the last vector and store nothing.
     const int vecs = a.K / 8;
-    if (tid == 0) *sm_amax = 0;
-    __syncthreads();
     for (int i0 = 0; i0 < vecs; i0 += MV_WARPS * 32) {
-        float f[8], m = 0.f;
-        x_floats<BF>(ld_128(static_cast<const uint16_t*>(a.x) + min(i0 + tid, vecs - 1) * 8), f);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(f[j]));
-        // (the bits of non-negative floats compare as they do)
-        const uint32_t most = __reduce_max_sync(FULL_MASK, __float_as_uint(m));
-        if (lane == 0) atomicMax(sm_amax, most);
-    }
-    __syncthreads();
-    const int exponent = x_exponent(*sm_amax);
-    const float fwd = __uint_as_float((uint32_t)(127 + 7 - exponent) << 23);
-    for (int i = tid; i < vecs; i += MV_WARPS * 32) {
+        const int i = i0 + tid;
         float f[8];
-        x_floats<BF>(ld_128(static_cast<const uint16_t*>(a.x) + i * 8), f);
+        x_floats<BF>(ld_128(static_cast<const uint16_t*>(a.x) + min(i, vecs - 1) * 8), f);
+        uint32_t most = 0;  // (the bits of non-negative floats compare as they do, NaN above all)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] *= fwd;
-        uint8_t* to = sm_x + ((i >> 2) * PARTS * 4 + (i & 3)) * 8;
+        for (int j = 0; j < 8; ++j) most = max(most, __float_as_uint(f[j]) & 0x7fffffffu);
 #pragma unroll
-        for (int p = 0; p < PARTS; ++p, to += 32) {
-            const uint32_t lo = e4m3_four(f[0], f[2], f[4], f[6]), hi = e4m3_four(f[1], f[3], f[5], f[7]);
-            *reinterpret_cast<uint2*>(to) = make_uint2(lo, hi);
-            if (p + 1 < PARTS) {  // what is left, times 16 (exact)
-                float2 u, v;
-                e4m3x4_to_float(lo, u, v);
-                f[0] = (f[0] - u.x) * 16.f, f[2] = (f[2] - u.y) * 16.f, f[4] = (f[4] - v.x) * 16.f, f[6] = (f[6] - v.y) * 16.f;
-                e4m3x4_to_float(hi, u, v);
-                f[1] = (f[1] - u.x) * 16.f, f[3] = (f[3] - u.y) * 16.f, f[5] = (f[5] - v.x) * 16.f, f[7] = (f[7] - v.y) * 16.f;
+        for (int o = 1; o < 4 * GB; o <<= 1) most = max(most, __shfl_xor_sync(FULL_MASK, most, o));
+        const int exponent = x_exponent(most);
+        const float fwd = __uint_as_float((uint32_t)(127 + 7 - exponent) << 23);
+        if (i < vecs) {
+            if (i % (4 * GB) == 0)
+                sm_unit[i / (4 * GB)] = __uint_as_float(most >= 0x7f800000u ? 0x7fc00000u : (uint32_t)(127 - 7 + exponent) << 23);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] *= fwd;
+            uint8_t* to = sm_x + ((i >> 2) * PARTS * 4 + (i & 3)) * 8;
+#pragma unroll
+            for (int p = 0; p < PARTS; ++p, to += 32) {
+                const uint32_t lo = e4m3_four(f[0], f[2], f[4], f[6]), hi = e4m3_four(f[1], f[3], f[5], f[7]);
+                *reinterpret_cast<uint2*>(to) = make_uint2(lo, hi);
+                if (p + 1 < PARTS) {  // what is left, times 16 (exact)
+                    float2 u, v;
+                    e4m3x4_to_float(lo, u, v);
+                    f[0] = (f[0] - u.x) * 16.f, f[2] = (f[2] - u.y) * 16.f, f[4] = (f[4] - v.x) * 16.f, f[6] = (f[6] - v.y) * 16.f;
+                    e4m3x4_to_float(hi, u, v);
+                    f[1] = (f[1] - u.x) * 16.f, f[3] = (f[3] - u.y) * 16.f, f[5] = (f[5] - v.x) * 16.f, f[7] = (f[7] - v.y) * 16.f;
+                }
             }
         }
     }
+    for (int i = kg + tid; i < (per_warp << kw_log) * NGS; i += MV_WARPS * 32) sm_unit[i] = 0.f;  // beyond K
     __syncthreads();
     // The lane's column (the last part again beyond the parts: not stored), and
     // what a lane's two columns count: parts 0 and 1 (t = 0), part 2 (t = 1).
@@ -574,7 +584,9 @@ __global__ void __launch_bounds__(MV_WARPS * 32, 2) matvec4_one_kernel(const __g
                     e4m3_mma(xs, ones, xb, bb == 0);
                 }
                 // the parts together, all in units of 2^-9
-                const float xsum = fmaf(xs[1], c_second, xs[0] * c_first) * (1.f / 512);
+                const float unit = sm_unit[step * NGS + grp];
+                const float u_first = c_first * unit, u_second = c_second * unit;
+                const float xsum = fmaf(xs[1], u_second, xs[0] * u_first) * (1.f / 512);
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -590,7 +602,7 @@ __global__ void __launch_bounds__(MV_WARPS * 32, 2) matvec4_one_kernel(const __g
                             sc = __half2float(hh);
                         }
                         const float zz = __half2float(__ushort_as_half((uint16_t)(v >> 16)));
-                        tot[mt][h] += sc * fmaf(-zz, xsum, fmaf(acc[mt][2 * h + 1], c_second, acc[mt][2 * h] * c_first));
+                        tot[mt][h] += sc * fmaf(-zz, xsum, fmaf(acc[mt][2 * h + 1], u_second, acc[mt][2 * h] * u_first));
                     }
             }
         }
@@ -608,10 +620,9 @@ __global__ void __launch_bounds__(MV_WARPS * 32, 2) matvec4_one_kernel(const __g
             float v = 0.f;
             for (int w = 0; w < kws; ++w) {
                 v += first[w * MT * 32];
-                if (PARTS > 2) v += first[w * MT * 32 + 1];
+                v += first[w * MT * 32 + 1];
             }
-            // codes in units of 2^-9, x times 2^(7 - exponent)
-            v = v * 512.f * __uint_as_float((uint32_t)(127 - 7 + exponent) << 23);
+            v *= 512.f;  // codes in units of 2^-9
             if (row0 + r < a.N) {
                 if (BF)
                     static_cast<__nv_bfloat16*>(a.y)[row0 + r] = __float2bfloat16_rn(v);
@@ -643,17 +654,23 @@ static int mv_tiles2(const Matvec4Args& a, const DeviceInfo& di) {
 
 // Enough weight rows to repay the splitting of x, whose parts fit shared
 // memory beside the ring.
-static bool one_row(const Matvec4Args& a, const DeviceInfo& di, bool bf) {
-    return a.T == 1 && mv_tiles2(a, di) >= 2 * di.sm_count && (int64_t)a.K * (bf ? 2 : 3) <= 65536;
+static bool one_row(const Matvec4Args& a, const DeviceInfo& di) {
+    return a.T == 1 && mv_tiles2(a, di) >= 2 * di.sm_count && a.K * (int64_t)MV_PARTS <= 65536;
+}
+
+// A factor for each group of the steps that the warps take, those beyond K too.
+static size_t mv_unit_bytes(const Matvec4Args& a, const DeviceInfo& di) {
+    const int steps = (a.K + MV_STEP - 1) / MV_STEP, kws = 1 << mv_kw_log(a, di);
+    return (size_t)(steps + kws - 1) / kws * kws * (MV_STEP / a.group) * 4;
 }
 
 template <int MT, int GB, bool BF>
 static cudaError_t launch_mv_one(const Matvec4Args& a, const DeviceInfo& di, cudaStream_t st) {
-    constexpr size_t fixed = (size_t)MV_WARPS * MV_ONE_STAGES * MT * 16 * MV_ROW + (size_t)MV_WARPS * MT * 32 * 4 + 16;
-    const size_t smem = fixed + (size_t)a.K * (BF ? 2 : 3);
+    constexpr size_t fixed = (size_t)MV_WARPS * MV_ONE_STAGES * MT * 16 * MV_ROW + (size_t)MV_WARPS * MT * 32 * 4;
+    const size_t smem = fixed + (size_t)a.K * MV_PARTS + mv_unit_bytes(a, di);
     auto kernel = matvec4_one_kernel<MT, GB, BF>;
     static SmemOnce once;
-    const cudaError_t e = once.set(reinterpret_cast<const void*>(kernel), (int)fixed + 65536);
+    const cudaError_t e = once.set(reinterpret_cast<const void*>(kernel), (int)fixed + 65536 + (65536 / MV_PARTS / MV_STEP + 8) * (MV_STEP / 32) * 4);
     if (e != cudaSuccess) return e;
     const int steps = (a.K + MV_STEP - 1) / MV_STEP, kw_log = mv_kw_log(a, di);
     const int tile_rows = (MV_WARPS >> kw_log) * MT * 16;
@@ -695,7 +712,7 @@ static cudaError_t launch_mv_group(const Matvec4Args& a, const DeviceInfo& di, c
 template <bool BF>
 static cudaError_t launch_mv_rows(const Matvec4Args& a, const DeviceInfo& di, cudaStream_t st) {
     const bool two = mv_tiles2(a, di) >= di.sm_count;  // two row tiles a warp once they fill the SMs
-    if (one_row(a, di, BF)) return launch_mv_one_group<2, BF>(a, di, st);
+    if (one_row(a, di)) return launch_mv_one_group<2, BF>(a, di, st);
     if (a.T <= 8) return two ? launch_mv_group<2, 1, BF>(a, di, st) : launch_mv_group<1, 1, BF>(a, di, st);
     if (a.T <= 16) return two ? launch_mv_group<2, 2, BF>(a, di, st) : launch_mv_group<1, 2, BF>(a, di, st);
     return two ? launch_mv_group<2, 4, BF>(a, di, st) : launch_mv_group<1, 4, BF>(a, di, st);
