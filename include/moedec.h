@@ -60,7 +60,7 @@ enum moe_status {
 #define MOE_DEVERR_TIMEOUT 0x2   /* a kernel's bounded wait gave up (never expected) */
 #define MOE_DEVERR_LOGIT 0x4     /* a router row had fewer than k logits above -inf */
 #define MOE_DEVERR_PAGE 0x8      /* a page id, slot or sequence length beyond its range */
-#define MOE_DEVERR_WORKSPACE 0x10 /* attention counters that were not zero at the call */
+#define MOE_DEVERR_WORKSPACE 0x10 /* attention counters above what a call can leave (some that were not zero) */
 
 /* Limits of the decode kernels (moe_gate_up, moe_down, moe_layer*). */
 #define MOE_MAX_EXPERTS 1024  /* E */
@@ -424,7 +424,10 @@ int moe_mx_requant(const void* in, void* out, int64_t rows, int K, moe_stream_t 
  *              call; every call leaves them zero, so a workspace is cleared
  *              once and kept, for calls of any shape that it is large enough
  *              for.  Calls that overlap in time need workspaces of their own.
- *              Counters found not zero set MOE_DEVERR_WORKSPACE.
+ *              A counter found above what the call adds to it sets
+ *              MOE_DEVERR_WORKSPACE; one that is not zero but below that is not
+ *              noticed, and makes this call's result and later ones wrong: a
+ *              workspace in doubt is cleared again.
  * The result does not depend on timing (no floating-point atomics).
  * Limits: B <= MOE_ATTN_MAX_BATCH, D a multiple of 16 up to MOE_ATTN_MAX_DIM,
  * Hq a multiple of Hkv.

@@ -215,7 +215,8 @@ __device__ __forceinline__ void join_slots(const AttnArgs& a, int n, int heads, 
 
 // True in every thread of the block that is the last of `n` to arrive at the
 // counter, which is then zero again.  What the blocks wrote before is visible
-// to it.
+// to it.  (A counter that began above zero is noticed only where some block
+// finds n or more: a lower value looks like an arrival.)
 __device__ __forceinline__ bool arrive_last(int* counter, int n, int* err, int* flag) {
     __threadfence();
     __syncthreads();
