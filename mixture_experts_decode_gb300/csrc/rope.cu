@@ -230,7 +230,8 @@ __global__ void __launch_bounds__(ROPE_THREADS, INTER ? 3 : 2)
     rope_turns(a, sm_turns);
     __syncthreads();
     int buf = 0;
-    for (int tok = blockIdx.x; tok < a.T; tok += gridDim.x, buf ^= 1) {
+    const uint32_t T = a.T;  // (unsigned: a token number past T may pass 2^31)
+    for (uint32_t tok = blockIdx.x; tok < T; tok += gridDim.x, buf ^= 1) {
         // the first heads are on their way while the sines are made
         P pq[AHEAD], pk, pv;
 #pragma unroll
@@ -241,7 +242,7 @@ __global__ void __launch_bounds__(ROPE_THREADS, INTER ? 3 : 2)
             pv.load(v, two, half);
         }
         rope_token(a, position, slot, sm_turns, sm_tok[buf]);
-        if (tok + gridDim.x < a.T) {
+        if (tok + gridDim.x < T) {
             position = a.positions[tok + gridDim.x];
             slot = a.slots[tok + gridDim.x];
         }
@@ -452,7 +453,8 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_append_any_kernel(const __g
     rope_turns(a, sm_turns);
     __syncthreads();
     int buf = 0;
-    for (int tok = blockIdx.x; tok < a.T; tok += gridDim.x, buf ^= 1) {
+    const uint32_t T = a.T;  // (unsigned: a token number past T may pass 2^31)
+    for (uint32_t tok = blockIdx.x; tok < T; tok += gridDim.x, buf ^= 1) {
         rope_token(a, a.positions[tok], a.slots[tok], sm_turns, sm_tok[buf]);
         __syncthreads();
         for (int i = threadIdx.x; i < total; i += blockDim.x) {
@@ -501,7 +503,7 @@ static cudaError_t launch_rope(const RopeArgs& a, const DeviceInfo& di, cudaStre
         int toks = std::min(jobs / heads, std::min(ROPE_TOKS, a.T / blocks));
         if (a.rot) toks = std::min(toks, 2 * ROPE_SINES / a.rot);
         toks = std::max(toks, 1);
-        const int grid = std::min((a.T + toks - 1) / toks, blocks);
+        const int grid = std::min((a.T - 1) / toks + 1, blocks);
         if (a.interleaved)
             return launch_after(rope_tokens_kernel<BF, E4, true>, dim3(grid), ROPE_THREADS, 0, st, a, units, toks);
         return launch_after(rope_tokens_kernel<BF, E4, false>, dim3(grid), ROPE_THREADS, 0, st, a, units, toks);
