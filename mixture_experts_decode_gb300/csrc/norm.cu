@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(NORM_ANY_WARPS * 32) norm_any_kernel(const Nor
 template <int WARPS, int NV, int VW, bool BF, bool RF>
 static cudaError_t norm_rows(const NormArgs& a, cudaStream_t st) {
     constexpr int rows = WARPS == 1 ? 4 : 1;
-    return launch_after(norm_rows_kernel<WARPS, NV, VW, BF, RF>, dim3((a.T + rows - 1) / rows), WARPS == 1 ? 128 : WARPS * 32, 0,
+    return launch_after(norm_rows_kernel<WARPS, NV, VW, BF, RF>, dim3((a.T - 1) / rows + 1), WARPS == 1 ? 128 : WARPS * 32, 0,
                         st, a);
 }
 

@@ -33,3 +33,16 @@ def test_rope_of_the_most_tokens(cuda_device):
     want = torch.zeros(16, device=cuda_device)
     want[11] = 1
     assert torch.equal(cache.view(-1).float(), 5 * want) and torch.equal(values.view(-1).float(), 3 * want)
+
+
+def test_norm_of_the_most_rows(cuda_device):
+    """d = 1, four rows a block; RMS norm makes each row its sign."""
+    y = torch.ones(MOST, dtype=BF, device=cuda_device)
+    y[-1] = -2
+    y[MOST // 2] = -3
+    out = torch.zeros(MOST + 64, dtype=BF, device=cuda_device)
+    moe.norm_residual(y.view(MOST, 1), pre=moe.Norm(eps=0.0), out=out[32:32 + MOST].view(MOST, 1))
+    torch.cuda.synchronize()
+    assert float(out[32 + MOST - 1]) == -1 and float(out[32 + MOST // 2]) == -1
+    assert int((out[32:32 + MOST] == 1).sum()) == MOST - 2
+    assert not bool(out[:32].any()) and not bool(out[32 + MOST:].any())
