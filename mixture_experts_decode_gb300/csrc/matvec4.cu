@@ -649,7 +649,7 @@ static int mv_kw_log(const Matvec4Args& a, const DeviceInfo& di) {
 // Tiles of a block with two row tiles a warp.
 static int mv_tiles2(const Matvec4Args& a, const DeviceInfo& di) {
     const int rows = (MV_WARPS >> mv_kw_log(a, di)) * 32;
-    return (a.N + rows - 1) / rows;
+    return (a.N - 1) / rows + 1;
 }
 
 // Enough weight rows to repay the splitting of x, whose parts fit shared
@@ -674,7 +674,7 @@ static cudaError_t launch_mv_one(const Matvec4Args& a, const DeviceInfo& di, cud
     if (e != cudaSuccess) return e;
     const int steps = (a.K + MV_STEP - 1) / MV_STEP, kw_log = mv_kw_log(a, di);
     const int tile_rows = (MV_WARPS >> kw_log) * MT * 16;
-    const int tiles = (a.N + tile_rows - 1) / tile_rows;
+    const int tiles = (a.N - 1) / tile_rows + 1;
     const int per_sm = std::max(1, std::min(2, (int)((size_t)di.smem_per_sm / (smem + 1024))));
     return launch_after(kernel, dim3(std::min(tiles, di.sm_count * per_sm)), MV_WARPS * 32, smem, st, a, tiles, steps, kw_log);
 }
@@ -696,7 +696,7 @@ static cudaError_t launch_mv(const Matvec4Args& a, const DeviceInfo& di, cudaStr
     if (e != cudaSuccess) return e;
     const int steps = (a.K + MV_STEP - 1) / MV_STEP, kw_log = mv_kw_log(a, di);
     const int tile_rows = (MV_WARPS >> kw_log) * MT * 16;
-    const int tiles = (a.N + tile_rows - 1) / tile_rows;
+    const int tiles = (a.N - 1) / tile_rows + 1;
     const int per_sm = std::max(1, std::min(3, (int)((size_t)di.smem_per_sm / (smem + 1024))));
     const dim3 grid(std::min(tiles, di.sm_count * per_sm), (a.T + NT * 8 - 1) / (NT * 8));
     return launch_after(kernel, grid, MV_WARPS * 32, smem, st, a, tiles, steps, kw_log);

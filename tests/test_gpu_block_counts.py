@@ -46,3 +46,23 @@ def test_norm_of_the_most_rows(cuda_device):
     assert float(out[32 + MOST - 1]) == -1 and float(out[32 + MOST // 2]) == -1
     assert int((out[32:32 + MOST] == 1).sum()) == MOST - 2
     assert not bool(out[:32].any()) and not bool(out[32 + MOST:].any())
+
+
+@pytest.mark.parametrize("T", [1, 2])
+def test_matvec_of_the_most_weight_rows(cuda_device, T):
+    """K = 32 (34 GB of codes): weight rows of 8 - 8 = 0 except the first, a middle and the last one."""
+    free, _ = torch.cuda.mem_get_info()
+    if free < 80 << 30:
+        pytest.skip("needs 80 GB free")
+    codes = torch.full((MOST, 16), 0x88, dtype=torch.uint8, device=cuda_device)
+    scales = torch.ones(MOST, 1, dtype=HF, device=cuda_device)
+    rows = {0: 1, MOST // 2: 2, MOST - 1: 3}
+    for r, w in rows.items():
+        codes[r] = (8 + w) * 0x11
+    x = torch.full((T, 32), 0.5, dtype=HF, device=cuda_device)
+    y = moe.matvec4(x, moe.W4(codes, scales))
+    torch.cuda.synchronize()
+    for t in range(T):
+        for r, w in rows.items():
+            assert float(y[t, r]) == 16 * w
+        assert int((y[t] != 0).sum()) == len(rows)
