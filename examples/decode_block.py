@@ -37,6 +37,19 @@ def pack4(w: torch.Tensor, group: int) -> moe.W4:
     return moe.W4((code[:, 0::2] | code[:, 1::2] << 4).contiguous(), scale.contiguous(), zero.to(torch.uint8).contiguous())
 
 
+def first_slots(table: torch.Tensor, page: int, pages: int) -> torch.Tensor:
+    """Slot of the first row of each page of a sequence, and behind them one past the cache: a token of a sequence
+    whose pages are full is not written, and the library reports it (device_error) as it does the length."""
+    past = torch.full_like(table[:, :1], pages)
+    return torch.cat((table, past), 1).long() * page
+
+
+def cache_slots(first: torch.Tensor, positions: torch.Tensor, page: int) -> torch.Tensor:
+    """Slot of each sequence's next token."""
+    at = (positions // page).clamp(max=first.shape[1] - 1).long()
+    return torch.gather(first, 1, at[:, None])[:, 0] + positions % page
+
+
 class DecodeBlock:
     """Weights of one block and the pages of its cache for up to `batch` sequences of `capacity` tokens."""
 
@@ -59,6 +72,7 @@ class DecodeBlock:
         self.k_cache = torch.zeros(pages, page, Hkv, D, dtype=BF, device=device)
         self.v_cache = torch.zeros_like(self.k_cache)
         self.table = torch.randperm(pages, generator=g, device=device).view(batch, most).to(torch.int32)
+        self.first = first_slots(self.table, page, pages)
         self.lens = torch.zeros(batch, dtype=torch.int32, device=device)
         self.workspace = moe.attention_workspace(Hq, Hkv, D, device)
 
@@ -66,8 +80,7 @@ class DecodeBlock:
         """One new token for every sequence: resid float32 [B, d] in and out (in place)."""
         B = resid.shape[0]
         positions = self.lens.clone()
-        pages = torch.gather(self.table, 1, (positions // self.page).long()[:, None])[:, 0]
-        slots = pages.long() * self.page + positions % self.page
+        slots = cache_slots(self.first, positions, self.page)
         self.lens += 1
 
         # (the first norm has nothing to add: the residual stream is its input)
