@@ -404,7 +404,10 @@ int moe_mx_requant(const void* in, void* out, int64_t rows, int K, moe_stream_t 
  *   window = 0: every j is visible; window > 0: those with
  *   j >= seq_lens[b] - window or j < sinks.  Tokens that are not visible are
  *   not read.  Scores, softmax and sums are FP32, out is rounded once.  A
- *   sequence of length 0 gets out = 0 and lse = -inf.
+ *   sequence of length 0 gets out = 0 and lse = -inf.  A visible value that is
+ *   infinite or NaN leaves its dim of the outputs of its heads infinite or NaN
+ *   (either: weights are held as two parts, one of which may be 0); a score of
+ *   -inf leaves its key out, one of +inf or NaN makes its head's outputs NaN.
  * Arguments
  *   q          [B][Hq][D] of dtype MOE_BF16 or MOE_F16; strides in elements,
  *              multiples of 8, 16-byte aligned.  out [B][Hq][D] contiguous of
