@@ -446,8 +446,8 @@ int moe_paged_attention(const void* q, int64_t q_stride, int64_t q_head_stride, 
 /*
  * moe_rope_append -- rotary positions for new tokens, and their keys and
  * values into the paged cache.  Per token t and pair i < rot/2, with
- * a = positions[t] * freqs[i] (to 2^-33 turns and 2^-52 of itself, that is to
- * 2^-24 turns at the largest int32 position):
+ * a = positions[t] * freqs[i] (to 2^-26 turns, the last step's FP32; to 2^-23
+ * turns at the largest int32 position):
  *     (x, y) -> mscale * (x cos a - y sin a, y cos a + x sin a)
  *   on the pairs (x_i, x_{i + rot/2}) of a head, or (x_{2i}, x_{2i+1}) when
  *   interleaved; dims from rot on are unchanged.  q is rotated into q_out,

@@ -6,10 +6,10 @@
 //   (x, y) -> mscale * (x cos a - y sin a,  y cos a + x sin a).
 // The angle is reduced exactly: f_i / 2 pi is taken modulo 1 as a 64-bit
 // fraction F_i of a turn (FP64, once per block), and pos * F_i wraps modulo
-// 2^64, that is modulo a whole turn: a position of 2^20 has its angle to 2^-33
-// turns, one of 2^31 to 2^-24 (FP64's rounding of F_i), where an FP32 product
-// would be off by radians.  The top 32 bits, as a signed fraction of half a
-// turn, go to sincospif.
+// 2^64, that is modulo a whole turn: the phase is right to 2^-32 turns at a
+// position of 2^20, to 2^-23 at one of 2^31 (FP64's rounding of F_i), where an
+// FP32 product would be off by radians.  Its top 32 bits, as a signed fraction
+// of half a turn, become a float (2^-26 turns off at most) for sincospif.
 //
 // Bound: HBM, each element in and out once (16384 tokens of 64 + 8 + 8 heads
 // of 128: 671 MB, 106 us, 6.3 TB/s).  One block takes one or a few tokens at a
