@@ -1,9 +1,11 @@
-"""One decoder block, token by token, with every step in this library.
+"""One decoder block, token by token, on this library's operators.
 
 The block around the expert layer: norm, 4-bit projections, head norms, rotary
 positions with the cache append, paged attention, output projection, residual
 and norm, router, expert layer.  A decode step is one CUDA graph: positions,
-page slots and lengths live on the device and move on inside it.
+page slots and lengths live on the device and move on inside it.  Three things
+are torch calls: the router's small projection, the slots and lengths of the new
+tokens, and the conversion of the 32-bit stream for the first norm.
 
     python examples/decode_block.py [--batch 8] [--context 4096] [--steps 64]
 

@@ -391,9 +391,10 @@ int moe_mx_requant(const void* in, void* out, int64_t rows, int K, moe_stream_t 
 
 /*
  * The decode block around the expert layer.  The four entry points below are
- * the other steps of a decoder block, so that a token's whole step stays in
- * this library; the source pages describe the expert layer alone, and these
- * have no counterpart there.  Each is one launch.
+ * the other steps of a decoder block, so that with them a token's step needs
+ * little from elsewhere (the router's projection, the slots of new tokens).
+ * The source pages describe the expert layer alone, and these have no
+ * counterpart there.  Each is one launch.
  *
  * moe_paged_attention -- attention of one new token per sequence over a paged
  * key-value cache.  For sequence b and query head h (key-value head

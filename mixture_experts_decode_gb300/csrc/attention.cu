@@ -38,7 +38,7 @@
 // keeps the result independent of timing.
 //
 // Measured: 4 sequences of 124000 keys, 64 / 8 heads of 128, E4M3 (1.02 GB):
-// 180 to 195 us, 5.2 to 5.7 TB/s; 32 sequences of 0..32768, 32 / 4 heads of
+// 176 to 194 us, 5.3 to 5.8 TB/s; 32 sequences of 0..32768, 32 / 4 heads of
 // 128, BF16 (201 MB): 44 us, 4.5 TB/s; one of 777 keys: 10 us, latency alone.
 #include "block_common.cuh"
 #include "internal.h"

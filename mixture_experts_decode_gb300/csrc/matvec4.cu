@@ -14,7 +14,7 @@
 // weight rows: products of 8-bit parts of x, to the same accuracy, below.)
 //
 // Bound: HBM on the codes for few rows of x (half a byte per weight; scales
-// and zero points add 3 bytes per group), then instruction issue: about 25
+// and zero points add 3 bytes per group), then instruction issue: about 26
 // instructions per eight codes of a thread, all told (28672 x 8192, one row:
 // 129 MB in 34.7 us, 3.7 TB/s, 2.5 instructions per cycle of 4).  A warp takes 16 * MT weight rows
 // (M of mma.m16n8k16) by 256 k per step through its own cp.async ring, eight

@@ -12,7 +12,7 @@
 // of half a turn, become a float (2^-26 turns off at most) for sincospif.
 //
 // Bound: HBM, each element in and out once (16384 tokens of 64 + 8 + 8 heads
-// of 128: 671 MB, 106 us, 6.3 TB/s).  One block takes one or a few tokens at a
+// of 128: 671 MB, 107 us, 6.3 TB/s).  One block takes one or a few tokens at a
 // time (blocks stride over the tokens): their rot/2 sines go to shared memory
 // once and serve every head.  A thread keeps one place within a head (a
 // 16-byte vector, or the two vectors of eight rotated pairs) of the same heads
@@ -295,7 +295,8 @@ __global__ void __launch_bounds__(ROPE_THREADS, INTER ? 3 : 2)
 // are dealt to groups of `units` threads, JOBS to each at most.  A thread's
 // jobs stay the same heads of the block's first, second .. token throughout.
 // (Half layout: four jobs of 32 bytes in two blocks per SM, 66 us at 16384
-// tokens of 32 / 4 heads of 128; two in three blocks 81, three in two 75.)
+// tokens of 32 / 4 heads of 128, 336 MB, 5.1 TB/s; two in three blocks 81, three
+// in two 75.)
 constexpr int ROPE_SINES = 512;  // pairs of a block's tokens at most
 constexpr int ROPE_TOKS = 16;
 constexpr int ROPE_JOBS = 4;
