@@ -478,7 +478,8 @@ int moe_rope_append(const void* q, int64_t q_stride, int64_t q_head_stride, cons
  *   MOE_ROPE_NTK       with base * factor^(rot/(rot-2)) as the base;
  *   MOE_ROPE_BY_PARTS  f * (g + (1-g)/factor), g = clamp((n - beta_slow) /
  *                      (beta_fast - beta_slow), 0, 1), n = original_length *
- *                      f / 2 pi the turns within the original length.
+ *                      f / 2 pi the turns within the original length (a ramp
+ *                      over the turns, not over the index i).
  * rot even and >= 2 (NTK: > 2), base > 0, factor > 0, beta_fast > beta_slow.
  */
 int moe_rope_freqs(int rot, double base, int scaling, double factor, double original_length, double beta_fast,
