@@ -60,6 +60,7 @@ enum moe_status {
 #define MOE_DEVERR_TIMEOUT 0x2   /* a kernel's bounded wait gave up (never expected) */
 #define MOE_DEVERR_LOGIT 0x4     /* a router row had fewer than k logits above -inf */
 #define MOE_DEVERR_PAGE 0x8      /* a page id, slot or sequence length beyond its range */
+#define MOE_DEVERR_POOL 0x20     /* a request refused by moe_plan_pages, or a stack of free pages beyond its range */
 #define MOE_DEVERR_WORKSPACE 0x10 /* attention counters above what a call can leave (some that were not zero) */
 
 /* Limits of the decode kernels (moe_gate_up, moe_down, moe_layer*). */
@@ -73,6 +74,13 @@ enum moe_status {
 #define MOE_ROUTER_MAX_K 32
 #define MOE_ROUTER_SOFTMAX 0
 #define MOE_ROUTER_SIGMOID 1
+
+/* Scores of a group of experts, and limits, of moe_router_grouped_topk. */
+#define MOE_ROUTER_GROUP_MAX 0
+#define MOE_ROUTER_GROUP_TOP2 1
+#define MOE_ROUTER_MAX_GROUPS 32
+/* Limit of moe_plan_pages and moe_release_pages. */
+#define MOE_PAGES_MAX_BATCH 4096
 
 /* Element types of the attention, rotary, norm and 4-bit entry points. */
 #define MOE_BF16 0
@@ -530,6 +538,95 @@ int moe_norm_residual(const void* y, int64_t y_stride, int T, int d, int dtype, 
  */
 int moe_matvec4(const void* x, int64_t x_stride, int T, int K, int dtype, const uint8_t* codes, const void* scales,
                 const uint8_t* zeros, int N, int group, void* y, int64_t y_stride, moe_stream_t stream);
+
+/*
+ * moe_router_grouped_topk -- routing with a bias for balance and groups of
+ * experts.  Per token t, with s the scores of its E logits (MOE_ROUTER_SOFTMAX:
+ * softmax over all E; MOE_ROUTER_SIGMOID: 1 / (1 + exp(-logit))):
+ *     key_e = s_e + bias_e decides, bias NULL standing for zeros;
+ *     the experts, in `groups` runs of E / groups, are first narrowed to the
+ *     top_groups groups worth most (ties: the lower group), a group's worth
+ *     being its largest key (MOE_ROUTER_GROUP_MAX) or the sum of its two
+ *     largest (MOE_ROUTER_GROUP_TOP2);
+ *     topk_ids[t] are the k largest keys within them, in descending order
+ *     (ties: the lower expert index first);
+ *     topk_w[t][j] = scale * s_e, divided by the sum of the k chosen s with
+ *     renorm != 0.  The bias has no part in the weights.
+ *   Keys are compared as real numbers: where FP32 leaves open which of two is
+ *   larger, they are computed again in 64 bits.  Weights are FP32.
+ * Arguments
+ *   logits   [T][E] of dtype MOE_F32, MOE_BF16 or MOE_F16, row stride in
+ *            elements; finite values expected.  An expert whose logit or bias
+ *            is -inf or NaN is never chosen; a row with fewer than k others in
+ *            its chosen groups gets id -1 and weight 0 in the missing places
+ *            and sets MOE_DEVERR_LOGIT.
+ *   bias     float32 [E] or NULL.
+ *   topk_ids int32 [T][k], topk_w float32 [T][k] out.
+ * Limits: 1 <= E <= MOE_ROUTER_MAX_EXPERTS, E a multiple of groups, 1 <=
+ * top_groups <= groups <= MOE_ROUTER_MAX_GROUPS, groups of at least 2 for
+ * MOE_ROUTER_GROUP_TOP2 (where top_groups < groups), 1 <= k <= min(top_groups *
+ * E / groups, MOE_ROUTER_MAX_K).
+ */
+int moe_router_grouped_topk(const void* logits, int64_t stride, int T, int E, int dtype, const float* bias, int k,
+                            int score, int groups, int top_groups, int group_score, int renorm, float scale,
+                            int32_t* topk_ids, float* topk_w, moe_stream_t stream);
+
+/*
+ * moe_plan_pages -- the bookkeeping of a step over a paged cache, on the
+ * device: request b has past_lens[b] tokens in the cache and brings
+ * new_lens[b].  In the order of the requests:
+ *   pages       a request needs ceil((past + new) / page_size) - ceil(past /
+ *               page_size) pages; they are taken from the top of the stack
+ *               free_pages[0 .. *n_free) and entered into its row of
+ *               block_table behind those that it has;
+ *   tokens      its new ones take the next new_lens[b] rows of positions
+ *               (past, past + 1, ...), slots (page * page_size + row, what
+ *               moe_rope_append writes to) and seq_ids (b); starts[b] is the
+ *               first of them, starts[B] the number of all;
+ *   lengths     seq_lens[b] = past + new, *n_free_out what is left.
+ *   Rows from starts[B] to T get position 0, slot -1 and seq_id -1 (padding).
+ *   A request that brings tokens right behind a shared prefix (past_lens[b] ==
+ *   n_shared * page_size, and shares[b] where shares is given) gets the shared
+ *   pages into the first n_shared entries of its row.
+ *   A request is refused where the tokens of all requests up to it pass T, the
+ *   pages of all up to it pass the stack (and it needs one), its row has no
+ *   entry left for it, or a length is negative: it gets no tokens and no
+ *   pages, keeps its length, and MOE_DEVERR_POOL is set; what it asked for
+ *   still counts before those behind it.
+ * Arguments
+ *   past_lens, new_lens int32 [B].  block_table int32 [B][max_pages], row
+ *   stride table_stride, in and out.  free_pages int32 [capacity], n_free
+ *   int32 [1] (beyond 0 .. capacity: cut, and MOE_DEVERR_POOL is set), both
+ *   only read.  shared_pages int32 [n_shared] or NULL; shares uint8 [B]
+ *   (nonzero: shares) or NULL for all.
+ *   positions, seq_ids int32 [T], slots int64 [T], starts int32 [B + 1],
+ *   seq_lens int32 [B], n_free_out int32 [1].  seq_lens may be past_lens and
+ *   n_free_out may be n_free (a call of many tokens is then two launches);
+ *   other arrays do not overlap.
+ * Limits: B <= MOE_PAGES_MAX_BATCH.
+ */
+int moe_plan_pages(const int32_t* past_lens, const int32_t* new_lens, int B, int32_t* block_table, int64_t table_stride,
+                   int max_pages, const int32_t* free_pages, int capacity, const int32_t* n_free, int page_size,
+                   const int32_t* shared_pages, int n_shared, const uint8_t* shares, int T, int32_t* positions,
+                   int64_t* slots, int32_t* seq_ids, int32_t* starts, int32_t* seq_lens, int32_t* n_free_out,
+                   moe_stream_t stream);
+
+/*
+ * moe_release_pages -- the pages of requests that have ended (ended[b] != 0)
+ * back onto the stack, in the order of the requests and of their pages: entries
+ * 0 .. ceil(seq_lens[b] / page_size) of row b, without the first n_shared
+ * where shares[b] (NULL: all).  *n_free_out gets the stack's new height and
+ * seq_lens_out[b] = 0 for the ended, seq_lens[b] for the others.  Pages beyond
+ * the stack's capacity are dropped and set MOE_DEVERR_POOL, as does a length
+ * that is negative or beyond the row (cut).
+ *   seq_lens int32 [B], ended uint8 [B]; the others as in moe_plan_pages, with
+ *   free_pages written from *n_free on.  seq_lens_out may be seq_lens and
+ *   n_free_out may be n_free.
+ */
+int moe_release_pages(const int32_t* block_table, int64_t table_stride, int max_pages, const int32_t* seq_lens, int B,
+                      const uint8_t* ended, int32_t* free_pages, int capacity, const int32_t* n_free, int page_size,
+                      int n_shared, const uint8_t* shares, int32_t* seq_lens_out, int32_t* n_free_out,
+                      moe_stream_t stream);
 
 /*
  * moe_device_error -- synchronise `stream`, then read and clear the sticky

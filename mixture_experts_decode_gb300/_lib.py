@@ -28,7 +28,8 @@ EXPORTS = ("moe_version", "moe_strerror", "moe_gate_up", "moe_down", "moe_layer_
            "moe_copy", "moe_device_error", "moe_router_topk", "moe_mx_requant", "moe_gate_up_fp4",
            "moe_layer_grouped_workspace_bytes", "moe_layer_grouped",
            "moe_down_fp4", "moe_paged_attention_workspace_bytes", "moe_paged_attention", "moe_rope_append",
-           "moe_rope_freqs", "moe_norm_residual", "moe_matvec4")
+           "moe_rope_freqs", "moe_norm_residual", "moe_matvec4", "moe_router_grouped_topk", "moe_plan_pages",
+           "moe_release_pages")
 
 
 class MoEError(RuntimeError):
@@ -101,6 +102,9 @@ def load(path: str = LIB_PATH):
         "moe_rope_freqs": ([I, D, I, D, D, D, D, P], I),
         "moe_norm_residual": ([P, L, I, I, I, P, L, I, NP, P, L, L, I, F, NP, P, P, P], I),
         "moe_matvec4": ([P, L, I, I, I, P, P, P, I, I, P, L, P], I),
+        "moe_router_grouped_topk": ([P, L, I, I, I, P, I, I, I, I, I, I, F, P, P, P], I),
+        "moe_plan_pages": ([P, P, I, P, L, I, P, I, P, I, P, I, P, I, P, P, P, P, P, P, P], I),
+        "moe_release_pages": ([P, L, I, P, I, P, P, I, P, I, I, P, P, P, P], I),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -555,3 +559,67 @@ def matvec4(x, w: W4, y: Optional[torch.Tensor] = None):
     """moe_matvec4: x [T, K] BF16 or FP16 times 4-bit weights -> y [T, N]; the
     group size is K / w.scales.shape[1] (32, 64 or 128)."""
     return (_block_module or _block()).matvec4(x, w, y)
+
+
+# ------------------------------------------------------ the serving step
+
+GROUP_SCORES = {"max": 0, "top2": 1}
+
+
+def router_grouped_topk(logits, k: int, bias: Optional[torch.Tensor] = None, score: str = "sigmoid", groups: int = 1,
+                        top_groups: int = 1, group_score: str = "top2", renormalize: bool = True, scale: float = 1.0,
+                        topk_ids: Optional[torch.Tensor] = None, topk_w: Optional[torch.Tensor] = None):
+    """moe_router_grouped_topk: the k experts of the largest score + bias within
+    the top_groups best of `groups` equal groups.
+
+    logits [T, E] float32, BF16 or FP16 (row stride free); bias float32 [E] or
+    None; score "softmax" or "sigmoid"; group_score "max" (a group's largest
+    key) or "top2" (the sum of its two largest).  Returns (topk_ids int32
+    [T, k], topk_w float32 [T, k]): the scores without the bias, over their sum
+    with renormalize, times scale."""
+    return (_block_module or _block()).router_grouped_topk(logits, k, bias, ROUTER_SCORES[score], groups, top_groups,
+                                                           GROUP_SCORES[group_score], renormalize, scale, topk_ids,
+                                                           topk_w)
+
+
+class PagePlan(NamedTuple):
+    """A step's tokens (positions int32, slots int64, seq_ids int32, each [T]; padding: 0, -1, -1), starts int32
+    [B + 1], and the lengths int32 [B] and free pages int32 [1] after it."""
+    positions: torch.Tensor
+    slots: torch.Tensor
+    seq_ids: torch.Tensor
+    starts: torch.Tensor
+    seq_lens: torch.Tensor
+    n_free: torch.Tensor
+
+
+def plan_pages(past_lens, new_lens, block_table, free_pages, n_free, page_size: int, tokens: int,
+               shared_pages: Optional[torch.Tensor] = None, shares: Optional[torch.Tensor] = None,
+               positions: Optional[torch.Tensor] = None, slots: Optional[torch.Tensor] = None,
+               seq_ids: Optional[torch.Tensor] = None, starts: Optional[torch.Tensor] = None,
+               seq_lens: Optional[torch.Tensor] = None, n_free_out: Optional[torch.Tensor] = None) -> PagePlan:
+    """moe_plan_pages: pages, positions and slots of new_lens int32 [B] tokens
+    behind past_lens int32 [B] ones.
+
+    New pages come from the top of the stack free_pages int32 [capacity] of
+    height n_free int32 [1], and go into block_table int32 [B, max_pages] in
+    place.  tokens: rows of the outputs, at least the new tokens (the rest is
+    padding, which rope_append leaves out).  shared_pages int32 [n]: entered
+    into the rows of requests (of shares, bool [B], where given) that begin
+    right behind them.  seq_lens may be past_lens and n_free_out may be n_free
+    (in place).  A request that does not fit keeps its length, and
+    device_error reports it."""
+    return PagePlan(*(_block_module or _block()).plan_pages(past_lens, new_lens, block_table, free_pages, n_free,
+                                                            page_size, tokens, shared_pages, shares, positions, slots,
+                                                            seq_ids, starts, seq_lens, n_free_out))
+
+
+def release_pages(block_table, seq_lens, ended, free_pages, n_free, page_size: int, shared: int = 0,
+                  shares: Optional[torch.Tensor] = None, seq_lens_out: Optional[torch.Tensor] = None,
+                  n_free_out: Optional[torch.Tensor] = None):
+    """moe_release_pages: the pages of requests with ended (bool [B]) back onto
+    the stack free_pages (written in place from n_free on), without the first
+    `shared` ones where shares (bool [B]; None: all).  Returns (seq_lens,
+    n_free), new tensors or the given ones, which may be the inputs."""
+    return (_block_module or _block()).release_pages(block_table, seq_lens, ended, free_pages, n_free, page_size, shared,
+                                                     shares, seq_lens_out, n_free_out)

@@ -610,6 +610,69 @@ int moe_matvec4(const void* x, int64_t x_stride, int T, int K, int dtype, const 
     return cuda_status(launch_matvec4(a, dtype, (cudaStream_t)stream));
 }
 
+int moe_router_grouped_topk(const void* logits, int64_t stride, int T, int E, int dtype, const float* bias, int k,
+                            int score, int groups, int top_groups, int group_score, int renorm, float scale,
+                            int32_t* topk_ids, float* topk_w, moe_stream_t stream) {
+    if (T < 0 || E < 1 || k < 1 || groups < 1 || top_groups < 1 || (!half_type(dtype) && dtype != MOE_F32)) return MOE_ERR_ARG;
+    if ((score != MOE_ROUTER_SOFTMAX && score != MOE_ROUTER_SIGMOID) || (renorm != 0 && renorm != 1) ||
+        (group_score != MOE_ROUTER_GROUP_MAX && group_score != MOE_ROUTER_GROUP_TOP2))
+        return MOE_ERR_ARG;
+    if (E % groups || top_groups > groups || k > (int64_t)top_groups * (E / groups)) return MOE_ERR_SHAPE;
+    if (group_score == MOE_ROUTER_GROUP_TOP2 && top_groups < groups && E / groups < 2) return MOE_ERR_SHAPE;
+    if (E > MOE_ROUTER_MAX_EXPERTS || k > MOE_ROUTER_MAX_K || groups > MOE_ROUTER_MAX_GROUPS) return MOE_ERR_LIMIT;
+    if (T == 0) return MOE_OK;
+    if (!logits || !topk_ids || !topk_w) return MOE_ERR_ARG;
+    if (!aligned(logits, dtype == MOE_F32 ? 4 : 2) || !aligned(bias, 4) || !aligned(topk_ids, 4) || !aligned(topk_w, 4))
+        return MOE_ERR_ALIGN;
+    const RouterGroupedArgs a{logits, stride, bias, T, E, k, score, groups, top_groups, group_score, renorm, scale, topk_ids,
+                              topk_w, nullptr};
+    return cuda_status(launch_router_grouped(a, dtype, (cudaStream_t)stream));
+}
+
+int moe_plan_pages(const int32_t* past_lens, const int32_t* new_lens, int B, int32_t* block_table, int64_t table_stride,
+                   int max_pages, const int32_t* free_pages, int capacity, const int32_t* n_free, int page_size,
+                   const int32_t* shared_pages, int n_shared, const uint8_t* shares, int T, int32_t* positions,
+                   int64_t* slots, int32_t* seq_ids, int32_t* starts, int32_t* seq_lens, int32_t* n_free_out,
+                   moe_stream_t stream) {
+    if (B < 0 || T < 0 || max_pages < 0 || capacity < 0 || page_size < 1 || n_shared < 0) return MOE_ERR_ARG;
+    if (B > MOE_PAGES_MAX_BATCH) return MOE_ERR_LIMIT;
+    if (B > 0 && (!past_lens || !new_lens || !seq_lens || (max_pages > 0 && !block_table))) return MOE_ERR_ARG;
+    if (!n_free || !n_free_out || !starts || (capacity > 0 && !free_pages) || (n_shared > 0 && !shared_pages)) return MOE_ERR_ARG;
+    if (T > 0 && (!positions || !slots || !seq_ids)) return MOE_ERR_ARG;
+    if (!aligned(past_lens, 4) || !aligned(new_lens, 4) || !aligned(block_table, 4) || !aligned(free_pages, 4) ||
+        !aligned(n_free, 4) || !aligned(shared_pages, 4) || !aligned(positions, 4) || !aligned(slots, 8) ||
+        !aligned(seq_ids, 4) || !aligned(starts, 4) || !aligned(seq_lens, 4) || !aligned(n_free_out, 4))
+        return MOE_ERR_ALIGN;
+    PagesArgs a{};
+    a.past = past_lens, a.news = new_lens, a.shares = shares, a.shared = shared_pages, a.shared_n = n_shared;
+    a.table = block_table, a.table_stride = table_stride;
+    a.free_pages = const_cast<int32_t*>(free_pages), a.capacity = capacity, a.n_free = n_free;
+    a.B = B, a.T = T, a.max_pages = max_pages, a.page = page_size;
+    a.positions = positions, a.slots = slots, a.seq_ids = seq_ids, a.starts = starts;
+    a.lens_out = seq_lens, a.n_free_out = n_free_out;
+    return cuda_status(launch_plan_pages(a, (cudaStream_t)stream));
+}
+
+int moe_release_pages(const int32_t* block_table, int64_t table_stride, int max_pages, const int32_t* seq_lens, int B,
+                      const uint8_t* ended, int32_t* free_pages, int capacity, const int32_t* n_free, int page_size,
+                      int n_shared, const uint8_t* shares, int32_t* seq_lens_out, int32_t* n_free_out,
+                      moe_stream_t stream) {
+    if (B < 0 || max_pages < 0 || capacity < 0 || page_size < 1 || n_shared < 0) return MOE_ERR_ARG;
+    if (B > MOE_PAGES_MAX_BATCH) return MOE_ERR_LIMIT;
+    if (B > 0 && (!seq_lens || !ended || !seq_lens_out || (max_pages > 0 && !block_table))) return MOE_ERR_ARG;
+    if (!n_free || !n_free_out || (capacity > 0 && !free_pages)) return MOE_ERR_ARG;
+    if (!aligned(seq_lens, 4) || !aligned(block_table, 4) || !aligned(free_pages, 4) || !aligned(n_free, 4) ||
+        !aligned(seq_lens_out, 4) || !aligned(n_free_out, 4))
+        return MOE_ERR_ALIGN;
+    PagesArgs a{};
+    a.past = seq_lens, a.ended = ended, a.shares = shares, a.shared_n = n_shared;
+    a.table = const_cast<int32_t*>(block_table), a.table_stride = table_stride;
+    a.free_pages = free_pages, a.capacity = capacity, a.n_free = n_free;
+    a.B = B, a.max_pages = max_pages, a.page = page_size;
+    a.lens_out = seq_lens_out, a.n_free_out = n_free_out;
+    return cuda_status(launch_release_pages(a, (cudaStream_t)stream));
+}
+
 int moe_device_error(moe_stream_t stream, int* bits) {
     if (!bits) return MOE_ERR_ARG;
     DeviceInfo di;

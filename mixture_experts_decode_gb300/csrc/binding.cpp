@@ -1,6 +1,7 @@
 // binding.cpp -- CPython module `_block`: argument marshalling of the decode
 // block's entry points (moe_paged_attention, moe_rope_append,
-// moe_norm_residual, moe_matvec4).
+// moe_norm_residual, moe_matvec4) and of the serving step's around them
+// (moe_router_grouped_topk, moe_plan_pages, moe_release_pages).
 //
 // These calls are a few microseconds of GPU work for one token, and the same
 // checks made in Python through ctypes took 20 to 30 us on the host (a
@@ -15,6 +16,7 @@
 
 #include <cmath>
 #include <exception>
+#include <initializer_list>
 #include <optional>
 #include <string>
 
@@ -386,6 +388,134 @@ PyObject* matvec4(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// A uint8 or bool array of B flags.
+const uint8_t* flags(PyObject* o, const char* name, const at::Device& dev, int64_t B) {
+    const Tensor& t = tensor(o, name);
+    if (t.scalar_type() != at::kBool) is(t, name, at::kByte, dev, 1);
+    is(t, name, t.scalar_type(), dev, 1);
+    dense(t, name);
+    if (t.size(0) != B) value_error(std::string(name) + " must be [B]");
+    return static_cast<const uint8_t*>(t.data_ptr());
+}
+// A contiguous int32 array of n elements (n < 0: any number).
+int32_t* ints(PyObject* o, const char* name, const at::Device& dev, int64_t n) {
+    const Tensor& t = tensor(o, name);
+    is(t, name, at::kInt, dev, 1);
+    dense(t, name);
+    if (n >= 0 && t.size(0) != n) value_error(std::string(name) + " must be [" + std::to_string(n) + "]");
+    return static_cast<int32_t*>(t.data_ptr());
+}
+const Tensor& table_of(PyObject* o, const at::Device& dev, int64_t B) {
+    const Tensor& t = tensor(o, "block_table");
+    is(t, "block_table", at::kInt, dev, 2);
+    if (t.size(0) != B || (t.size(1) > 1 && t.stride(1) != 1))
+        value_error("block_table must be [B, max_pages] with contiguous rows");
+    return t;
+}
+PyObject* tuple_of(std::initializer_list<Tensor> parts) {
+    PyObject* r = PyTuple_New((Py_ssize_t)parts.size());
+    if (!r) throw Raised{};
+    Py_ssize_t i = 0;
+    for (const Tensor& t : parts) PyTuple_SET_ITEM(r, i++, THPVariable_Wrap(t));
+    return r;
+}
+
+// logits, k, bias, score, groups, top_groups, group_score, renormalize, scale,
+// topk_ids, topk_w
+PyObject* router_grouped_topk(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 11, [&]() -> PyObject* {
+        const Tensor& logits = tensor(a[0], "logits");
+        const at::ScalarType type = logits.scalar_type();
+        if (type != at::kFloat && type != at::kBFloat16 && type != at::kHalf)
+            type_error(std::string("logits must be float32, bfloat16 or float16, got ") + c10::toString(type));
+        const at::Device dev = logits.device();
+        is(logits, "logits", type, dev, 2);
+        last_dense(logits, "logits");
+        const int64_t T = logits.size(0), E = logits.size(1);
+        const int k = integer(a[1]);
+        if (k < 0) value_error("k must not be negative");
+        const float* bias = nullptr;
+        if (a[2] != Py_None) {
+            const Tensor& b = tensor(a[2], "bias");
+            is(b, "bias", at::kFloat, dev, 1);
+            dense(b, "bias");
+            if (b.size(0) != E) value_error("bias must be [E]");
+            bias = static_cast<const float*>(b.data_ptr());
+        }
+        const OnDevice on(dev);
+        const Tensor ids = output(a[9], "topk_ids", {T, k}, logits.options().dtype(at::kInt));
+        const Tensor w = output(a[10], "topk_w", {T, k}, logits.options().dtype(at::kFloat));
+        check("moe_router_grouped_topk",
+              moe_router_grouped_topk(logits.data_ptr(), step_of(logits, 0), size32(T, "logits"), size32(E, "logits"),
+                                      dtype_code(type), bias, k, integer(a[3]), integer(a[4]), integer(a[5]), integer(a[6]),
+                                      truth(a[7]) ? 1 : 0, (float)number(a[8]), static_cast<int32_t*>(ids.data_ptr()),
+                                      static_cast<float*>(w.data_ptr()), on.stream));
+        return tuple_of({ids, w});
+    });
+}
+
+// past_lens, new_lens, block_table, free_pages, n_free, page_size, tokens,
+// shared_pages, shares, positions, slots, seq_ids, starts, seq_lens, n_free_out
+PyObject* plan_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 15, [&]() -> PyObject* {
+        const Tensor& past = tensor(a[0], "past_lens");
+        const at::Device dev = past.device();
+        is(past, "past_lens", at::kInt, dev, 1);
+        dense(past, "past_lens");
+        const int64_t B = past.size(0);
+        const int32_t* news = ints(a[1], "new_lens", dev, B);
+        const Tensor& table = table_of(a[2], dev, B);
+        const int32_t* stack = ints(a[3], "free_pages", dev, -1);
+        const int32_t* height = ints(a[4], "n_free", dev, 1);
+        const int T = integer(a[6]);
+        if (T < 0) value_error("tokens must not be negative");
+        int64_t ns = 0;
+        const int32_t* shared = nullptr;
+        if (a[7] != Py_None) {
+            shared = ints(a[7], "shared_pages", dev, -1);
+            ns = THPVariable_Unpack(a[7]).size(0);
+        }
+        const uint8_t* shares = a[8] == Py_None ? nullptr : flags(a[8], "shares", dev, B);
+        const OnDevice on(dev);
+        const at::TensorOptions i32 = past.options();
+        const Tensor pos = output(a[9], "positions", {T}, i32), slots = output(a[10], "slots", {T}, i32.dtype(at::kLong)),
+                     seqs = output(a[11], "seq_ids", {T}, i32), starts = output(a[12], "starts", {B + 1}, i32),
+                     lens = output(a[13], "seq_lens", {B}, i32), left = output(a[14], "n_free_out", {1}, i32);
+        auto p32 = [](const Tensor& t) { return static_cast<int32_t*>(t.data_ptr()); };
+        check("moe_plan_pages",
+              moe_plan_pages(p32(past), news, size32(B, "past_lens"), p32(table), step_of(table, 0),
+                             size32(table.size(1), "block_table"), stack, size32(THPVariable_Unpack(a[3]).size(0), "free_pages"),
+                             height, integer(a[5]), shared, size32(ns, "shared_pages"), shares, T, p32(pos),
+                             static_cast<int64_t*>(slots.data_ptr()), p32(seqs), p32(starts), p32(lens), p32(left), on.stream));
+        return tuple_of({pos, slots, seqs, starts, lens, left});
+    });
+}
+
+// block_table, seq_lens, ended, free_pages, n_free, page_size, shared, shares,
+// seq_lens_out, n_free_out
+PyObject* release_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 10, [&]() -> PyObject* {
+        const Tensor& past = tensor(a[1], "seq_lens");
+        const at::Device dev = past.device();
+        is(past, "seq_lens", at::kInt, dev, 1);
+        dense(past, "seq_lens");
+        const int64_t B = past.size(0);
+        const Tensor& table = table_of(a[0], dev, B);
+        const uint8_t* ended = flags(a[2], "ended", dev, B);
+        int32_t* stack = ints(a[3], "free_pages", dev, -1);
+        const int32_t* height = ints(a[4], "n_free", dev, 1);
+        const uint8_t* shares = a[7] == Py_None ? nullptr : flags(a[7], "shares", dev, B);
+        const OnDevice on(dev);
+        const Tensor lens = output(a[8], "seq_lens_out", {B}, past.options()), left = output(a[9], "n_free_out", {1}, past.options());
+        auto p32 = [](const Tensor& t) { return static_cast<int32_t*>(t.data_ptr()); };
+        check("moe_release_pages",
+              moe_release_pages(p32(table), step_of(table, 0), size32(table.size(1), "block_table"), p32(past),
+                                size32(B, "seq_lens"), ended, stack, size32(THPVariable_Unpack(a[3]).size(0), "free_pages"),
+                                height, integer(a[5]), integer(a[6]), shares, p32(lens), p32(left), on.stream));
+        return tuple_of({lens, left});
+    });
+}
+
 PyObject* set_fail(PyObject*, PyObject* f) {
     Py_INCREF(f);
     Py_XSETREF(g_fail, f);
@@ -402,6 +532,9 @@ PyMethodDef methods[] = {
     {"rope_append", fast(rope_append), METH_FASTCALL, nullptr},
     {"norm_residual", fast(norm_residual), METH_FASTCALL, nullptr},
     {"matvec4", fast(matvec4), METH_FASTCALL, nullptr},
+    {"router_grouped_topk", fast(router_grouped_topk), METH_FASTCALL, nullptr},
+    {"plan_pages", fast(plan_pages), METH_FASTCALL, nullptr},
+    {"release_pages", fast(release_pages), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_block", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -199,4 +199,45 @@ struct Matvec4Args {
 };
 cudaError_t launch_matvec4(Matvec4Args a, int dtype, cudaStream_t st);
 
+struct RouterGroupedArgs {
+    const void* logits;
+    int64_t stride;  // of a row, in elements
+    const float* bias;
+    int T, E, k, score, groups, top_groups, group_score, renorm;
+    float scale;
+    int32_t* ids;
+    float* w;
+    int* err;  // filled by the launch
+};
+cudaError_t launch_router_grouped(RouterGroupedArgs a, int dtype, cudaStream_t st);
+
+constexpr int PAGES_MAX_BATCH = 4096;  // MOE_PAGES_MAX_BATCH
+enum { PAGES_ROWS = 1, PAGES_STATE = 2 };
+struct PagesArgs {
+    const int32_t* past;    // lengths before
+    const int32_t* news;    // plan: new tokens
+    const uint8_t* ended;   // release
+    const uint8_t* shares;  // or null: all
+    const int32_t* shared;
+    int shared_n;
+    int32_t* table;
+    int64_t table_stride;
+    int32_t* free_pages;
+    int capacity;
+    const int32_t* n_free;
+    int B, T, max_pages, page;
+    int32_t* positions;
+    int64_t* slots;
+    int32_t* seq_ids;
+    int32_t* starts;
+    int32_t* lens_out;
+    int32_t* n_free_out;
+    // filled by the launch
+    bool vec;   // outputs of tokens aligned to 16 bytes
+    int parts;  // what a launch writes: PAGES_ROWS, PAGES_STATE
+    int* err;
+};
+cudaError_t launch_plan_pages(PagesArgs a, cudaStream_t st);
+cudaError_t launch_release_pages(PagesArgs a, cudaStream_t st);
+
 }  // namespace moedec

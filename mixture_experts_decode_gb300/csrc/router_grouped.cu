@@ -1,0 +1,366 @@
+// router_grouped.cu -- routing with a bias for balance and with groups of
+// experts: per token, scores s (softmax or sigmoid of its E logits), keys
+// s + bias that decide, the best groups of experts by their best key or the
+// sum of their two best, the k largest keys within those groups (ties: the
+// lower expert first), and weights from the scores alone.
+//
+// Which of two keys is larger is decided for the real numbers, not for their
+// FP32 roundings: FP32 keys choose, and where two that matter lie within TAU
+// of each other, the keys of the candidates are computed again in 64 bits.
+// Without a bias (or with the same one for all) the logits themselves are the
+// keys, which needs no second look.
+//
+// One warp per token at a time, a lane holds NV consecutive logits; the
+// largest of 32 lanes is one redux instruction on order-preserving integers.
+// Bound: HBM for many tokens (each logit once).
+#include <algorithm>
+
+#include "block_common.cuh"
+#include "internal.h"
+
+namespace moedec {
+
+namespace {
+
+constexpr int RG_WARPS = 8;
+
+// Order-preserving map of floats (not NaN; the two zeros alike) to unsigned; 0 is below -inf's.
+__device__ __forceinline__ uint32_t ordered(float f) {
+    const uint32_t b = __float_as_uint(f + 0.f);
+    return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float unordered(uint32_t u) {
+    return __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xffffffffu));
+}
+__device__ __forceinline__ uint32_t warp_max(uint32_t v) { return __reduce_max_sync(FULL_MASK, v); }
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(FULL_MASK, v, o);
+    return v;
+}
+__device__ __forceinline__ double warp_sum(double v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(FULL_MASK, v, o);
+    return v;
+}
+
+template <int DT>
+__device__ __forceinline__ float logit_at(const void* row, int e) {
+    if (DT == MOE_F32) return static_cast<const float*>(row)[e];
+    const uint16_t h = static_cast<const uint16_t*>(row)[e];
+    if (DT == MOE_BF16) return __uint_as_float((uint32_t)h << 16);
+    return __half2float(__ushort_as_half(h));
+}
+
+// A score in 64 bits; `m` and `total` are the row's (softmax).
+__device__ __forceinline__ double score64(const RouterGroupedArgs& a, float x, double m, double total) {
+    return a.score == MOE_ROUTER_SOFTMAX ? exp((double)x - m) / total : 1.0 / (1.0 + exp(-(double)x));
+}
+
+}  // namespace
+
+template <int NV, int DT>
+__global__ void __launch_bounds__(RG_WARPS * 32) router_grouped_kernel(const __grid_constant__ RouterGroupedArgs a) {
+    __shared__ float sm_key[RG_WARPS][NV * 32];
+    const int lane = threadIdx.x & 31, warp = warp_index();
+    const int E = a.E, k = a.k;
+    const int e0 = lane * NV;
+    float* const sk = sm_key[warp];
+    after_previous();
+
+    float bias[NV];
+    bool same_bias = true;  // one bias for all experts changes no order
+    {
+        const float b0 = a.bias ? a.bias[0] : 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            bias[i] = a.bias && e0 + i < E ? a.bias[e0 + i] : 0.f;
+            if (e0 + i < E && bias[i] != b0) same_bias = false;
+        }
+        same_bias = __all_sync(FULL_MASK, same_bias) && fabsf(b0) < INFINITY;
+    }
+    const int gsize = E / a.groups;
+    const bool softmax = a.score == MOE_ROUTER_SOFTMAX;
+
+    for (int64_t t = (int64_t)blockIdx.x * RG_WARPS + warp; t < a.T; t += (int64_t)gridDim.x * RG_WARPS) {
+        const void* row = static_cast<const uint8_t*>(a.logits) + t * a.stride * (DT == MOE_F32 ? 4 : 2);
+        float x[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            x[i] = e0 + i < E ? logit_at<DT>(row, e0 + i) : -INFINITY;
+            if (!(x[i] > -INFINITY)) x[i] = -INFINITY;  // (NaN counts as absent)
+        }
+        // scores
+        float m = 0.f, total = 1.f, s[NV];
+        if (softmax) {
+            uint32_t u = 0;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) u = max(u, ordered(x[i]));
+            m = unordered(warp_max(u));
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                s[i] = x[i] == -INFINITY ? 0.f : __expf(x[i] - m);
+                sum += s[i];
+            }
+            total = warp_sum(sum);
+            const float inv = 1.f / total;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) s[i] *= inv;
+        } else {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) s[i] = __fdividef(1.f, 1.f + __expf(-x[i]));
+        }
+        // FP32 scores are off by less than this (the sigmoid: exp2, sum and
+        // quotient of a value of at most 1; the softmax: 2^-22 each of exp2 and
+        // quotient, NV + 6 half steps of the sum, |x - m| half steps of the
+        // exponent, relative to a score of at most 1 / total)
+        const float tau_s = softmax ? 0x1p-17f / total : 0x1p-20f;
+        uint32_t key[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const float f = same_bias ? x[i] : s[i] + bias[i];
+            key[i] = x[i] > -INFINITY && f > -INFINITY ? ordered(f) : 0u;
+        }
+
+        double m64 = 0., total64 = 1.;
+        bool have64 = false;
+        auto row64 = [&]() {  // the softmax's sum in 64 bits
+            if (have64 || !softmax) return;
+            m64 = m;
+            double d = 0.;
+#pragma unroll 1
+            for (int i = 0; i < NV; ++i)
+                if (e0 + i < E) {
+                    const float v = logit_at<DT>(row, e0 + i);
+                    if (v > -INFINITY) d += exp((double)v - m64);
+                }
+            total64 = warp_sum(d);
+            have64 = true;
+        };
+
+        if (a.top_groups < a.groups) {
+            // a group's worth: lane g looks over group g
+            const bool top2 = a.group_score == MOE_ROUTER_GROUP_TOP2;
+            const bool by_logit = same_bias && !top2;
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                sk[e0 + i] = key[i] == 0u ? -INFINITY : (by_logit ? x[i] : s[i] + (same_bias ? 0.f : bias[i]));
+            __syncwarp();
+            float best = -INFINITY, second = -INFINITY;
+            if (lane < a.groups) {
+                int at = lane % gsize;  // (lanes begin at different places: other banks)
+                for (int i = 0; i < gsize; ++i) {
+                    const float v = sk[lane * gsize + at];
+                    second = fmaxf(second, fminf(best, v));
+                    best = fmaxf(best, v);
+                    if (++at == gsize) at = 0;
+                }
+            }
+            float worth = top2 ? best + second : best;
+            if (!(worth >= -INFINITY)) worth = -INFINITY;
+            int rank = 0;
+            for (int g = 0; g < a.groups; ++g) {
+                const float o = __shfl_sync(FULL_MASK, worth, g);
+                rank += o > worth || (o == worth && g < lane);
+            }
+            bool in = lane < a.groups && rank < a.top_groups;
+            if (!by_logit) {
+                // the border between the last group in and the first one out
+                const float last = unordered(~warp_max(in ? ~ordered(worth) : 0u));
+                const float next = unordered(warp_max(lane < a.groups && !in ? ordered(worth) : 0u));
+                if (last - next <= 2.f * tau_s + 0x1p-20f * fmaxf(fabsf(last), fabsf(next))) {
+                    row64();
+                    double b64 = -INFINITY, s64 = -INFINITY;
+                    if (lane < a.groups)
+                        for (int i = 0; i < gsize; ++i) {
+                            const int e = lane * gsize + i;
+                            if (sk[e] == -INFINITY) continue;
+                            const double v = score64(a, logit_at<DT>(row, e), m64, total64) + (same_bias ? 0. : (double)a.bias[e]);
+                            s64 = fmax(s64, fmin(b64, v));
+                            b64 = fmax(b64, v);
+                        }
+                    const double w64 = top2 ? b64 + s64 : b64;
+                    rank = 0;
+                    for (int g = 0; g < a.groups; ++g) {
+                        const double o = __shfl_sync(FULL_MASK, w64, g);
+                        rank += o > w64 || (o == w64 && g < lane);
+                    }
+                    in = lane < a.groups && rank < a.top_groups;
+                }
+            }
+            const uint32_t kept = __ballot_sync(FULL_MASK, in);
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (!(kept >> min(31, (e0 + i) / gsize) & 1u)) key[i] = 0u;
+        }
+
+        // the picks: lane j keeps the j-th largest key
+        uint32_t mine = 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) mine = max(mine, key[i]);
+        uint32_t pick_key = 0;
+        int pick = -1, n = 0;
+        auto next_pick = [&]() -> uint32_t {
+            const uint32_t top = warp_max(mine);
+            if (top == 0u) return 0u;
+            const int owner = __ffs(__ballot_sync(FULL_MASK, mine == top)) - 1;
+            int at = 0;
+            if (lane == owner) {
+                bool gone = false;
+                mine = 0;
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    if (!gone && key[i] == top) {
+                        gone = true;
+                        at = e0 + i;
+                        key[i] = 0u;
+                    }
+                    mine = max(mine, key[i]);
+                }
+            }
+            at = __shfl_sync(FULL_MASK, at, owner);
+            if (lane == n) pick_key = top, pick = at;
+            ++n;
+            return top;
+        };
+        const int want = same_bias ? k : min(k + 1, 32);
+        while (n < want && next_pick()) {
+        }
+        float px = pick >= 0 ? logit_at<DT>(row, pick) : 0.f;
+        if (!same_bias && n > 1) {
+            // neighbours within tau of each other that are not the same values
+            const float f = unordered(pick_key);
+            const float pb = pick >= 0 ? a.bias[pick] : 0.f;
+            const float f0 = __shfl_up_sync(FULL_MASK, f, 1), x0 = __shfl_up_sync(FULL_MASK, px, 1),
+                        b0 = __shfl_up_sync(FULL_MASK, pb, 1);
+            const float tau = 2.f * tau_s + 0x1p-22f * fmaxf(fabsf(f), fabsf(f0));
+            const bool close = lane > 0 && lane < n && f0 - f <= tau;
+            bool look = __any_sync(FULL_MASK, close && !(px == x0 && pb == b0));
+            if (!look && k < 32 && (__ballot_sync(FULL_MASK, close) >> k & 1u)) {
+                // the last one in and the first one out are the same values: anything else as near?
+                const float fk = __shfl_sync(FULL_MASK, f, k), xk = __shfl_sync(FULL_MASK, px, k), bk = __shfl_sync(FULL_MASK, pb, k);
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    if (key[i] != 0u && fk - unordered(key[i]) <= 2.f * tau_s + 0x1p-22f * fabsf(fk) &&
+                        !(x[i] == xk && bias[i] == bk))
+                        look = true;
+                look = __any_sync(FULL_MASK, look);
+            } else if (!look && k == 32 && n == 32) {  // (no lane is left for the first one out)
+                const float fk = __shfl_sync(FULL_MASK, f, 31);
+                const uint32_t top = warp_max(mine);
+                look = top != 0u && fk - unordered(top) <= 2.f * tau_s + 0x1p-22f * fabsf(fk);
+            }
+            if (look) {
+                // candidates: all within tau of the k-th
+                float fk = unordered(__shfl_sync(FULL_MASK, pick_key, min(k, n) - 1));
+                float edge = fk - (2.f * tau_s + 0x1p-22f * fabsf(fk));
+                bool full = false;
+                while (true) {
+                    const uint32_t top = warp_max(mine);
+                    if (top == 0u || !(unordered(top) >= edge)) break;
+                    if (n == 32) {
+                        full = true;
+                        break;
+                    }
+                    next_pick();
+                }
+                row64();
+                if (!full) {
+                    double d = -INFINITY;
+                    if (pick >= 0) d = score64(a, logit_at<DT>(row, pick), m64, total64) + (double)a.bias[pick];
+                    int rank = 0;
+                    for (int j = 0; j < n; ++j) {
+                        const double o = __shfl_sync(FULL_MASK, d, j);
+                        const int oi = __shfl_sync(FULL_MASK, pick, j);
+                        rank += o > d || (o == d && oi < pick);
+                    }
+                    // lane `rank` takes it
+                    int from = lane;
+                    for (int j = 0; j < n; ++j)
+                        if (__shfl_sync(FULL_MASK, rank, j) == lane && lane < n) from = j;
+                    pick = __shfl_sync(FULL_MASK, pick, from);
+                } else {
+                    // more than 32 candidates: every key of the row in 64 bits, k passes over them
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < NV; ++i) sk[e0 + i] = key[i] == 0u ? 0.f : 1.f;
+                    __syncwarp();
+                    if (pick >= 0) sk[pick] = 1.f;
+                    __syncwarp();
+                    double d[NV];
+#pragma unroll
+                    for (int i = 0; i < NV; ++i)
+                        d[i] = sk[e0 + i] == 0.f ? -INFINITY : score64(a, x[i], m64, total64) + (double)bias[i];
+                    pick = -1;
+                    for (int j = 0; j < k; ++j) {
+                        double bd = -INFINITY;
+                        int bi = 0x7fffffff;
+#pragma unroll
+                        for (int i = 0; i < NV; ++i)
+                            if (d[i] > bd) bd = d[i], bi = e0 + i;
+#pragma unroll
+                        for (int o = 16; o; o >>= 1) {
+                            const double od = __shfl_xor_sync(FULL_MASK, bd, o);
+                            const int oi = __shfl_xor_sync(FULL_MASK, bi, o);
+                            if (od > bd || (od == bd && oi < bi)) bd = od, bi = oi;
+                        }
+                        if (lane == j) pick = bi;
+#pragma unroll
+                        for (int i = 0; i < NV; ++i)
+                            if (e0 + i == bi) d[i] = -INFINITY;
+                    }
+                }
+                px = pick >= 0 ? logit_at<DT>(row, pick) : 0.f;
+            }
+        }
+        const bool here = lane < k && pick >= 0;
+        const bool short_row = __any_sync(FULL_MASK, lane < k && pick < 0);
+
+        // weights from the scores: with renormalisation relative to the largest
+        // chosen logit, so that no sum of the k is zero
+        float w = 0.f;
+        float ref = m;
+        if (a.renorm) ref = unordered(warp_max(here ? ordered(px) : 0u));
+        if (softmax) {
+            w = here ? expf(px - ref) : 0.f;
+            if (!a.renorm) w /= total;
+        } else if (here) {
+            const float shift = a.renorm ? fminf(ref, 0.f) : 0.f;
+            w = expf(fminf(px, 0.f) - shift) / (1.f + expf(-fabsf(px)));
+        }
+        if (a.renorm) w = w / warp_sum(w);
+        if (lane < k) {
+            a.ids[t * k + lane] = here ? pick : -1;
+            a.w[t * k + lane] = here ? a.scale * w : 0.f;
+        }
+        if (short_row && lane == 0) atomicOr(a.err, MOE_DEVERR_LOGIT);
+    }
+}
+
+template <int NV, int DT>
+static cudaError_t launch_rg(const RouterGroupedArgs& a, const DeviceInfo& di, cudaStream_t st) {
+    const int64_t blocks = (a.T + RG_WARPS - 1) / RG_WARPS;
+    return launch_after(router_grouped_kernel<NV, DT>, dim3((unsigned)std::min<int64_t>(blocks, di.sm_count * 8)),
+                        RG_WARPS * 32, 0, st, a);
+}
+
+template <int DT>
+static cudaError_t launch_rg_dt(const RouterGroupedArgs& a, const DeviceInfo& di, cudaStream_t st) {
+    if (a.E <= 128) return launch_rg<4, DT>(a, di, st);
+    if (a.E <= 256) return launch_rg<8, DT>(a, di, st);
+    if (a.E <= 512) return launch_rg<16, DT>(a, di, st);
+    return launch_rg<32, DT>(a, di, st);
+}
+
+cudaError_t launch_router_grouped(RouterGroupedArgs a, int dtype, cudaStream_t st) {
+    DeviceInfo di;
+    const cudaError_t e = device_info(&di);
+    if (e != cudaSuccess) return e;
+    a.err = di.err_word;
+    if (dtype == MOE_F32) return launch_rg_dt<MOE_F32>(a, di, st);
+    return dtype == MOE_BF16 ? launch_rg_dt<MOE_BF16>(a, di, st) : launch_rg_dt<MOE_F16>(a, di, st);
+}
+
+}  // namespace moedec
