@@ -540,6 +540,41 @@ int moe_matvec4(const void* x, int64_t x_stride, int T, int K, int dtype, const 
                 const uint8_t* zeros, int N, int group, void* y, int64_t y_stride, moe_stream_t stream);
 
 /*
+ * moe_shared_prefix_attention -- moe_paged_attention (window 0) for a batch
+ * whose sequences begin with the same shared_len tokens, whose keys and values
+ * are then read once for all of them and not once per sequence.  Outputs as
+ * there, to rounding: for sequence b and query head h
+ *     s_j = scale * sum_c q[b,h,c] * k[j,c],  j < seq_lens[b]
+ *     out[b,h] = sum_j exp(s_j - max s) v[j] / sum_j exp(s_j - max s)
+ *     lse[b,h] = log sum_j exp(s_j)
+ *   A sequence shares the prefix where shares[b] is not 0 (NULL: all) and
+ *   seq_lens[b] >= shared_len: its token j < shared_len is row j % page_size of
+ *   page shared_pages[j / page_size], and its later ones are found by its row of
+ *   block_table, indexed by j / page_size as in moe_paged_attention.  Any other
+ *   sequence (also one that ends within the prefix) has all its tokens by its
+ *   row, and has no part in the prefix.  The first entries of a sharing
+ *   sequence's row must be the shared pages too: which of the two is read for
+ *   them is left open.  shared_len need not end with a page.
+ *   What infinities, NaN, and pages outside the cache give is said there.
+ * Arguments
+ *   as in moe_paged_attention; shared_pages int32 [n_shared], shares uint8 [B]
+ *   or NULL.  workspace >= moe_shared_prefix_workspace_bytes for this B (or
+ *   more) and head layout, 256-byte aligned, its first MOE_ATTN_COUNTER_BYTES
+ *   zero before the first call and left zero by every call; one that is kept
+ *   may serve moe_paged_attention calls too, one after the other.
+ * Launches: three (own keys, prefix, join), or one where nothing is shared.
+ * Limits as there; shared_len <= n_shared * page_size and <= max_pages *
+ * page_size.
+ */
+int moe_shared_prefix_workspace_bytes(int B, int Hq, int Hkv, int D, size_t* bytes);
+int moe_shared_prefix_attention(const void* q, int64_t q_stride, int64_t q_head_stride, int B, int Hq, int Hkv, int D,
+                                int dtype, moe_cache_t k, moe_cache_t v, int cache_dtype, int num_pages, int page_size,
+                                const int32_t* shared_pages, int n_shared, int shared_len, const uint8_t* shares,
+                                const int32_t* block_table, int64_t table_stride, int max_pages, const int32_t* seq_lens,
+                                float scale, void* workspace, size_t workspace_bytes, void* out, float* lse,
+                                moe_stream_t stream);
+
+/*
  * moe_router_grouped_topk -- routing with a bias for balance and groups of
  * experts.  Per token t, with s the scores of its E logits (MOE_ROUTER_SOFTMAX:
  * softmax over all E; MOE_ROUTER_SIGMOID: 1 / (1 + exp(-logit))):

@@ -9,10 +9,12 @@ from ._lib import (MX, MoEError, Norm, PagePlan, W4, align_block_size, align_blo
                    attention_workspace, attention_workspace_bytes, copy, device_error, down, gate_up, layer,
                    layer_grouped, layer_grouped_workspace_bytes, layer_host, layer_host_workspace_bytes,
                    layer_workspace_bytes, load, matvec4, mx_requant, norm_residual, paged_attention, plan_pages,
-                   release_pages, rope_append, rope_freqs, router_grouped_topk, router_topk, version)
+                   release_pages, rope_append, rope_freqs, router_grouped_topk, router_topk,
+                   shared_prefix_attention, shared_prefix_workspace, shared_prefix_workspace_bytes, version)
 
 __all__ = ["MX", "MoEError", "Norm", "PagePlan", "W4", "align_block_size", "align_block_size_static", "align_sizes",
            "attention_workspace", "attention_workspace_bytes", "copy", "device_error", "down", "gate_up", "layer",
            "layer_grouped", "layer_grouped_workspace_bytes", "layer_host", "layer_host_workspace_bytes",
            "layer_workspace_bytes", "load", "matvec4", "mx_requant", "norm_residual", "paged_attention", "plan_pages",
-           "release_pages", "rope_append", "rope_freqs", "router_grouped_topk", "router_topk", "version"]
+           "release_pages", "rope_append", "rope_freqs", "router_grouped_topk", "router_topk",
+           "shared_prefix_attention", "shared_prefix_workspace", "shared_prefix_workspace_bytes", "version"]

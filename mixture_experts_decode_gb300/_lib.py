@@ -28,8 +28,8 @@ EXPORTS = ("moe_version", "moe_strerror", "moe_gate_up", "moe_down", "moe_layer_
            "moe_copy", "moe_device_error", "moe_router_topk", "moe_mx_requant", "moe_gate_up_fp4",
            "moe_layer_grouped_workspace_bytes", "moe_layer_grouped",
            "moe_down_fp4", "moe_paged_attention_workspace_bytes", "moe_paged_attention", "moe_rope_append",
-           "moe_rope_freqs", "moe_norm_residual", "moe_matvec4", "moe_router_grouped_topk", "moe_plan_pages",
-           "moe_release_pages")
+           "moe_rope_freqs", "moe_norm_residual", "moe_matvec4", "moe_shared_prefix_workspace_bytes",
+           "moe_shared_prefix_attention", "moe_router_grouped_topk", "moe_plan_pages", "moe_release_pages")
 
 
 class MoEError(RuntimeError):
@@ -102,6 +102,9 @@ def load(path: str = LIB_PATH):
         "moe_rope_freqs": ([I, D, I, D, D, D, D, P], I),
         "moe_norm_residual": ([P, L, I, I, I, P, L, I, NP, P, L, L, I, F, NP, P, P, P], I),
         "moe_matvec4": ([P, L, I, I, I, P, P, P, I, I, P, L, P], I),
+        "moe_shared_prefix_workspace_bytes": ([I, I, I, I, ctypes.POINTER(S)], I),
+        "moe_shared_prefix_attention": ([P, L, L, I, I, I, I, I, CacheView, CacheView, I, I, I, P, I, I, P, P, L, I, P, F,
+                                         P, S, P, P, P], I),
         "moe_router_grouped_topk": ([P, L, I, I, I, P, I, I, I, I, I, I, F, P, P, P], I),
         "moe_plan_pages": ([P, P, I, P, L, I, P, I, P, I, P, I, P, I, P, P, P, P, P, P, P], I),
         "moe_release_pages": ([P, L, I, P, I, P, P, I, P, I, I, P, P, P, P], I),
@@ -562,6 +565,41 @@ def matvec4(x, w: W4, y: Optional[torch.Tensor] = None):
 
 
 # ------------------------------------------------------ the serving step
+
+def shared_prefix_workspace_bytes(B: int, Hq: int, Hkv: int, D: int) -> int:
+    """Workspace bytes shared_prefix_attention needs for up to B sequences of a head layout."""
+    out = ctypes.c_size_t()
+    _check("moe_shared_prefix_workspace_bytes",
+           load().moe_shared_prefix_workspace_bytes(B, Hq, Hkv, D, ctypes.byref(out)))
+    return out.value
+
+
+def shared_prefix_workspace(B: int, Hq: int, Hkv: int, D: int, device=None) -> torch.Tensor:
+    """A workspace to keep for shared_prefix_attention (and paged_attention) calls on one stream, its counters cleared."""
+    ws = torch.empty(shared_prefix_workspace_bytes(B, Hq, Hkv, D), dtype=torch.uint8, device=device or "cuda")
+    ws[:4096].zero_()
+    return ws
+
+
+def shared_prefix_attention(q, k_cache, v_cache, shared_pages, shared_len: int, block_table, seq_lens,
+                            shares: Optional[torch.Tensor] = None, scale: Optional[float] = None, k_scale: float = 1.0,
+                            v_scale: float = 1.0, workspace: Optional[torch.Tensor] = None,
+                            out: Optional[torch.Tensor] = None, return_lse: bool = False,
+                            lse: Optional[torch.Tensor] = None):
+    """moe_shared_prefix_attention: paged_attention for sequences that begin
+    with the same shared_len tokens, in shared_pages int32 [n], read once for
+    all of them.
+
+    block_table, seq_lens and the rest as in paged_attention (whole sequences:
+    seq_lens counts the shared tokens, and the rows of the table begin with the
+    shared pages).  shares bool [B]: which sequences begin so (None: all); one
+    that does not, or that is shorter than shared_len, is read by its own row.
+    Pass a kept workspace (see shared_prefix_workspace).  Returns out
+    [B, Hq, D], or (out, lse float32 [B, Hq]) with return_lse."""
+    return (_block_module or _block()).shared_prefix_attention(q, k_cache, v_cache, shared_pages, shared_len, block_table,
+                                                               seq_lens, shares, scale, k_scale, v_scale, workspace, out,
+                                                               return_lse, lse)
+
 
 GROUP_SCORES = {"max": 0, "top2": 1}
 

@@ -22,7 +22,8 @@ LIB = os.path.join(PKG, "libmoedec.so")
 BLOCK = os.path.join(PKG, "_block.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 SOURCES = ["api.cu", "gate_up.cu", "down.cu", "grouped.cu", "align.cu", "router.cu", "requant.cu", "decode_fp4.cu",
-           "attention.cu", "rope.cu", "norm.cu", "matvec4.cu", "router_grouped.cu", "pages.cu"]
+           "attention.cu", "rope.cu", "norm.cu", "matvec4.cu", "router_grouped.cu", "pages.cu",
+           "prefix_attention.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "--expt-relaxed-constexpr",
               "-I" + INCLUDE, "-I" + CSRC]

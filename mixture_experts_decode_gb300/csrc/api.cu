@@ -473,6 +473,39 @@ int moe_copy(void* dst, const void* src, size_t bytes, moe_stream_t stream) {
     return cuda_status(launch_copy(dst, src, bytes, (cudaStream_t)stream));
 }
 
+// The checks of the attention calls, and their arguments; *a is filled where
+// there is something to launch (MOE_OK and B > 0).
+static int attention_args(const void* q, int64_t q_stride, int64_t q_head_stride, int B, int Hq, int Hkv, int D, int dtype,
+                          const moe_cache_t& k, const moe_cache_t& v, int cache_dtype, int num_pages, int page_size,
+                          const int32_t* block_table, int64_t table_stride, int max_pages, const int32_t* seq_lens,
+                          float scale, int window, int sinks, const void* workspace, size_t workspace_bytes, size_t need,
+                          void* out, float* lse, AttnArgs* args) {
+    if (!q || !seq_lens || !out) return MOE_ERR_ARG;
+    if ((max_pages > 0 && !block_table) || (num_pages > 0 && max_pages > 0 && (!k.data || !v.data))) return MOE_ERR_ARG;
+    if (!workspace || workspace_bytes < need) return MOE_ERR_WORKSPACE;
+    const int es = cache_dtype == MOE_E4M3 ? 1 : 2;
+    if (!aligned(q, 16) || !strides_aligned(2, 16, q_stride, q_head_stride, 0) || !aligned(k.data, 16) ||
+        !aligned(v.data, 16) || !strides_aligned(es, 16, k.page_stride, k.token_stride, k.head_stride) ||
+        !strides_aligned(es, 16, v.page_stride, v.token_stride, v.head_stride) || !aligned(workspace, 256) ||
+        !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(out, 2) || !aligned(lse, 4))
+        return MOE_ERR_ALIGN;
+    const bool e4 = cache_dtype == MOE_E4M3;
+    AttnArgs& a = *args;
+    a = {};
+    a.q = q, a.q_sb = q_stride, a.q_sh = q_head_stride;
+    a.k = k.data, a.k_sp = k.page_stride, a.k_st = k.token_stride, a.k_sh = k.head_stride;
+    a.v = v.data, a.v_sp = v.page_stride, a.v_st = v.token_stride, a.v_sh = v.head_stride;
+    a.table = block_table, a.table_stride = table_stride, a.lens = seq_lens;
+    a.B = B, a.Hq = Hq, a.Hkv = Hkv, a.D = D;
+    a.num_pages = num_pages, a.page = page_size;
+    a.max_pages = num_pages > 0 ? max_pages : 0;  // a cache without pages holds no token
+    a.window = window, a.sinks = sinks;
+    a.scale_log2 = scale * (e4 ? k.scale : 1.f) * 1.44269504088896341f;
+    a.v_scale = e4 ? v.scale : 1.f;
+    a.out = out, a.lse = lse;
+    return MOE_OK;
+}
+
 int moe_paged_attention_workspace_bytes(int Hq, int Hkv, int D, size_t* bytes) {
     if (!bytes || Hq < 1 || Hkv < 1 || D < 1) return MOE_ERR_ARG;
     if (Hq % Hkv || D % 16) return MOE_ERR_SHAPE;
@@ -494,29 +527,57 @@ int moe_paged_attention(const void* q, int64_t q_stride, int64_t q_head_stride, 
     if (rc) return rc;
     if (B > MOE_ATTN_MAX_BATCH || (int64_t)Hq * D > (1 << 24)) return MOE_ERR_LIMIT;
     if (B == 0) return MOE_OK;
-    if (!q || !seq_lens || !out) return MOE_ERR_ARG;
-    if ((max_pages > 0 && !block_table) || (num_pages > 0 && max_pages > 0 && (!k.data || !v.data))) return MOE_ERR_ARG;
-    if (!workspace || workspace_bytes < need) return MOE_ERR_WORKSPACE;
-    const int es = cache_dtype == MOE_E4M3 ? 1 : 2;
-    if (!aligned(q, 16) || !strides_aligned(2, 16, q_stride, q_head_stride, 0) || !aligned(k.data, 16) ||
-        !aligned(v.data, 16) || !strides_aligned(es, 16, k.page_stride, k.token_stride, k.head_stride) ||
-        !strides_aligned(es, 16, v.page_stride, v.token_stride, v.head_stride) || !aligned(workspace, 256) ||
-        !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(out, 2) || !aligned(lse, 4))
-        return MOE_ERR_ALIGN;
-    const bool e4 = cache_dtype == MOE_E4M3;
-    AttnArgs a{};
-    a.q = q, a.q_sb = q_stride, a.q_sh = q_head_stride;
-    a.k = k.data, a.k_sp = k.page_stride, a.k_st = k.token_stride, a.k_sh = k.head_stride;
-    a.v = v.data, a.v_sp = v.page_stride, a.v_st = v.token_stride, a.v_sh = v.head_stride;
-    a.table = block_table, a.table_stride = table_stride, a.lens = seq_lens;
-    a.B = B, a.Hq = Hq, a.Hkv = Hkv, a.D = D;
-    a.num_pages = num_pages, a.page = page_size;
-    a.max_pages = num_pages > 0 ? max_pages : 0;  // a cache without pages holds no token
-    a.window = window, a.sinks = sinks;
-    a.scale_log2 = scale * (e4 ? k.scale : 1.f) * 1.44269504088896341f;
-    a.v_scale = e4 ? v.scale : 1.f;
-    a.out = out, a.lse = lse;
+    AttnArgs a;
+    const int bad = attention_args(q, q_stride, q_head_stride, B, Hq, Hkv, D, dtype, k, v, cache_dtype, num_pages, page_size,
+                                   block_table, table_stride, max_pages, seq_lens, scale, window, sinks, workspace,
+                                   workspace_bytes, need, out, lse, &a);
+    if (bad) return bad;
     return cuda_status(launch_paged_attention(a, dtype, cache_dtype, workspace, (cudaStream_t)stream));
+}
+
+int moe_shared_prefix_workspace_bytes(int B, int Hq, int Hkv, int D, size_t* bytes) {
+    size_t own = 0;
+    if (B < 0) return MOE_ERR_ARG;
+    const int rc = moe_paged_attention_workspace_bytes(Hq, Hkv, D, &own);
+    if (rc) return rc;
+    if (!bytes) return MOE_ERR_ARG;
+    if (B > MOE_ATTN_MAX_BATCH || (int64_t)Hq * D > (1 << 24)) return MOE_ERR_LIMIT;
+    *bytes = own + (B ? round_up(prefix_workspace_bytes(B, Hq, Hkv, D), 256) : 0);
+    return MOE_OK;
+}
+
+int moe_shared_prefix_attention(const void* q, int64_t q_stride, int64_t q_head_stride, int B, int Hq, int Hkv, int D,
+                                int dtype, moe_cache_t k, moe_cache_t v, int cache_dtype, int num_pages, int page_size,
+                                const int32_t* shared_pages, int n_shared, int shared_len, const uint8_t* shares,
+                                const int32_t* block_table, int64_t table_stride, int max_pages, const int32_t* seq_lens,
+                                float scale, void* workspace, size_t workspace_bytes, void* out, float* lse,
+                                moe_stream_t stream) {
+    if (B < 0 || Hq < 1 || Hkv < 1 || D < 1 || num_pages < 0 || page_size < 1 || max_pages < 0 || n_shared < 0 || shared_len < 0)
+        return MOE_ERR_ARG;
+    if (!half_type(dtype) || (cache_dtype != dtype && cache_dtype != MOE_E4M3)) return MOE_ERR_ARG;
+    size_t need = 0;
+    const int rc = moe_shared_prefix_workspace_bytes(B, Hq, Hkv, D, &need);
+    if (rc) return rc;
+    if (shared_len > (int64_t)n_shared * page_size || shared_len > (int64_t)max_pages * page_size) return MOE_ERR_SHAPE;
+    if (B == 0) return MOE_OK;
+    if (shared_len > 0 && !shared_pages) return MOE_ERR_ARG;
+    if (!aligned(shared_pages, 4)) return MOE_ERR_ALIGN;
+    AttnArgs a;
+    const int bad = attention_args(q, q_stride, q_head_stride, B, Hq, Hkv, D, dtype, k, v, cache_dtype, num_pages, page_size,
+                                   block_table, table_stride, max_pages, seq_lens, scale, 0, 0, workspace, workspace_bytes,
+                                   need, out, lse, &a);
+    if (bad) return bad;
+    if (shared_len == 0 || num_pages == 0)  // nothing is shared, or no page holds a token
+        return cuda_status(launch_paged_attention(a, dtype, cache_dtype, workspace, (cudaStream_t)stream));
+    PrefixArgs p{};
+    p.q = a.q, p.q_sb = a.q_sb, p.q_sh = a.q_sh;
+    p.k = a.k, p.k_sp = a.k_sp, p.k_st = a.k_st, p.k_sh = a.k_sh;
+    p.v = a.v, p.v_sp = a.v_sp, p.v_st = a.v_st, p.v_sh = a.v_sh;
+    p.table = shared_pages, p.lens = seq_lens, p.shares = shares, p.len = shared_len;
+    p.cap = (int64_t)max_pages * page_size;
+    p.B = B, p.Hq = Hq, p.Hkv = Hkv, p.D = D, p.num_pages = num_pages, p.page = page_size;
+    p.scale_log2 = a.scale_log2, p.v_scale = a.v_scale, p.out = out, p.lse = lse;
+    return cuda_status(launch_shared_prefix(p, a, dtype, cache_dtype, workspace, (cudaStream_t)stream));
 }
 
 int moe_rope_append(const void* q, int64_t q_stride, int64_t q_head_stride, const void* k, int64_t k_stride,

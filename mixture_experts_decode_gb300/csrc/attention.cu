@@ -147,16 +147,31 @@ __device__ __forceinline__ Visible visible_keys(int n, int window, int sinks) {
     return {head + window, head, start - head};
 }
 
+// Behind a shared prefix (PART) a sequence that shares it and reaches its end
+// has the tokens from a.first on to itself.
+template <bool PART>
+__device__ __forceinline__ Visible visible_of(const AttnArgs& a, int b, int n) {
+    if (!PART) return visible_keys(n, a.window, a.sinks);
+    const int first = n >= a.first && (!a.shares || a.shares[b]) ? a.first : 0;
+    return {n - first, 0, first};
+}
+
 __device__ __forceinline__ void add_scaled(float4& s, float f, const float4& v) {
     s.x += f * v.x, s.y += f * v.y, s.z += f * v.z, s.w += f * v.w;
 }
 
 // Four output values of a head from its joined sums; ml = (maximum, l).
 // l = 0 (no visible key, or every score -inf) gives 0 and a log-sum of -inf.
-template <bool QBF>
+// PART: the sums as they are, (maximum, l) brought to one reference.
+template <bool QBF, bool PART>
 __device__ __forceinline__ void store_head4(const AttnArgs& a, int b, int h, int dim, const float4& sum, float2 ml,
                                             float shift) {
     const int64_t row = (int64_t)b * a.Hq + h;
+    if (PART) {
+        *reinterpret_cast<float4*>(a.part_o + row * a.D + dim) = sum;
+        if (dim == 0) reinterpret_cast<float2*>(a.part_ml)[row] = make_float2(ml.x - shift, ml.y);
+        return;
+    }
     const float f = ml.y == 0.f ? 0.f : a.v_scale / ml.y;
     float v[4] = {sum.x * f, sum.y * f, sum.z * f, sum.w * f};
     uint16_t* out = static_cast<uint16_t*>(a.out) + row * a.D + dim;
@@ -238,7 +253,7 @@ __device__ __forceinline__ bool arrive_last(int* counter, int n, int* err, int* 
 // (no other item begins in that block and goes on), its later groups and the
 // item itself by block / 8 (an item of more than eight blocks is the only one
 // with a later group, or an end, in such a place).
-template <bool QBF>
+template <bool QBF, bool PART>
 __device__ __noinline__ void join_pieces(const AttnArgs& a, int c1, int c2, int b, int head0, int heads, float shift,
                                          float2* head_ml, int* flag) {
     const int pieces = c2 - c1 + 1;
@@ -248,7 +263,9 @@ __device__ __noinline__ void join_pieces(const AttnArgs& a, int c1, int c2, int 
     int* const later = a.counters + ATTN_MAX_BLOCKS;
     int* const ends = later + ATT_JOIN_MOST;
     auto slot = [&](int c) { return 2 * c + (c == c1 ? 1 : 0); };
-    auto finish = [&](int h, int dim, const float4& sum, float2 ml) { store_head4<QBF>(a, b, head0 + h, dim, sum, ml, shift); };
+    auto finish = [&](int h, int dim, const float4& sum, float2 ml) {
+        store_head4<QBF, PART>(a, b, head0 + h, dim, sum, ml, shift);
+    };
     if (!arrive_last(grp == 0 ? a.counters + c1 : later + g0 / ATT_JOIN, in_group, a.err, flag)) return;
     if (pieces <= ATT_JOIN) {
         join_slots(a, pieces, heads, [&](int p) { return slot(c1 + p); }, finish);
@@ -269,7 +286,7 @@ __device__ __noinline__ void join_pieces(const AttnArgs& a, int c1, int c2, int 
     join_slots(a, groups, heads, [&](int p) { return slot(c1 + p * ATT_JOIN); }, finish);
 }
 
-template <int DP, int NT, int KV, bool QBF>
+template <int DP, int NT, int KV, bool QBF, bool PART>
 __global__ void __launch_bounds__(ATT_THREADS, att_blocks(DP, NT)) paged_attention_kernel(const __grid_constant__ AttnArgs a) {
     constexpr int ES = KV == KV_E4M3 ? 1 : 2;
     constexpr bool BF = KV == KV_BF16;  // operand type of the products
@@ -311,7 +328,7 @@ __global__ void __launch_bounds__(ATT_THREADS, att_blocks(DP, NT)) paged_attenti
                 if (blockIdx.x == 0) atomicOr(a.err, MOE_DEVERR_PAGE);
             }
             const int nn = (int)(n < 0 ? 0 : (n > cap ? cap : n));
-            const Visible v = visible_keys(nn, a.window, a.sinks);
+            const Visible v = visible_of<PART>(a, b, nn);
             u = ((int64_t)v.vis + ATT_UNIT - 1) / ATT_UNIT;
             if (u) u += ATT_BEGIN;
         }
@@ -332,6 +349,11 @@ __global__ void __launch_bounds__(ATT_THREADS, att_blocks(DP, NT)) paged_attenti
     // a sequence without keys has no units: its rows are written here
     for (int b = blockIdx.x; b < a.B; b += gridDim.x)
         if (prefix[b] == (b ? prefix[b - 1] : 0)) {
+            if (PART) {
+                for (int h = tid; h < a.Hq; h += ATT_THREADS)
+                    reinterpret_cast<float2*>(a.part_ml)[(int64_t)b * a.Hq + h] = make_float2(-INFINITY, 0.f);
+                continue;
+            }
             for (int i = tid; i < a.Hq * a.D; i += ATT_THREADS)
                 static_cast<uint16_t*>(a.out)[(int64_t)b * a.Hq * a.D + i] = 0;
             if (a.lse)
@@ -375,7 +397,7 @@ __global__ void __launch_bounds__(ATT_THREADS, att_blocks(DP, NT)) paged_attenti
         const int heads = min(a.hpi, a.G - chunk * a.hpi);
         const int n_raw = a.lens[b];
         const int n = (int)(n_raw > cap ? cap : n_raw);
-        const Visible vis = visible_keys(n, a.window, a.sinks);
+        const Visible vis = visible_of<PART>(a, b, n);
         const int key_end = (int)min((int64_t)vis.vis, t1 * ATT_UNIT);
         const int step0 = (int)(t0 * ATT_WARPS) + warp;
         const int64_t step_end = ((int64_t)key_end + ATT_STEP - 1) / ATT_STEP;
@@ -718,7 +740,7 @@ __global__ void __launch_bounds__(ATT_THREADS, att_blocks(DP, NT)) paged_attenti
                 add_scaled(sum, sm_m[w * NH + h],
                            *reinterpret_cast<const float4*>(smem + (size_t)w * NST * 2 * HALF + (h * SO + dim) * 4));
             if (whole)
-                store_head4<QBF>(a, b, head0 + h, dim, sum, head_ml[h], P_SHIFT);
+                store_head4<QBF, PART>(a, b, head0 + h, dim, sum, head_ml[h], P_SHIFT);
             else
                 *reinterpret_cast<float4*>(a.ws_o + ((int64_t)slot * a.hpi + h) * a.D + dim) = sum;
         }
@@ -728,7 +750,7 @@ __global__ void __launch_bounds__(ATT_THREADS, att_blocks(DP, NT)) paged_attenti
             // whose costs start before its first key and before its end
             const int c1 = (int)(((first_u + ATT_BEGIN + 1) * blocks - 1) / total);
             const int c2 = (int)(((first_u + cost) * blocks - 1) / total);
-            join_pieces<QBF>(a, c1, c2, b, head0, heads, P_SHIFT, head_ml, reinterpret_cast<int*>(sm_warp));
+            join_pieces<QBF, PART>(a, c1, c2, b, head0, heads, P_SHIFT, head_ml, reinterpret_cast<int*>(sm_warp));
         }
         __syncthreads();  // the ring and the flags are free again
         u = first_u + ATT_BEGIN + t1;
@@ -741,12 +763,12 @@ static int attn_max_blocks(int D, int hpi) {
     return 160 * att_blocks(D <= 64 ? 64 : D <= 128 ? 128 : 256, nt);
 }
 
-template <int DP, int NT, int KV, bool QBF>
+template <int DP, int NT, int KV, bool QBF, bool PART>
 static cudaError_t launch_attn(const AttnArgs& a, const DeviceInfo& di, cudaStream_t st) {
     constexpr int ES = KV == KV_E4M3 ? 1 : 2;
     const size_t smem = (size_t)ATT_WARPS * att_stages(DP, ES, NT) * 2 * ATT_STEP * DP * ES +
                         ATT_WARPS * att_stages(DP, ES, NT) * 4 + 2 * ATT_WARPS * NT * 8 * 4 + NT * 8 * 8 + 64 + (size_t)a.B * 8;
-    auto kernel = paged_attention_kernel<DP, NT, KV, QBF>;
+    auto kernel = paged_attention_kernel<DP, NT, KV, QBF, PART>;
     static SmemOnce once;
     cudaError_t e = once.set(reinterpret_cast<const void*>(kernel), di.max_smem_optin);
     if (e != cudaSuccess) return e;
@@ -757,12 +779,21 @@ static cudaError_t launch_attn(const AttnArgs& a, const DeviceInfo& di, cudaStre
     return launch_after(kernel, dim3(grid), ATT_THREADS, smem, st, a);
 }
 
-template <int KV, bool QBF>
+template <int KV, bool QBF, bool PART>
 static cudaError_t launch_attn_kv(const AttnArgs& a, const DeviceInfo& di, cudaStream_t st) {
     const bool two = a.hpi > 8;
-    if (a.D <= 64) return two ? launch_attn<64, 2, KV, QBF>(a, di, st) : launch_attn<64, 1, KV, QBF>(a, di, st);
-    if (a.D <= 128) return two ? launch_attn<128, 2, KV, QBF>(a, di, st) : launch_attn<128, 1, KV, QBF>(a, di, st);
-    return two ? launch_attn<256, 2, KV, QBF>(a, di, st) : launch_attn<256, 1, KV, QBF>(a, di, st);
+    if (a.D <= 64) return two ? launch_attn<64, 2, KV, QBF, PART>(a, di, st) : launch_attn<64, 1, KV, QBF, PART>(a, di, st);
+    if (a.D <= 128) return two ? launch_attn<128, 2, KV, QBF, PART>(a, di, st) : launch_attn<128, 1, KV, QBF, PART>(a, di, st);
+    return two ? launch_attn<256, 2, KV, QBF, PART>(a, di, st) : launch_attn<256, 1, KV, QBF, PART>(a, di, st);
+}
+
+template <bool PART>
+static cudaError_t launch_attn_types(const AttnArgs& a, int dtype, int cache_dtype, const DeviceInfo& di, cudaStream_t st) {
+    if (cache_dtype == MOE_E4M3)
+        return dtype == MOE_BF16 ? launch_attn_kv<KV_E4M3, true, PART>(a, di, st)
+                                 : launch_attn_kv<KV_E4M3, false, PART>(a, di, st);
+    return dtype == MOE_BF16 ? launch_attn_kv<KV_BF16, true, PART>(a, di, st)
+                             : launch_attn_kv<KV_F16, false, PART>(a, di, st);
 }
 
 // Query heads of one item: the group of a key-value head in equal parts of at
@@ -793,9 +824,8 @@ cudaError_t launch_paged_attention(AttnArgs a, int dtype, int cache_dtype, void*
     a.counters = static_cast<int*>(ws);
     a.ws_ml = reinterpret_cast<float*>(static_cast<char*>(ws) + ATTN_COUNTER_BYTES);
     a.ws_o = a.ws_ml + (size_t)2 * attn_max_blocks(a.D, a.hpi) * a.hpi * 2;
-    if (cache_dtype == MOE_E4M3)
-        return dtype == MOE_BF16 ? launch_attn_kv<KV_E4M3, true>(a, di, st) : launch_attn_kv<KV_E4M3, false>(a, di, st);
-    return dtype == MOE_BF16 ? launch_attn_kv<KV_BF16, true>(a, di, st) : launch_attn_kv<KV_F16, false>(a, di, st);
+    return a.part_o ? launch_attn_types<true>(a, dtype, cache_dtype, di, st)
+                    : launch_attn_types<false>(a, dtype, cache_dtype, di, st);
 }
 
 }  // namespace moedec

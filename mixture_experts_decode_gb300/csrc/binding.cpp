@@ -1,7 +1,8 @@
 // binding.cpp -- CPython module `_block`: argument marshalling of the decode
 // block's entry points (moe_paged_attention, moe_rope_append,
 // moe_norm_residual, moe_matvec4) and of the serving step's around them
-// (moe_router_grouped_topk, moe_plan_pages, moe_release_pages).
+// (moe_shared_prefix_attention, moe_router_grouped_topk, moe_plan_pages,
+// moe_release_pages).
 //
 // These calls are a few microseconds of GPU work for one token, and the same
 // checks made in Python through ctypes took 20 to 30 us on the host (a
@@ -420,6 +421,50 @@ PyObject* tuple_of(std::initializer_list<Tensor> parts) {
     return r;
 }
 
+// q, k_cache, v_cache, shared_pages, shared_len, block_table, seq_lens, shares,
+// scale, k_scale, v_scale, workspace, out, return_lse, lse
+PyObject* shared_prefix_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 15, [&]() -> PyObject* {
+        const Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k_cache"), &v = tensor(a[2], "v_cache");
+        const int dt = half_code(q, "q");
+        const at::ScalarType type = q.scalar_type();
+        const at::Device dev = q.device();
+        heads(q, "q", type, dev, -1, 0, 0);
+        const int64_t B = q.size(0), Hq = q.size(1), D = q.size(2);
+        const Caches c = caches(k, v, type, dev, D, number(a[9]), number(a[10]));
+        const int32_t* shared = ints(a[3], "shared_pages", dev, -1);
+        const Tensor& table = table_of(a[5], dev, B);
+        const int32_t* lens = ints(a[6], "seq_lens", dev, B);
+        const uint8_t* shares = a[7] == Py_None ? nullptr : flags(a[7], "shares", dev, B);
+        const double scale = a[8] == Py_None ? 1.0 / std::sqrt((double)D) : number(a[8]);
+        const OnDevice on(dev);
+        Tensor ws;
+        if (a[11] == Py_None) {
+            size_t bytes = 0;
+            check("moe_shared_prefix_workspace_bytes",
+                  moe_shared_prefix_workspace_bytes(size32(B, "q"), size32(Hq, "q"), c.heads, size32(D, "q"), &bytes));
+            ws = at::empty({(int64_t)bytes}, q.options().dtype(at::kByte));
+            ws.narrow(0, 0, MOE_ATTN_COUNTER_BYTES).zero_();
+        } else {
+            ws = tensor(a[11], "workspace");
+            is(ws, "workspace", at::kByte, dev, 1);
+            dense(ws, "workspace");
+        }
+        const Tensor out = output(a[12], "out", {B, Hq, D}, q.options());
+        const bool want = truth(a[13]);
+        Tensor lse;
+        if (want || a[14] != Py_None) lse = output(a[14], "lse", {B, Hq}, q.options().dtype(at::kFloat));
+        check("moe_shared_prefix_attention",
+              moe_shared_prefix_attention(
+                  q.data_ptr(), step_of(q, 0), step_of(q, 1), size32(B, "q"), size32(Hq, "q"), c.heads, size32(D, "q"), dt,
+                  c.k, c.v, c.dtype, c.pages, c.page, shared, size32(THPVariable_Unpack(a[3]).size(0), "shared_pages"),
+                  integer(a[4]), shares, static_cast<const int32_t*>(table.data_ptr()), step_of(table, 0),
+                  size32(table.size(1), "block_table"), lens, (float)scale, ws.data_ptr(), (size_t)ws.numel(), out.data_ptr(),
+                  lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr, on.stream));
+        return want ? tuple_of({out, lse}) : THPVariable_Wrap(out);
+    });
+}
+
 // logits, k, bias, score, groups, top_groups, group_score, renormalize, scale,
 // topk_ids, topk_w
 PyObject* router_grouped_topk(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -532,6 +577,7 @@ PyMethodDef methods[] = {
     {"rope_append", fast(rope_append), METH_FASTCALL, nullptr},
     {"norm_residual", fast(norm_residual), METH_FASTCALL, nullptr},
     {"matvec4", fast(matvec4), METH_FASTCALL, nullptr},
+    {"shared_prefix_attention", fast(shared_prefix_attention), METH_FASTCALL, nullptr},
     {"router_grouped_topk", fast(router_grouped_topk), METH_FASTCALL, nullptr},
     {"plan_pages", fast(plan_pages), METH_FASTCALL, nullptr},
     {"release_pages", fast(release_pages), METH_FASTCALL, nullptr},

@@ -128,6 +128,13 @@ struct AttnArgs {
     float scale_log2, v_scale;
     void* out;
     float* lse;
+    // the part behind a shared prefix (part_o not null): sequences that share it
+    // (shares null: all) and reach its end begin at token `first`, and (m, l) and
+    // the unnormalised sums [B][Hq][D] go to part_ml, part_o in place of out
+    int first;
+    const uint8_t* shares;
+    float* part_o;
+    float* part_ml;
     // filled by the launch
     bool out_aligned;    // to 8 bytes
     uint32_t page_mul;
@@ -140,6 +147,39 @@ struct AttnArgs {
 };
 size_t attn_workspace_bytes(int Hq, int Hkv, int D);
 cudaError_t launch_paged_attention(AttnArgs a, int dtype, int cache_dtype, void* ws, cudaStream_t st);
+
+// Attention of a batch with a shared prefix; `own` in launch_shared_prefix is
+// the call on the sequences' own keys.
+constexpr int PX_MAX_BLOCKS = 160;  // of a prefix launch that cuts the prefix (one per SM)
+struct PrefixArgs {
+    const void* q;
+    int64_t q_sb, q_sh;  // strides in elements, here and below
+    const void* k;
+    int64_t k_sp, k_st, k_sh;  // page, token, head
+    const void* v;
+    int64_t v_sp, v_st, v_sh;
+    const int32_t* table;  // pages of the prefix
+    const int32_t* lens;
+    const uint8_t* shares;
+    int len;      // tokens of the prefix
+    int64_t cap;  // tokens that a row of the block table holds
+    int B, Hq, Hkv, D, num_pages, page;
+    float scale_log2, v_scale;
+    void* out;
+    float* lse;
+    // filled by the launch
+    bool out_aligned;
+    uint32_t page_mul;
+    int page_shift;
+    int G, group_rows, splits, pieces;
+    float* own_o;   // [B][Hq][D]
+    float* own_ml;  // [B][Hq][2]
+    float* ws_o;    // [Hkv][pieces][B * G][D]
+    float* ws_ml;   // [Hkv][pieces][B * G][2]
+    int* err;
+};
+size_t prefix_workspace_bytes(int B, int Hq, int Hkv, int D);
+cudaError_t launch_shared_prefix(PrefixArgs a, const AttnArgs& own, int dtype, int cache_dtype, void* ws, cudaStream_t st);
 
 struct RopeArgs {
     const void* q;
