@@ -313,6 +313,7 @@ __global__ void __launch_bounds__(ATT_THREADS, att_blocks(DP, NT)) paged_attenti
     int64_t* prefix = sm_warp + 8;                                          // [B] cost up to and with b
 
     after_previous();
+    if (PART) let_next_start();  // the prefix's blocks take the SMs that these leave
     const int nk = a.D / 16;
     const int chunks16 = a.D * ES / 16;
     const int64_t cap = (int64_t)a.max_pages * a.page;

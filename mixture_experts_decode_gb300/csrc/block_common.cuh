@@ -34,6 +34,10 @@ __device__ __forceinline__ int warp_index() { return __shfl_sync(FULL_MASK, (int
 // (ld.global.nc, __ldg): the wait orders the writes before the former only.
 __device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// The kernel behind this one in the stream may be set up from here on (once
+// every block has come here), not only from this one's end on.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 template <class... Params, class... Args>
 cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t st, Args... args) {
     cudaLaunchAttribute attr[1];

@@ -171,7 +171,7 @@ struct PrefixArgs {
     bool out_aligned;
     uint32_t page_mul;
     int page_shift;
-    int G, group_rows, splits, pieces;
+    int G, group_rows, splits, pieces, join_groups;
     float* own_o;   // [B][Hq][D]
     float* own_ml;  // [B][Hq][2]
     float* ws_o;    // [Hkv][pieces][B * G][D]

@@ -42,34 +42,39 @@ constexpr int KV_BF16 = 0, KV_F16 = 1, KV_E4M3 = 2;
 constexpr int PX_ROWS = 128;            // query rows of a tile (the MMA's M, a warpgroup's threads)
 constexpr int PX_SOFT = 8;              // softmax warps (two warpgroups)
 constexpr int PX_MMA = PX_SOFT;         // the warp that issues the products
-constexpr int PX_KW = PX_SOFT + 1;      // first of four warps that bring K
-constexpr int PX_VW = PX_KW + 4;        // first of four warps that bring V
-constexpr int PX_THREADS = (PX_VW + 4) * 32;
+constexpr int PX_KW = PX_SOFT + 1;      // first of two warps that bring K
+constexpr int PX_VW = PX_KW + 2;        // first of two warps that bring V
+constexpr int PX_BRING = 64;            // threads of each
+constexpr int PX_THREADS = (PX_VW + 2) * 32;
 
 // DB: blocks of 64 dims that hold a head.
 constexpr int px_streams(int db) { return db == 4 ? 1 : 2; }  // (two sums of 256 columns would leave no room for scores)
 constexpr int px_keys(int db) { return db == 4 ? 64 : 128; }  // keys of a tile
-constexpr int px_stages(int db) { return db == 1 ? 4 : 2; }
-constexpr int px_half(int db) { return db * px_keys(db) * 128; }  // bytes of a K (or V) tile
-
-// Masks of live keys that are kept: the warps that write tile t's have waited
-// for S(t - 2 - ST) or later, which was issued after the softmax of job
-// t - 2 - 2 ST at the latest.
-constexpr int px_masks(int db) { return 2 * px_stages(db) + 4; }
+constexpr int px_half(int db) { return db * px_keys(db) * 128; }  // bytes of a K (or V) tile of 16-bit values
+// Stages of 16-bit tiles, and for an E4M3 cache of codes in front of them: there
+// the codes' stages hide the latency, and a widened tile is wanted again only
+// when the softmax between two uses is over.
+constexpr int px_stages(int db, bool e4) { return db == 1 ? (e4 ? 2 : 4) : (e4 ? 1 : 2); }
+constexpr int px_code_stages(int db, bool e4) { return !e4 ? 0 : db == 1 ? 3 : 2; }
+// Masks of live keys that are kept: when tile t's is written, the scores of
+// tile t - (both kinds of stages) have been issued, so the softmax of the tile
+// two before that is over.
+constexpr int px_masks(int db, bool e4) { return px_stages(db, e4) + px_code_stages(db, e4) + 4; }
 
 struct PxLayout {
-    uint32_t k, v, koff, voff, live, back, bars, slot, abort, total;
+    uint32_t k, v, codes, koff, voff, live, back, bars, slot, abort, total;
 };
-constexpr PxLayout px_layout(int db) {
+constexpr PxLayout px_layout(int db, bool e4) {
     PxLayout L{};
     uint32_t off = (uint32_t)px_streams(db) * db * PX_ROWS * 128;  // Q first
-    L.k = off;     off += px_stages(db) * px_half(db);
-    L.v = off;     off += px_stages(db) * px_half(db);
+    L.k = off;     off += px_stages(db, e4) * px_half(db);
+    L.v = off;     off += px_stages(db, e4) * px_half(db);
+    L.codes = off; off += 2 * px_code_stages(db, e4) * (px_half(db) / 2);
     L.koff = off;  off += 2 * 128 * 8;
     L.voff = off;  off += 2 * 128 * 8;
-    L.live = off;  off += px_masks(db) * 16;
+    L.live = off;  off += px_masks(db, e4) * 16;
     L.back = off;  off += 2 * PX_ROWS * 4;
-    L.bars = off;  off += (4 * px_stages(db) + 7) * 8;
+    L.bars = off;  off += (4 * px_stages(db, e4) + 12) * 8;
     L.slot = off;  off += 8;
     L.abort = off; off += 8;
     L.total = off;
@@ -79,12 +84,13 @@ constexpr PxLayout px_layout(int db) {
 __device__ __forceinline__ uint32_t swz(int row, int chunk) { return (uint32_t)(row * 128 + ((chunk ^ (row & 7)) << 4)); }
 
 // Matrix descriptor of a tile in the 128-byte swizzle: rows of 128 bytes, 8
-// rows to a group of 1024 bytes (the stride offset).  K-major operands (Q, K:
-// dims contiguous) ignore the leading offset; of an MN-major one (V: dims are
-// the product's N) it is the distance between blocks of 64 dims.
-__device__ __forceinline__ uint64_t px_desc(uint32_t saddr, uint32_t lead_bytes) {
-    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(lead_bytes >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
-           (1ull << 46) | (2ull << 61);
+// rows to a group of 1024 bytes (the stride offset, in the constant upper
+// half).  K-major operands (Q, K: dims contiguous) ignore the leading offset;
+// of an MN-major one (V: dims are the product's N) it is the distance between
+// blocks of 64 dims.  An address moves on by adding to the lower half.
+constexpr uint32_t PX_DESC_HI = (1024 >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t px_desc_lo(uint32_t saddr, uint32_t lead_bytes) {
+    return ((saddr >> 4) & 0x3FFFu) | ((lead_bytes >> 4) << 16);
 }
 // kind::f16: FP32 sums (bit 4), types of A and B (bits 7, 10: 1 for BF16), B
 // MN-major (bit 16), N / 8, M / 16.
@@ -92,30 +98,44 @@ __device__ __forceinline__ uint32_t px_idesc(bool bf, bool b_mn, int n) {
     return (1u << 4) | (bf ? (1u << 7) | (1u << 10) : 0u) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
            ((uint32_t)(PX_ROWS >> 4) << 24);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// Products and commits: the whole warp comes here, so that addresses stay in
+// uniform registers, and its leader (the same lane every time) issues.
+__device__ __forceinline__ uint32_t leader_lane() {
+    uint32_t e;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(e));
+    return e;
+}
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{ .reg .pred p; setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        "{ .reg .pred p, q; .reg .b64 a, b;\n\t"
+        "setp.ne.b32 q, %0, 0; setp.ne.b32 p, %5, 0;\n\t"
+        "mov.b64 a, {%2, %6}; mov.b64 b, {%3, %6};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%1], a, b, %4, p; }" ::"r"(lead), "r"(d), "r"(a_lo), "r"(b_lo), "r"(idesc),
+        "r"(acc), "n"(PX_DESC_HI)
         : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{ .reg .pred p; setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        "{ .reg .pred p, q; .reg .b64 b;\n\t"
+        "setp.ne.b32 q, %0, 0; setp.ne.b32 p, %5, 0;\n\t"
+        "mov.b64 b, {%3, %6};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%1], [%2], b, %4, p; }" ::"r"(lead), "r"(d), "r"(a), "r"(b_lo), "r"(idesc),
+        "r"(acc), "n"(PX_DESC_HI)
         : "memory");
 }
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
-                 : "memory");
+__device__ __forceinline__ void mma_commit(uint32_t lead, uint64_t* bar) {
+    asm volatile(
+        "{ .reg .pred q; setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(smem_addr(bar)), "r"(lead)
+        : "memory");
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// 32 (16) consecutive columns of the warp's 32 lanes of tensor memory.
-__device__ __forceinline__ void tm_ld32(uint32_t at, float (&v)[32]) {
-    uint32_t r[32];
+// 32 (16) consecutive columns of the warp's 32 lanes of tensor memory.  A
+// load's registers hold its values from the wait on.
+__device__ __forceinline__ void tm_ld32(uint32_t at, uint32_t (&r)[32]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
         "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
@@ -123,21 +143,27 @@ __device__ __forceinline__ void tm_ld32(uint32_t at, float (&v)[32]) {
           "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
           "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
           "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(at));
-    wait_ld();
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+        : "r"(at)
+        : "memory");
 }
-__device__ __forceinline__ void tm_ld16(uint32_t at, float (&v)[16]) {
-    uint32_t r[16];
+__device__ __forceinline__ void tm_wait32(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                   "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                   "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                   "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void tm_ld16(uint32_t at, uint32_t (&r)[16]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
           "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(at));
-    wait_ld();
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+        : "r"(at)
+        : "memory");
 }
 __device__ __forceinline__ void tm_st32(uint32_t at, const uint32_t (&r)[32]) {
     asm volatile(
@@ -180,45 +206,75 @@ __device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& lo, uint32_t
 }
 __device__ __forceinline__ float exp2_fast(float x) {
     float r;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));  // (results below 2^-126 are 0)
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+// p - h for the two 16-bit values h of a word, each in one instruction.
+template <bool BF>
+__device__ __forceinline__ float2 rest2(float2 p, uint32_t h) {
+    float2 r;
+    if (BF)
+        asm("{ .reg .b16 a, b, o; mov.b32 {a, b}, %4; mov.b16 o, 0xbf80;\n\t"
+            "fma.rn.f32.bf16 %0, a, o, %2; fma.rn.f32.bf16 %1, b, o, %3; }"
+            : "=f"(r.x), "=f"(r.y)
+            : "f"(p.x), "f"(p.y), "r"(h));
+    else
+        asm("{ .reg .b16 a, b, o; mov.b32 {a, b}, %4; mov.b16 o, 0xbc00;\n\t"
+            "fma.rn.f32.f16 %0, a, o, %2; fma.rn.f32.f16 %1, b, o, %3; }"
+            : "=f"(r.x), "=f"(r.y)
+            : "f"(p.x), "f"(p.y), "r"(h));
     return r;
 }
 __device__ __forceinline__ float finite_or_zero(float m) { return m == -INFINITY ? 0.f : m; }
-__device__ __forceinline__ bool mbar_done(uint64_t* bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile("{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
-                 : "=r"(ok)
-                 : "r"(smem_addr(bar)), "r"(parity)
-                 : "memory");
-    return ok != 0;
+// The barrier gets an arrival of this thread when its copies so far have landed.
+__device__ __forceinline__ void arrive_after_copies(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+// An ordinary load past L1 (the inputs may be newer than L1's lines where the
+// kernel begins before its predecessor's end).
+__device__ __forceinline__ uint4 ld_128_l2(const void* p) {
+    uint4 r;
+    asm volatile("ld.global.cg.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p) : "memory");
+    return r;
 }
 template <int ID>
-__device__ __forceinline__ void four_warps_sync() {
-    asm volatile("bar.sync %0, 128;" ::"n"(ID) : "memory");
+__device__ __forceinline__ void bringers_sync() {
+    asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(PX_BRING) : "memory");
 }
 
 }  // namespace
 
 // A block: one key-value head, one group of row tiles, one run of key tiles.
-// Roles: softmax warps 0 .. 7 (they also bring Q), the MMA warp, four warps
-// that bring K tiles and four that bring V tiles (rows of pages by 16-byte
+// Roles: softmax warps 0 .. 7 (they also bring Q), the MMA warp, two warps that
+// bring K tiles and two that bring V tiles (rows of pages by 16-byte
 // asynchronous copies into the swizzle; E4M3 codes through registers, widened).
 // Job j: scores and products of one row tile with one key tile, on score
 // buffer j & 1; the MMA warp issues S(0) S(1) PV(0) S(2) PV(1) S(3) ...: the
 // products of one thread run in order, so S(j + 2) may take the buffer that
-// PV(j) reads.  Barriers: k_full / v_full (the bringing warps), k_empty /
-// v_empty (commits), s_full (commit, and an arrival of the MMA thread that
-// carries what it saw of the tile's live keys), p_full (softmax warps), o_done
-// (commit of the stream's last PV).  Every wait is bounded; one that gives up
-// raises `abort`, and every role goes to the end.
+// PV(j) reads.  PV comes in two halves of the keys, each as soon as its
+// weights are there.  Barriers: q_full, k_full / v_full (those that bring;
+// their writes are generic, so the MMA warp fences before the tensor cores
+// read), k_empty / v_empty (commits), s_full (commit, and an arrival of the
+// MMA warp that carries what it saw of the tile's live keys), p_full (softmax
+// warps, per half), h_done / o_done (commits of PV's halves).  Every wait is
+// bounded; one that gives up raises `abort`, and every role goes to the end.
+// The kernel does not wait for its predecessor, the own keys' kernel, which
+// lets it start after everything before that one has completed; it does so at
+// its end, so that the join behind it finds both.
 template <int DB, int KV, bool QBF>
 __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attention_kernel(const __grid_constant__ PrefixArgs a) {
-    constexpr int NS = px_streams(DB), KT = px_keys(DB), ST = px_stages(DB), HALF = px_half(DB);
+    constexpr bool E4 = KV == KV_E4M3;
+    constexpr int NS = px_streams(DB), KT = px_keys(DB), ST = px_stages(DB, E4), HALF = px_half(DB), MASKS = px_masks(DB, E4);
     constexpr bool BF = KV == KV_BF16;          // operand type of the products
-    constexpr bool LO = !(KV == KV_E4M3 && QBF);  // P as hi + lo
-    constexpr float P_SHIFT = BF ? 0.f : 14.f;
-    constexpr float SLACK = BF ? 8.f : 1.f;  // FP16 holds 2^15 p
-    constexpr PxLayout L = px_layout(DB);
+    constexpr bool LO = !(E4 && QBF);  // P as hi + lo
+    constexpr float P_SHIFT = BF ? 0.f : 7.f;
+    constexpr float SLACK = 8.f;  // (FP16 holds up to 2^15)
+    constexpr PxLayout L = px_layout(DB, E4);
 
     extern __shared__ __align__(1024) uint8_t px_smem[];
     uint8_t* const sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(px_smem) + 1023) & ~uintptr_t(1023));
@@ -228,9 +284,11 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attention_kernel(const _
     uint64_t* const v_empty = k_full + 3 * ST;
     uint64_t* const s_full = k_full + 4 * ST;
     uint64_t* const p_full = s_full + 2;
-    uint64_t* const o_done = s_full + 4;
-    uint64_t* const drained = s_full + 6;
-    uint32_t* const live = reinterpret_cast<uint32_t*>(sm + L.live);  // [px_masks][4]
+    uint64_t* const o_done = s_full + 6;  // (p_full: [buffer][half])
+    uint64_t* const h_done = s_full + 8;
+    uint64_t* const q_full = s_full + 10;
+    uint64_t* const drained = s_full + 11;
+    uint32_t* const live = reinterpret_cast<uint32_t*>(sm + L.live);  // [MASKS][4]
     float* const back = reinterpret_cast<float*>(sm + L.back);        // [rows]
     volatile int* const abort = reinterpret_cast<volatile int*>(sm + L.abort);
 
@@ -251,16 +309,19 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attention_kernel(const _
 
     if (tid == 0) {
         for (int i = 0; i < ST; ++i) {
-            mbar_init(&k_full[i], 4);
+            mbar_init(&k_full[i], E4 ? 2 : PX_BRING);
             mbar_init(&k_empty[i], 1);
-            mbar_init(&v_full[i], 4);
+            mbar_init(&v_full[i], E4 ? 2 : PX_BRING);
             mbar_init(&v_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 2);
-            mbar_init(&p_full[i], 4);
+            mbar_init(&p_full[2 * i], 4);
+            mbar_init(&p_full[2 * i + 1], 4);
             mbar_init(&o_done[i], 1);
+            mbar_init(&h_done[i], 1);
         }
+        mbar_init(q_full, PX_SOFT * 32);
         mbar_init(drained, 1);
         *abort = 0;
         mbar_init_fence();
@@ -271,25 +332,28 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attention_kernel(const _
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    after_previous();
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = *reinterpret_cast<const uint32_t*>(sm + L.slot);
+    let_next_start();
 
     // Q, by the softmax warps: CH lanes of 16 bytes a row
     if (warp < PX_SOFT) {
         const int CH = D / 8;
-        const bool flip = a.scale_log2 < 0.f;  // the products take |scale|, q its sign
         const int per = CH <= 8 ? 8 : CH <= 16 ? 16 : 32;  // lanes of a row
         const int c = lane & (per - 1);
-        const int rows = NS * PX_ROWS;
-#pragma unroll 4
-        for (int r = tid / per; r < rows; r += PX_SOFT * 32 / per) {
-            const int row = row0 + r;
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (row < R && c < CH) {
-                const int b = row / a.G, h = kvh * a.G + (row - b * a.G);
-                v = ld_128(static_cast<const uint16_t*>(a.q) + (int64_t)b * a.q_sb + (int64_t)h * a.q_sh + c * 8);
-            }
-            uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            if (KV == KV_E4M3 && QBF) {
+        auto place = [&](int r) { return sm + ((r >> 7) * DB + (c >> 3)) * (PX_ROWS * 128) + swz(r & 127, c & 7); };
+        auto source = [&](int row) {
+            const int b = row / a.G, h = kvh * a.G + (row - b * a.G);
+            return static_cast<const uint16_t*>(a.q) + (int64_t)b * a.q_sb + (int64_t)h * a.q_sh + c * 8;
+        };
+        if constexpr (E4 && QBF) {
+#pragma unroll 8
+            for (int r = tid / per; r < MT * PX_ROWS; r += PX_SOFT * 32 / per) {
+                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                if (row0 + r < R && c < CH) v = ld_128_l2(source(row0 + r));
+                uint32_t w[4] = {v.x, v.y, v.z, v.w};
                 float amax = 0.f;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -307,163 +371,191 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attention_kernel(const _
                     const float2 p = bf16x2_to_float2(w[i]);
                     w[i] = pack2<false>(p.x * fwd, p.y * fwd);
                 }
+                if (c < CH) *reinterpret_cast<uint4*>(place(r)) = make_uint4(w[0], w[1], w[2], w[3]);
             }
-            if (c < CH) {
-                const uint32_t s = flip ? 0x80008000u : 0u;
-                *reinterpret_cast<uint4*>(sm + ((r >> 7) * DB + (c >> 3)) * (PX_ROWS * 128) + swz(r & 127, c & 7)) =
-                    make_uint4(w[0] ^ s, w[1] ^ s, w[2] ^ s, w[3] ^ s);
-            }
+            mbar_arrive(q_full);
+        } else {
+            for (int r = tid / per; r < MT * PX_ROWS; r += PX_SOFT * 32 / per)
+                if (c < CH) {
+                    const bool have = row0 + r < R;
+                    cp_async_16_zfill(place(r), have ? source(row0 + r) : a.q, have ? 16 : 0);
+                }
+            arrive_after_copies(q_full);
         }
-        fence_proxy_async();
     }
-    fence_before();
-    __syncthreads();
-    fence_after();
-    const uint32_t tmem = *reinterpret_cast<const uint32_t*>(sm + L.slot);
 
     if (warp == PX_MMA) {
-        if (lane == 0) {
-            const uint32_t q0 = smem_addr(sm), k0 = smem_addr(sm + L.k), v0 = smem_addr(sm + L.v);
-            const uint32_t id_s = px_idesc(BF, false, KT), id_o = px_idesc(BF, true, D);
-            bool ok = true;
-            auto scores = [&](int j) {
-                const int t = MT == 2 ? j >> 1 : j, st = t % ST;
-                if (!mbar_wait_abort(&k_full[st], (t / ST) & 1, abort)) return false;
-                fence_after();
-                const uint32_t q = q0 + (MT == 2 ? (j & 1) * DB * (PX_ROWS * 128) : 0);
-                for (int kk = 0; kk < D / 16; ++kk)
-                    mma_ss(tmem + (j & 1) * 128, px_desc(q + (kk >> 2) * (PX_ROWS * 128) + (kk & 3) * 32, 16),
-                           px_desc(k0 + st * HALF + (kk >> 2) * (KT * 128) + (kk & 3) * 32, 16), id_s, kk > 0);
-                mma_commit(&s_full[j & 1]);
-                mbar_arrive(&s_full[j & 1]);
-                if (MT == 1 || (j & 1)) mma_commit(&k_empty[st]);
-                return true;
-            };
-            for (int j = 0; j < 2 && j < jobs && ok; ++j) ok = scores(j);
-            for (int j = 0; j < jobs && ok; ++j) {
-                const int t = MT == 2 ? j >> 1 : j, st = t % ST, s = NS == 2 ? j & 1 : 0;
-                if (!mbar_wait_abort(&p_full[j & 1], (j >> 1) & 1, abort) ||
-                    !mbar_wait_abort(&v_full[st], (t / ST) & 1, abort)) {
-                    ok = false;
-                    break;
-                }
-                fence_after();
-                const uint32_t o = tmem + 256 + s * 128, p = tmem + (j & 1) * 128;
-                const bool first = j < NS;
-                for (int kk = 0; kk < KT / 16; ++kk) {
-                    const uint64_t v = px_desc(v0 + st * HALF + kk * 2048, KT * 128);
-                    const uint32_t pa = p + (kk >> 1) * 32 + (kk & 1) * 8;
-                    mma_ts(o, pa, v, id_o, !first || kk > 0);
-                    if (LO) mma_ts(o, pa + 16, v, id_o, 1u);
-                }
-                mma_commit(&o_done[s]);
-                if (MT == 1 || (j & 1)) mma_commit(&v_empty[st]);
-                if (j + 2 < jobs) ok = scores(j + 2);
+        const uint32_t lead = leader_lane();
+        const uint32_t q0 = px_desc_lo(smem_addr(sm), 16), k0 = px_desc_lo(smem_addr(sm + L.k), 16),
+                       v0 = px_desc_lo(smem_addr(sm + L.v), KT * 128);
+        const uint32_t id_s = px_idesc(BF, false, KT), id_o = px_idesc(BF, true, D);
+        const int nk = D / 16;
+        bool ok = __all_sync(FULL_MASK, mbar_wait_abort(q_full, 0, abort));
+        auto scores = [&](int j) {
+            const int t = MT == 2 ? j >> 1 : j, st = t % ST;
+            if (!__all_sync(FULL_MASK, mbar_wait_abort(&k_full[st], (t / ST) & 1, abort))) return false;
+            fence_proxy_async();
+            fence_after();
+            const uint32_t q = q0 + (MT == 2 ? (j & 1) * (DB * PX_ROWS * 128 >> 4) : 0), k = k0 + st * (HALF >> 4);
+            const uint32_t d = tmem + (j & 1) * 128;
+#pragma unroll
+            for (int kk = 0; kk < DB * 4; ++kk)
+                if (kk < nk)
+                    mma_ss(lead, d, q + (kk >> 2) * (PX_ROWS * 128 >> 4) + (kk & 3) * 2,
+                           k + (kk >> 2) * (KT * 128 >> 4) + (kk & 3) * 2, id_s, kk > 0);
+            mma_commit(lead, &s_full[j & 1]);
+            if (lead) mbar_arrive(&s_full[j & 1]);
+            if (MT == 1 || (j & 1)) mma_commit(lead, &k_empty[st]);
+            return true;
+        };
+        for (int j = 0; j < 2 && j < jobs && ok; ++j) ok = scores(j);
+        for (int j = 0; j < jobs && ok; ++j) {
+            const int t = MT == 2 ? j >> 1 : j, st = t % ST, s = NS == 2 ? j & 1 : 0;
+            if (!__all_sync(FULL_MASK, mbar_wait_abort(&v_full[st], (t / ST) & 1, abort))) {
+                ok = false;
+                break;
             }
-            // products already issued finish before tensor memory is freed
-            mma_commit(drained);
-            mbar_wait(drained, 0);
+            fence_proxy_async();
+            const uint32_t o = tmem + 256 + s * 128, p = tmem + (j & 1) * 128, v = v0 + st * (HALF >> 4);
+            const uint32_t more = j >= NS;
+#pragma unroll
+            for (int h = 0; h < 2 && ok; ++h) {
+                ok = __all_sync(FULL_MASK, mbar_wait_abort(&p_full[2 * (j & 1) + h], (j >> 1) & 1, abort));
+                if (!ok) break;
+                fence_after();
+#pragma unroll
+                for (int kk = h * (KT / 32); kk < (h + 1) * (KT / 32); ++kk) {
+                    const uint32_t pa = p + (kk >> 1) * 32 + (kk & 1) * 8;
+                    mma_ts(lead, o, pa, v + kk * (2048 >> 4), id_o, kk > 0 ? 1u : more);
+                    if (LO) mma_ts(lead, o, pa + 16, v + kk * (2048 >> 4), id_o, 1u);
+                }
+                mma_commit(lead, h ? &o_done[s] : &h_done[s]);
+            }
+            if (!ok) break;
+            if (MT == 1 || (j & 1)) mma_commit(lead, &v_empty[st]);
+            if (j + 2 < jobs) ok = scores(j + 2);
         }
-        __syncwarp();
+        // products already issued finish before tensor memory is freed
+        mma_commit(lead, drained);
+        mbar_wait(drained, 0);
     } else if (warp < PX_SOFT) {
         const int s = NS == 2 ? warp >> 2 : 0;
         const int r = (NS == 2 && MT == 2 ? s * PX_ROWS : 0) + (warp & 3) * 32 + lane;  // row of the group
         if (NS == 2 || warp < 4) {
             const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
             const uint32_t o_at = tmem + lanes + 256 + s * 128;
+            float m = -INFINITY;  // m: a whole number, so that its steps scale exactly
+            float2 l2 = make_float2(0.f, 0.f);
+            int c = 0;            // jobs of this stream so far
+            bool ok = __all_sync(FULL_MASK, mbar_wait_abort(q_full, 0, abort));
+            const bool flip = a.scale_log2 < 0.f;
             float sl = fabsf(a.scale_log2);
-            if (KV == KV_E4M3 && QBF) sl *= back[r];
+            if (E4 && QBF) sl *= back[r];
             sl = fmaxf(sl, 0x1p-126f);  // (masked scores of -inf stay so with a scale of 0)
-            float m = -INFINITY, l = 0.f;
-            int c = 0;  // jobs of this stream so far
-            bool ok = true;
-            for (int j = s; j < jobs; j += NS, ++c) {
+            for (int j = s; j < jobs && ok; j += NS, ++c) {
                 const int t = MT == 2 ? j >> 1 : j;
-                if (!__all_sync(FULL_MASK, mbar_wait_abort(&s_full[j & 1], (j >> 1) & 1, abort))) {
-                    ok = false;
-                    break;
-                }
+                ok = __all_sync(FULL_MASK, mbar_wait_abort(&s_full[j & 1], (j >> 1) & 1, abort));
+                if (!ok) break;
                 fence_after();
                 const uint32_t s_at = tmem + lanes + (j & 1) * 128;
-                const uint32_t* mask = live + (t % px_masks(DB)) * 4;
-                bool all = true;
+                const uint32_t* mask = live + (t % MASKS) * 4;
+                // 32 keys, read a chunk ahead, become weights in their place
+                auto weights = [&](int i, uint32_t(&x)[32]) {
+                    if (flip)
 #pragma unroll
-                for (int i = 0; i < KT / 32; ++i) all &= mask[i] == FULL_MASK;
-                float mx = -INFINITY;
+                        for (int e = 0; e < 32; ++e) x[e] ^= 0x80000000u;
+                    const uint32_t on = mask[i];
+                    if (on != FULL_MASK)
 #pragma unroll
-                for (int i = 0; i < KT / 32; ++i) {
-                    float v[32];
-                    tm_ld32(s_at + i * 32, v);
-                    if (!all) {
-                        const uint32_t on = mask[i];
+                        for (int e = 0; e < 32; ++e) x[e] = on >> e & 1u ? x[e] : 0xff800000u;
+                    float m0 = __uint_as_float(x[0]), m1 = __uint_as_float(x[1]);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = on >> e & 1u ? v[e] : -INFINITY;
+                    for (int e = 2; e < 30; e += 4) {
+                        m0 = max3(m0, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+                        m1 = max3(m1, __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
                     }
-                    float m0 = v[0], m1 = v[1];
+                    const float mx = max3(m0, m1, fmaxf(__uint_as_float(x[30]), __uint_as_float(x[31]))) * sl;
+                    if (__any_sync(FULL_MASK, mx > m + SLACK)) {
+                        // m moves up: so do l, O as far as it goes, and the weights of this half
+                        const float mn = fmaxf(m, ceilf(mx));
+                        const float f = exp2_fast(m - finite_or_zero(mn));
+                        m = mn;
+                        l2.x *= f, l2.y *= f;
+                        constexpr int HC = KT / 64;  // chunks of a half
+                        const bool second = i >= HC;
+                        if (second || c > 0) {
+                            ok = ok && __all_sync(FULL_MASK, second ? mbar_wait_abort(&h_done[s], c & 1, abort)
+                                                                    : mbar_wait_abort(&o_done[s], (c - 1) & 1, abort));
+                            fence_after();
+                            for (int d = 0; d < D; d += 16) {
+                                uint32_t w[16];
+                                tm_ld16(o_at + d, w);
 #pragma unroll
-                    for (int e = 2; e < 32; e += 2) m0 = fmaxf(m0, v[e]), m1 = fmaxf(m1, v[e + 1]);
-                    mx = fmaxf(mx, fmaxf(m0, m1));
-                }
-                mx *= sl;
-                if (__any_sync(FULL_MASK, mx > m + SLACK)) {
-                    const float mn = fmaxf(m, mx);
-                    const float f = exp2_fast(m - finite_or_zero(mn));
-                    m = mn;
-                    l *= f;
-                    if (c > 0) {
-                        if (!__all_sync(FULL_MASK, mbar_wait_abort(&o_done[s], (c - 1) & 1, abort))) {
-                            ok = false;
-                            break;
+                                for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * f);
+                                tm_st16(o_at + d, w);
+                            }
                         }
-                        fence_after();
-                        for (int d = 0; d < D; d += 16) {
-                            float o[16];
-                            uint32_t w[16];
-                            tm_ld16(o_at + d, o);
+                        if (HC == 2 && (i & 1))
+                            for (int d = 0; d < 32; d += 16) {
+                                uint32_t w[16];
+                                tm_ld16(s_at + (i - 1) * 32 + d, w);
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * f);
-                            tm_st16(o_at + d, w);
-                        }
-                        wait_st();
+                                for (int e = 0; e < 16; ++e) {
+                                    const float2 u = unpack2<BF>(w[e]);
+                                    w[e] = pack2<BF>(u.x * f, u.y * f);
+                                }
+                                tm_st16(s_at + (i - 1) * 32 + d, w);
+                            }
                     }
-                }
-                const float mu = finite_or_zero(m) - P_SHIFT;
-                float l0 = 0.f, l1 = 0.f;
-#pragma unroll
-                for (int i = 0; i < KT / 32; ++i) {
-                    float v[32];
-                    tm_ld32(s_at + i * 32, v);
-                    if (!all) {
-                        const uint32_t on = mask[i];
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = on >> e & 1u ? v[e] : -INFINITY;
-                    }
-                    uint32_t w[32];
+                    const float mu = finite_or_zero(m) - P_SHIFT;
+                    uint32_t w[LO ? 32 : 16];
+                    const float2 sl2 = make_float2(sl, sl), mu2 = make_float2(-mu, -mu);
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        const float p0 = exp2_fast(fmaf(v[2 * e], sl, -mu)), p1 = exp2_fast(fmaf(v[2 * e + 1], sl, -mu));
-                        l0 += p0, l1 += p1;
-                        w[e] = pack2<BF>(p0, p1);
-                        if (LO) {
-                            const float2 h = unpack2<BF>(w[e]);
-                            w[16 + e] = pack2<BF>(p0 - h.x, p1 - h.y);
+                        float2 p = __ffma2_rn(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), sl2, mu2);
+                        p = make_float2(exp2_fast(p.x), exp2_fast(p.y));
+                        l2 = __fadd2_rn(l2, p);
+                        w[e] = pack2<BF>(p.x, p.y);
+                        if constexpr (LO) {
+                            const float2 r = rest2<BF>(p, w[e]);
+                            w[16 + e] = pack2<BF>(r.x, r.y);
                         }
                     }
-                    if (LO) {
+                    if constexpr (LO)
                         tm_st32(s_at + i * 32, w);
-                    } else {
-                        uint32_t hi[16];
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) hi[e] = w[e];
-                        tm_st16(s_at + i * 32, hi);
+                    else
+                        tm_st16(s_at + i * 32, w);
+                };
+                auto half_done = [&](int h) {
+                    wait_st();
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&p_full[2 * (j & 1) + h]);
+                };
+                uint32_t x[32], y[32];
+                tm_ld32(s_at, x);
+                if constexpr (KT == 128) {
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) {
+                        tm_wait32(x);
+                        tm_ld32(s_at + h * 64 + 32, y);
+                        weights(2 * h, x);
+                        tm_wait32(y);
+                        if (h == 0) tm_ld32(s_at + 64, x);
+                        weights(2 * h + 1, y);
+                        half_done(h);
                     }
+                } else {
+                    tm_wait32(x);
+                    tm_ld32(s_at + 32, y);
+                    weights(0, x);
+                    half_done(0);
+                    tm_wait32(y);
+                    weights(1, y);
+                    half_done(1);
                 }
-                l += l0 + l1;
-                wait_st();
-                fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[j & 1]);
             }
+            const float l = l2.x + l2.y;
             // the piece: (m, l) and O of this row, O only where some job ran
             if (ok && c > 0) ok = __all_sync(FULL_MASK, mbar_wait_abort(&o_done[s], (c - 1) & 1, abort));
             const int row = row0 + r;
@@ -475,151 +567,146 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attention_kernel(const _
                 fence_after();
                 float* out = a.ws_o + at * D;
                 for (int d = 0; d < D; d += 16) {
-                    float o[16];
+                    uint32_t o[16];
                     tm_ld16(o_at + d, o);
                     if (row < R) {
 #pragma unroll
-                        for (int e = 0; e < 16; e += 4)
-                            *reinterpret_cast<float4*>(out + d + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                        for (int e = 0; e < 16; e += 8)  // whole sectors
+                            asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(out + d + e), "r"(o[e]),
+                                         "r"(o[e + 1]), "r"(o[e + 2]), "r"(o[e + 3]), "r"(o[e + 4]), "r"(o[e + 5]),
+                                         "r"(o[e + 6]), "r"(o[e + 7])
+                                         : "memory");
                     }
                 }
             }
         }
     } else {
-        // ---------------- K and V tiles, four warps each ----------------
+        // ---------------- K and V tiles, two warps each ----------------
         const bool is_v = warp >= PX_VW;
-        const int pt = tid - (is_v ? PX_VW : PX_KW) * 32;  // 0 .. 127
+        const int pt = tid - (is_v ? PX_VW : PX_KW) * 32;  // 0 .. 63
         uint64_t* const full = is_v ? v_full : k_full;
         uint64_t* const empty = is_v ? v_empty : k_empty;
         int64_t* const offs = reinterpret_cast<int64_t*>(sm + (is_v ? L.voff : L.koff));
         uint8_t* const ring = sm + (is_v ? L.v : L.k);
-        constexpr int ES = KV == KV_E4M3 ? 1 : 2;
+        constexpr int ES = E4 ? 1 : 2;
+        constexpr int KEYS = KT / PX_BRING;  // keys a thread looks up
         const int64_t sp = (is_v ? a.v_sp : a.k_sp) * ES, stt = (is_v ? a.v_st : a.k_st) * ES;
         const uint8_t* const src = static_cast<const uint8_t*>(is_v ? a.v : a.k) + (int64_t)kvh * (is_v ? a.v_sh : a.k_sh) * ES;
 
-        // Thread i finds key i's row, a tile ahead of its use.
-        int pg = 0, off = 0;
+        // Thread i finds the rows of keys i, i + 64, a tile ahead of their use.
+        int pg[KEYS], off[KEYS];
         auto find = [&](int t) {
-            if (t >= tiles || pt >= KT) return;
-            const int key = min((tile0 + t) * KT + pt, a.len - 1);
-            const int pi = (int)(((uint64_t)(uint32_t)key * a.page_mul) >> a.page_shift);
-            off = key - pi * a.page;
-            pg = a.table[pi];
+            if (t >= tiles) return;
+#pragma unroll
+            for (int i = 0; i < KEYS; ++i) {
+                const int key = min((tile0 + t) * KT + i * PX_BRING + pt, a.len - 1);
+                const int pi = (int)(((uint64_t)(uint32_t)key * a.page_mul) >> a.page_shift);
+                off[i] = key - pi * a.page;
+                pg[i] = __ldcg(a.table + pi);
+            }
         };
-        // Offsets of tile t's rows (-1: not live) to all four warps.
+        // Offsets of tile t's rows (-1: not live) to all that bring.
         auto publish = [&](int t) {
-            if (pt < KT) {
-                const bool known = pg >= 0 && pg < a.num_pages;
+#pragma unroll
+            for (int i = 0; i < KEYS; ++i) {
+                const bool known = pg[i] >= 0 && pg[i] < a.num_pages;
                 if (!known) atomicOr(a.err, MOE_DEVERR_PAGE);
-                const bool have = known && (tile0 + t) * KT + pt < a.len;
-                offs[(t & 1) * 128 + pt] = have ? pg * sp + off * stt : -1;
+                const int at = i * PX_BRING + pt;
+                const bool have = known && (tile0 + t) * KT + at < a.len;
+                offs[(t & 1) * 128 + at] = have ? pg[i] * sp + off[i] * stt : -1;
                 const uint32_t word = __ballot_sync(FULL_MASK, have);
-                if (!is_v && lane == 0) live[(t % px_masks(DB)) * 4 + (pt >> 5)] = word;
+                if (!is_v && lane == 0) live[(t % MASKS) * 4 + (at >> 5)] = word;
             }
             if (is_v)
-                four_warps_sync<2>();
+                bringers_sync<2>();
             else
-                four_warps_sync<1>();
-        };
-        auto arrive = [&](int t) {
-            fence_proxy_async();  // this thread's part of the tile, before the tensor cores read it
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&full[t % ST]);
+                bringers_sync<1>();
         };
         find(0);
         bool ok = true;
-        if (KV != KV_E4M3) {
-            const int CH = D / 8, per = 128 / CH;  // rows that the warps copy at once
+        if constexpr (!E4) {
+            const int CH = D / 8, per = PX_BRING / CH;  // rows that the two warps copy at once
             const int c = pt % CH, r0 = pt / CH;
             const uint32_t col = (c >> 3) * (KT * 128);
-            int sent = 0;  // tiles whose copies have been announced
             for (int t = 0; t < tiles; ++t) {
                 publish(t);
                 find(t + 1);
                 const int st = t % ST;
-                if (t >= ST && ok) {
-                    const uint32_t par = ((t / ST) - 1) & 1;
-                    // nothing to issue yet: what is on its way is announced first
-                    if (!__all_sync(FULL_MASK, mbar_done(&empty[st], par))) {
-                        cp_async_wait<0>();
-                        for (; sent < t; ++sent) arrive(sent);
-                        ok = __all_sync(FULL_MASK, mbar_wait_abort(&empty[st], par, abort));
-                    }
-                }
-                if (!ok) continue;  // (the four warps stay together at publish)
+                if (t >= ST && ok) ok = __all_sync(FULL_MASK, mbar_wait_abort(&empty[st], ((t / ST) - 1) & 1, abort));
+                if (!ok) continue;  // (the two warps stay together at publish)
                 uint8_t* const dst = ring + st * HALF + col;
                 const int64_t* const o = offs + (t & 1) * 128;
                 if (r0 < per)
-#pragma unroll 4
+#pragma unroll 8
                     for (int row = r0; row < KT; row += per) {
                         const int64_t at = o[row];
                         cp_async_16_zfill(dst + swz(row, c & 7), src + (at < 0 ? 0 : at) + c * 16, at < 0 ? 0 : 16);
                     }
-                cp_async_commit();
-                if (sent < t) {  // (at most tile t - 1 is left)
-                    cp_async_wait<1>();
-                    for (; sent < t; ++sent) arrive(sent);
-                }
+                arrive_after_copies(&full[st]);
             }
-            cp_async_wait<0>();
-            if (ok)
-                for (; sent < tiles; ++sent) arrive(sent);
         } else {
-            // 16 codes a thread at a time, the next tile's in registers
-            constexpr int PER = KT * DB * 4 / 128;  // pieces of 16 codes a thread has of a tile at most
+            // 16 codes at a time; a thread widens the pieces that it has copied
+            // itself, and piece i of all threads lies together
+            constexpr int PER = KT * DB * 4 / PX_BRING, RS = px_code_stages(DB, E4);
+            uint8_t* const codes = sm + L.codes + (is_v ? RS * (HALF / 2) : 0) + pt * 16;
             const int CH = D / 16;
-            uint4 next[PER];
-            int rows[PER], cols[PER];
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                rows[i] = (pt + i * 128) / CH;
-                cols[i] = pt + i * 128 - rows[i] * CH;
-            }
-            auto load = [&](int t) {
-                const int64_t* const o = offs + (t & 1) * 128;
-#pragma unroll
-                for (int i = 0; i < PER; ++i) {
-                    const int row = rows[i], c = cols[i];
-                    const int64_t at = row < KT ? o[row] : -1;
-                    next[i] = at < 0 ? make_uint4(0u, 0u, 0u, 0u) : ld_128(src + at + c * 16);
-                }
+            const int row0 = pt / CH, c0 = pt - row0 * CH, dr = PX_BRING / CH, dc = PX_BRING - dr * CH;
+            auto step = [&](int& row, int& c) {  // to the thread's next piece
+                row += dr;
+                c += dc;
+                if (c >= CH) c -= CH, ++row;
             };
-            if (tiles > 0) {
-                publish(0);
-                find(1);
-                load(0);
-            }
+            auto copy = [&](int t) {
+                if (t < tiles) {
+                    publish(t);
+                    find(t + 1);
+                    const int64_t* const o = offs + (t & 1) * 128;
+                    uint8_t* const to = codes + (t % RS) * (HALF / 2);
+                    int row = row0, c = c0;
+#pragma unroll
+                    for (int i = 0; i < PER; ++i) {
+                        if (row < KT) {
+                            const int64_t at = o[row];
+                            cp_async_16_zfill(to + i * (PX_BRING * 16), src + (at < 0 ? 0 : at) + c * 16, at < 0 ? 0 : 16);
+                        }
+                        step(row, c);
+                    }
+                }
+                cp_async_commit();
+            };
+#pragma unroll 1
+            for (int t = 0; t < RS - 1; ++t) copy(t);
             for (int t = 0; t < tiles; ++t) {
                 const int st = t % ST;
-                uint4 cur[PER];
-#pragma unroll
-                for (int i = 0; i < PER; ++i) cur[i] = next[i];
-                if (t + 1 < tiles) {
-                    publish(t + 1);
-                    find(t + 2);
-                    load(t + 1);
-                }
+                copy(t + RS - 1);
+                cp_async_wait<RS - 1>();
                 if (t >= ST && ok) ok = __all_sync(FULL_MASK, mbar_wait_abort(&empty[st], ((t / ST) - 1) & 1, abort));
-                if (!ok) continue;  // (the four warps stay together at publish)
+                if (!ok) continue;  // (the two warps stay together at publish)
+                const uint8_t* const from = codes + (t % RS) * (HALF / 2);
                 uint8_t* const dst = ring + st * HALF;
+                int row = row0, c = c0;
 #pragma unroll
                 for (int i = 0; i < PER; ++i) {
-                    const int row = rows[i], c = cols[i];
                     if (row < KT) {
+                        const uint4 x = *reinterpret_cast<const uint4*>(from + i * (PX_BRING * 16));
                         uint32_t w[8];
-                        e4m3x4_to_f16(cur[i].x, w[0], w[1]);
-                        e4m3x4_to_f16(cur[i].y, w[2], w[3]);
-                        e4m3x4_to_f16(cur[i].z, w[4], w[5]);
-                        e4m3x4_to_f16(cur[i].w, w[6], w[7]);
+                        e4m3x4_to_f16(x.x, w[0], w[1]);
+                        e4m3x4_to_f16(x.y, w[2], w[3]);
+                        e4m3x4_to_f16(x.z, w[4], w[5]);
+                        e4m3x4_to_f16(x.w, w[6], w[7]);
                         uint8_t* const d = dst + (c >> 2) * (KT * 128);
                         *reinterpret_cast<uint4*>(d + swz(row, (2 * c) & 7)) = make_uint4(w[0], w[1], w[2], w[3]);
                         *reinterpret_cast<uint4*>(d + swz(row, (2 * c + 1) & 7)) = make_uint4(w[4], w[5], w[6], w[7]);
                     }
+                    step(row, c);
                 }
-                arrive(t);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&full[st]);
             }
         }
     }
+    cp_async_commit();
+    cp_async_wait<0>();  // no copy still in flight on any exit
     fence_before();
     __syncthreads();
     if (warp == PX_MMA) {
@@ -627,30 +714,27 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attention_kernel(const _
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
     }
     if (tid == 0 && *abort) atomicOr(a.err, MOE_DEVERR_TIMEOUT);
+    after_previous();
 }
 
-// Every output from its pieces: the prefix's, in the order of its runs, where
-// the sequence shares it, then the sequence's own.  Four dims a thread, eight
-// pieces' loads in flight; a piece of weight 0 may hold anything.
+// Every output from its pieces: the sequence's own and, where it shares the
+// prefix, the prefix's.  A thread takes four dims of a row, and a.join_groups
+// threads with the same dims divide the row's pieces between them, eight or so
+// each with all loads in flight; the groups are added in order.  A piece of
+// weight 0 may hold anything.  (32 pieces of 1024 rows by one thread for each
+// four dims took 10 us, four dependent rounds to L2.)
+constexpr int PJ_THREADS = 256;
 template <bool QBF>
-__global__ void __launch_bounds__(128) prefix_join_kernel(const __grid_constant__ PrefixArgs a) {
-    after_previous();
-    const int vecs = a.D / 4;
-    const int64_t e = (int64_t)blockIdx.x * 128 + threadIdx.x;
-    if (e >= (int64_t)a.B * a.Hq * vecs) return;
-    const int64_t bh = e / vecs;
-    const int dim = (int)(e - bh * vecs) * 4;
-    const int b = (int)(bh / a.Hq), h = (int)(bh - (int64_t)b * a.Hq);
+__global__ void __launch_bounds__(PJ_THREADS) prefix_join_kernel(const __grid_constant__ PrefixArgs a) {
+    __shared__ float4 sm_o[PJ_THREADS];
+    __shared__ float2 sm_ml[PJ_THREADS];
+    const int vecs = a.D / 4, per_row = vecs * a.join_groups;
+    const int slot = threadIdx.x / per_row, in_row = threadIdx.x - slot * per_row;
+    const int g = in_row / vecs, dim = (in_row - g * vecs) * 4;
+    const int64_t bh = (int64_t)blockIdx.x * (PJ_THREADS / per_row) + slot;
+    const bool on = slot < PJ_THREADS / per_row && bh < (int64_t)a.B * a.Hq;
+    const int b = on ? (int)(bh / a.Hq) : 0, h = on ? (int)(bh - (int64_t)b * a.Hq) : 0;
     const int kvh = h / a.G, R = a.B * a.G, row = b * a.G + (h - kvh * a.G);
-    int np = 0;
-    if (min((int64_t)a.lens[b], a.cap) >= a.len && (!a.shares || a.shares[b])) {
-        const int g0 = row / a.group_rows * a.group_rows;
-        np = a.group_rows > PX_ROWS && R - g0 <= PX_ROWS ? 2 * a.splits : a.splits;
-    }
-    const float2* const mls = reinterpret_cast<const float2*>(a.ws_ml) + (int64_t)kvh * a.pieces * R + row;
-    const float* const os = a.ws_o + ((int64_t)kvh * a.pieces * R + row) * a.D + dim;
-    const float2 own_ml = reinterpret_cast<const float2*>(a.own_ml)[bh];
-    const float4 own = *reinterpret_cast<const float4*>(a.own_o + bh * a.D + dim);
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
     float m = -INFINITY, l = 0.f;
     auto scale = [&](float mn) {
@@ -665,26 +749,59 @@ __global__ void __launch_bounds__(128) prefix_join_kernel(const __grid_constant_
         l += f * ml.y;
         sum.x += f * v.x, sum.y += f * v.y, sum.z += f * v.z, sum.w += f * v.w;
     };
-#pragma unroll 1
-    for (int p0 = 0; p0 < np; p0 += 8) {
-        float4 v[8];
-        float2 ml[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int64_t at = (int64_t)min(p0 + i, np - 1) * R;
-            ml[i] = mls[at];
-            v[i] = *reinterpret_cast<const float4*>(os + at * a.D);
+    after_previous();
+    if (on) {
+        int np = 0;
+        if (min((int64_t)a.lens[b], a.cap) >= a.len && (!a.shares || a.shares[b])) {
+            const int g0 = row / a.group_rows * a.group_rows;
+            np = a.group_rows > PX_ROWS && R - g0 <= PX_ROWS ? 2 * a.splits : a.splits;
         }
-        float mn = m;
+        const float2* const mls = reinterpret_cast<const float2*>(a.ws_ml) + (int64_t)kvh * a.pieces * R + row;
+        const float* const os = a.ws_o + ((int64_t)kvh * a.pieces * R + row) * a.D + dim;
+        float2 own_ml = make_float2(-INFINITY, 0.f);
+        float4 own = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (g == 0) {
+            own_ml = reinterpret_cast<const float2*>(a.own_ml)[bh];
+            own = *reinterpret_cast<const float4*>(a.own_o + bh * a.D + dim);
+        }
+#pragma unroll 1
+        for (int p0 = g; p0 < np; p0 += 8 * a.join_groups) {
+            float4 v[8];
+            float2 ml[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) mn = fmaxf(mn, ml[i].x);
-        scale(mn);
+            for (int i = 0; i < 8; ++i) {
+                const int p = p0 + i * a.join_groups;
+                ml[i] = make_float2(-INFINITY, 0.f);
+                if (p < np) {
+                    ml[i] = mls[(int64_t)p * R];
+                    v[i] = *reinterpret_cast<const float4*>(os + (int64_t)p * R * a.D);
+                }
+            }
+            float mn = m;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (p0 + i < np) add(ml[i], v[i]);
+            for (int i = 0; i < 8; ++i) mn = fmaxf(mn, ml[i].x);
+            scale(mn);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (p0 + i * a.join_groups < np) add(ml[i], v[i]);
+        }
+        if (g == 0) {
+            scale(fmaxf(m, own_ml.x));
+            add(own_ml, own);
+        }
     }
-    scale(fmaxf(m, own_ml.x));
-    add(own_ml, own);
+    if (a.join_groups > 1) {  // (the same in all threads)
+        sm_ml[threadIdx.x] = make_float2(m, l);
+        sm_o[threadIdx.x] = sum;
+        __syncthreads();
+        if (on && g == 0) {
+            float mn = m;
+            for (int i = 1; i < a.join_groups; ++i) mn = fmaxf(mn, sm_ml[threadIdx.x + i * vecs].x);
+            scale(mn);
+            for (int i = 1; i < a.join_groups; ++i) add(sm_ml[threadIdx.x + i * vecs], sm_o[threadIdx.x + i * vecs]);
+        }
+    }
+    if (!on || g > 0) return;
     const float f = l == 0.f ? 0.f : a.v_scale / l;
     const uint32_t lo = pack2<QBF>(sum.x * f, sum.y * f), hi = pack2<QBF>(sum.z * f, sum.w * f);
     uint16_t* const out = static_cast<uint16_t*>(a.out) + bh * a.D + dim;
@@ -731,7 +848,7 @@ size_t prefix_workspace_bytes(int B, int Hq, int Hkv, int D) {
 
 template <int DB, int KV, bool QBF>
 static cudaError_t launch_px(const PrefixArgs& a, const DeviceInfo& di, int grid, cudaStream_t st) {
-    constexpr size_t smem = px_layout(DB).total + 1024;
+    constexpr size_t smem = px_layout(DB, KV == KV_E4M3).total + 1024;
     static_assert(smem <= 227 * 1024, "a block's shared memory");
     auto kernel = prefix_attention_kernel<DB, KV, QBF>;
     static SmemOnce once;
@@ -781,9 +898,13 @@ cudaError_t launch_shared_prefix(PrefixArgs a, const AttnArgs& own, int dtype, i
     else
         e = dtype == MOE_BF16 ? launch_px_kv<KV_BF16, true>(a, di, grid, st) : launch_px_kv<KV_F16, false>(a, di, grid, st);
     if (e != cudaSuccess) return e;
-    const unsigned blocks = (unsigned)((rows * (a.D / 4) + 127) / 128);
-    return dtype == MOE_BF16 ? launch_after(prefix_join_kernel<true>, dim3(blocks), 128, 0, st, a)
-                             : launch_after(prefix_join_kernel<false>, dim3(blocks), 128, 0, st, a);
+    const int np = (a.B * a.G) % a.group_rows <= PX_ROWS ? a.pieces : a.splits, vecs = a.D / 4;
+    a.join_groups = 1;
+    while (a.join_groups * 8 < np && 2 * a.join_groups * vecs <= PJ_THREADS) a.join_groups *= 2;
+    const int per_block = PJ_THREADS / (vecs * a.join_groups);
+    const dim3 blocks((unsigned)((rows + per_block - 1) / per_block));
+    return dtype == MOE_BF16 ? launch_after(prefix_join_kernel<true>, blocks, PJ_THREADS, 0, st, a)
+                             : launch_after(prefix_join_kernel<false>, blocks, PJ_THREADS, 0, st, a);
 }
 
 }  // namespace moedec
