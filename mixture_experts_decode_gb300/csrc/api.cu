@@ -686,7 +686,7 @@ int moe_router_grouped_topk(const void* logits, int64_t stride, int T, int E, in
     if (!aligned(logits, dtype == MOE_F32 ? 4 : 2) || !aligned(bias, 4) || !aligned(topk_ids, 4) || !aligned(topk_w, 4))
         return MOE_ERR_ALIGN;
     const RouterGroupedArgs a{logits, stride, bias, T, E, k, score, groups, top_groups, group_score, renorm, scale, topk_ids,
-                              topk_w, nullptr};
+                              topk_w, false, nullptr};
     return cuda_status(launch_router_grouped(a, dtype, (cudaStream_t)stream));
 }
 

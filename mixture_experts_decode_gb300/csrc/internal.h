@@ -247,7 +247,9 @@ struct RouterGroupedArgs {
     float scale;
     int32_t* ids;
     float* w;
-    int* err;  // filled by the launch
+    // filled by the launch
+    bool vec;  // four logits at a time
+    int* err;
 };
 cudaError_t launch_router_grouped(RouterGroupedArgs a, int dtype, cudaStream_t st);
 

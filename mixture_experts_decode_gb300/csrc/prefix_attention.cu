@@ -719,13 +719,12 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attention_kernel(const _
 
 // Every output from its pieces: the sequence's own and, where it shares the
 // prefix, the prefix's.  A thread takes four dims of a row, and a.join_groups
-// threads with the same dims divide the row's pieces between them, eight or so
+// threads with the same dims divide the row's pieces between them, four or so
 // each with all loads in flight; the groups are added in order.  A piece of
-// weight 0 may hold anything.  (32 pieces of 1024 rows by one thread for each
-// four dims took 10 us, four dependent rounds to L2.)
-constexpr int PJ_THREADS = 256;
+// weight 0 may hold anything.
+constexpr int PJ_THREADS = 256, PJ_FLIGHT = 4;
 template <bool QBF>
-__global__ void __launch_bounds__(PJ_THREADS) prefix_join_kernel(const __grid_constant__ PrefixArgs a) {
+__global__ void __launch_bounds__(PJ_THREADS, 5) prefix_join_kernel(const __grid_constant__ PrefixArgs a) {
     __shared__ float4 sm_o[PJ_THREADS];
     __shared__ float2 sm_ml[PJ_THREADS];
     const int vecs = a.D / 4, per_row = vecs * a.join_groups;
@@ -765,11 +764,11 @@ __global__ void __launch_bounds__(PJ_THREADS) prefix_join_kernel(const __grid_co
             own = *reinterpret_cast<const float4*>(a.own_o + bh * a.D + dim);
         }
 #pragma unroll 1
-        for (int p0 = g; p0 < np; p0 += 8 * a.join_groups) {
-            float4 v[8];
-            float2 ml[8];
+        for (int p0 = g; p0 < np; p0 += PJ_FLIGHT * a.join_groups) {
+            float4 v[PJ_FLIGHT];
+            float2 ml[PJ_FLIGHT];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < PJ_FLIGHT; ++i) {
                 const int p = p0 + i * a.join_groups;
                 ml[i] = make_float2(-INFINITY, 0.f);
                 if (p < np) {
@@ -779,10 +778,10 @@ __global__ void __launch_bounds__(PJ_THREADS) prefix_join_kernel(const __grid_co
             }
             float mn = m;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) mn = fmaxf(mn, ml[i].x);
+            for (int i = 0; i < PJ_FLIGHT; ++i) mn = fmaxf(mn, ml[i].x);
             scale(mn);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < PJ_FLIGHT; ++i)
                 if (p0 + i * a.join_groups < np) add(ml[i], v[i]);
         }
         if (g == 0) {
@@ -900,7 +899,7 @@ cudaError_t launch_shared_prefix(PrefixArgs a, const AttnArgs& own, int dtype, i
     if (e != cudaSuccess) return e;
     const int np = (a.B * a.G) % a.group_rows <= PX_ROWS ? a.pieces : a.splits, vecs = a.D / 4;
     a.join_groups = 1;
-    while (a.join_groups * 8 < np && 2 * a.join_groups * vecs <= PJ_THREADS) a.join_groups *= 2;
+    while (a.join_groups * PJ_FLIGHT < np && 2 * a.join_groups * vecs <= PJ_THREADS) a.join_groups *= 2;
     const int per_block = PJ_THREADS / (vecs * a.join_groups);
     const dim3 blocks((unsigned)((rows + per_block - 1) / per_block));
     return dtype == MOE_BF16 ? launch_after(prefix_join_kernel<true>, blocks, PJ_THREADS, 0, st, a)

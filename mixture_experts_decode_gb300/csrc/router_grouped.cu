@@ -10,9 +10,13 @@
 // Without a bias (or with the same one for all) the logits themselves are the
 // keys, which needs no second look.
 //
-// One warp per token at a time, a lane holds NV consecutive logits; the
-// largest of 32 lanes is one redux instruction on order-preserving integers.
-// Bound: HBM for many tokens (each logit once).
+// One warp per token at a time, a lane holds NV consecutive logits.  Each lane
+// sorts its keys (a network of maxima and minima) and leaves the list in shared
+// memory; a pick is the largest of the 32 list heads, one redux instruction on
+// order-preserving integers, and the next head of the list that had it.  Whose
+// index a picked key had is found once, for all picks at the same time.
+// Bound: HBM for many tokens (each logit once); the instructions of the scores
+// and the picks come close to it.
 #include <algorithm>
 
 #include "block_common.cuh"
@@ -22,7 +26,7 @@ namespace moedec {
 
 namespace {
 
-constexpr int RG_WARPS = 8;
+constexpr int rg_warps(int nv) { return nv == 32 ? 4 : 8; }  // (48 KB hold the lists of four warps of 1024)
 
 // Order-preserving map of floats (not NaN; the two zeros alike) to unsigned; 0 is below -inf's.
 __device__ __forceinline__ uint32_t ordered(float f) {
@@ -52,6 +56,66 @@ __device__ __forceinline__ float logit_at(const void* row, int e) {
     return __half2float(__ushort_as_half(h));
 }
 
+__device__ __forceinline__ float exp2_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// Descending order by odd-even merges.
+template <int N>
+__device__ __forceinline__ void sort_down(uint32_t (&v)[N]) {
+#pragma unroll
+    for (int p = 1; p < N; p *= 2)
+#pragma unroll
+        for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+            for (int j = k % p; j + k < N; j += 2 * k)
+#pragma unroll
+                for (int i = 0; i < k; ++i)
+                    if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+                        const uint32_t a = v[i + j], b = v[i + j + k];
+                        v[i + j] = max(a, b);
+                        v[i + j + k] = min(a, b);
+                    }
+}
+
+// NV consecutive logits from expert e0 on, -inf beyond E and for NaN.
+template <int NV, int DT>
+__device__ __forceinline__ void load_logits(const void* row, int e0, int E, bool vec, float (&x)[NV]) {
+    if (vec) {  // E a multiple of 4, rows aligned to four logits
+#pragma unroll
+        for (int i = 0; i < NV; i += 4) {
+            uint32_t w[4] = {0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u};
+            if (e0 + i < E) {
+                if (DT == MOE_F32) {
+                    const uint4 v = ld_128(static_cast<const float*>(row) + e0 + i);
+                    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+                } else {
+                    const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(row) + e0 + i);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t h = (k < 2 ? v.x : v.y) >> (k & 1) * 16 & 0xffffu;
+                        w[k] = DT == MOE_BF16 ? h << 16 : __float_as_uint(__half2float(__ushort_as_half((uint16_t)h)));
+                    }
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[i + k] = __uint_as_float(w[k]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) x[i] = e0 + i < E ? logit_at<DT>(row, e0 + i) : -INFINITY;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) x[i] = fmaxf(x[i], -INFINITY);  // (of NaN: -inf)
+}
+
 // A score in 64 bits; `m` and `total` are the row's (softmax).
 __device__ __forceinline__ double score64(const RouterGroupedArgs& a, float x, double m, double total) {
     return a.score == MOE_ROUTER_SOFTMAX ? exp((double)x - m) / total : 1.0 / (1.0 + exp(-(double)x));
@@ -60,12 +124,16 @@ __device__ __forceinline__ double score64(const RouterGroupedArgs& a, float x, d
 }  // namespace
 
 template <int NV, int DT>
-__global__ void __launch_bounds__(RG_WARPS * 32) router_grouped_kernel(const __grid_constant__ RouterGroupedArgs a) {
-    __shared__ float sm_key[RG_WARPS][NV * 32];
+__global__ void __launch_bounds__(rg_warps(NV) * 32) router_grouped_kernel(const __grid_constant__ RouterGroupedArgs a) {
+    constexpr int WARPS = rg_warps(NV);
+    __shared__ uint32_t sm_key[WARPS][NV * 32];         // keys by expert
+    __shared__ uint32_t sm_list[WARPS][32 * (NV + 1)];  // each lane's in descending order, and a 0 at the end
     const int lane = threadIdx.x & 31, warp = warp_index();
     const int E = a.E, k = a.k;
     const int e0 = lane * NV;
-    float* const sk = sm_key[warp];
+    uint32_t* const sk = sm_key[warp];
+    uint32_t* const list = sm_list[warp] + lane * (NV + 1);
+    list[NV] = 0u;
     after_previous();
 
     float bias[NV];
@@ -79,28 +147,30 @@ __global__ void __launch_bounds__(RG_WARPS * 32) router_grouped_kernel(const __g
         }
         same_bias = __all_sync(FULL_MASK, same_bias) && fabsf(b0) < INFINITY;
     }
-    const int gsize = E / a.groups;
     const bool softmax = a.score == MOE_ROUTER_SOFTMAX;
+    const bool narrow = a.top_groups < a.groups;
+    const int gsize = E / a.groups;
+    // lanes of a group, where each group is a power of two of whole lanes
+    const int q = gsize % NV ? 0 : gsize / NV;
+    const bool whole_lanes = q > 0 && (q & (q - 1)) == 0;
+    const bool top2 = a.group_score == MOE_ROUTER_GROUP_TOP2;
+    const bool by_logit = same_bias && !top2;
 
-    for (int64_t t = (int64_t)blockIdx.x * RG_WARPS + warp; t < a.T; t += (int64_t)gridDim.x * RG_WARPS) {
+    for (int64_t t = (int64_t)blockIdx.x * WARPS + warp; t < a.T; t += (int64_t)gridDim.x * WARPS) {
         const void* row = static_cast<const uint8_t*>(a.logits) + t * a.stride * (DT == MOE_F32 ? 4 : 2);
         float x[NV];
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            x[i] = e0 + i < E ? logit_at<DT>(row, e0 + i) : -INFINITY;
-            if (!(x[i] > -INFINITY)) x[i] = -INFINITY;  // (NaN counts as absent)
-        }
+        load_logits<NV, DT>(row, e0, E, a.vec, x);
         // scores
         float m = 0.f, total = 1.f, s[NV];
         if (softmax) {
-            uint32_t u = 0;
+            float u = x[0];
 #pragma unroll
-            for (int i = 0; i < NV; ++i) u = max(u, ordered(x[i]));
-            m = unordered(warp_max(u));
+            for (int i = 1; i < NV; ++i) u = fmaxf(u, x[i]);
+            m = unordered(warp_max(ordered(u)));
             float sum = 0.f;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                s[i] = x[i] == -INFINITY ? 0.f : __expf(x[i] - m);
+                s[i] = x[i] == -INFINITY ? 0.f : exp2_fast((x[i] - m) * 1.44269504f);
                 sum += s[i];
             }
             total = warp_sum(sum);
@@ -109,11 +179,11 @@ __global__ void __launch_bounds__(RG_WARPS * 32) router_grouped_kernel(const __g
             for (int i = 0; i < NV; ++i) s[i] *= inv;
         } else {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) s[i] = __fdividef(1.f, 1.f + __expf(-x[i]));
+            for (int i = 0; i < NV; ++i) s[i] = rcp_fast(1.f + exp2_fast(x[i] * -1.44269504f));
         }
         // FP32 scores are off by less than this (the sigmoid: exp2, sum and
         // quotient of a value of at most 1; the softmax: 2^-22 each of exp2 and
-        // quotient, NV + 6 half steps of the sum, |x - m| half steps of the
+        // quotient, NV + 6 half steps of the sum, 2 |x - m| half steps of the
         // exponent, relative to a score of at most 1 / total)
         const float tau_s = softmax ? 0x1p-17f / total : 0x1p-20f;
         uint32_t key[NV];
@@ -139,44 +209,64 @@ __global__ void __launch_bounds__(RG_WARPS * 32) router_grouped_kernel(const __g
             have64 = true;
         };
 
-        if (a.top_groups < a.groups) {
-            // a group's worth: lane g looks over group g
-            const bool top2 = a.group_score == MOE_ROUTER_GROUP_TOP2;
-            const bool by_logit = same_bias && !top2;
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-                sk[e0 + i] = key[i] == 0u ? -INFINITY : (by_logit ? x[i] : s[i] + (same_bias ? 0.f : bias[i]));
-            __syncwarp();
+        if (narrow) {
+            // a group's worth: lane g has group g's
             float best = -INFINITY, second = -INFINITY;
-            if (lane < a.groups) {
-                int at = lane % gsize;  // (lanes begin at different places: other banks)
-                for (int i = 0; i < gsize; ++i) {
-                    const float v = sk[lane * gsize + at];
-                    second = fmaxf(second, fminf(best, v));
-                    best = fmaxf(best, v);
-                    if (++at == gsize) at = 0;
+            auto see = [&](float v) {
+                second = fmaxf(second, fminf(best, v));
+                best = fmaxf(best, v);
+            };
+            auto part = [&](int i) {  // what counts of the lane's element i
+                return key[i] == 0u ? -INFINITY : by_logit ? x[i] : same_bias ? s[i] : s[i] + bias[i];
+            };
+            if (whole_lanes) {
+#pragma unroll
+                for (int i = 0; i < NV; ++i) see(part(i));
+                for (int o = 1; o < q; o *= 2) {
+                    const float b2 = __shfl_xor_sync(FULL_MASK, best, o), s2 = __shfl_xor_sync(FULL_MASK, second, o);
+                    second = fmaxf(fmaxf(second, s2), fminf(best, b2));
+                    best = fmaxf(best, b2);
+                }
+                best = __shfl_sync(FULL_MASK, best, lane * q & 31);
+                second = __shfl_sync(FULL_MASK, second, lane * q & 31);
+            } else {
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < NV; ++i) sk[e0 + i] = __float_as_uint(part(i));
+                __syncwarp();
+                if (lane < a.groups) {
+                    int at = lane % gsize;  // (lanes begin at different places: other banks)
+                    for (int i = 0; i < gsize; ++i) {
+                        see(__uint_as_float(sk[lane * gsize + at]));
+                        if (++at == gsize) at = 0;
+                    }
                 }
             }
             float worth = top2 ? best + second : best;
             if (!(worth >= -INFINITY)) worth = -INFINITY;
             int rank = 0;
+            bool close = false;
             for (int g = 0; g < a.groups; ++g) {
                 const float o = __shfl_sync(FULL_MASK, worth, g);
                 rank += o > worth || (o == worth && g < lane);
+                close |= g != lane && fabsf(o - worth) <= 2.f * tau_s + 0x1p-20f * fabsf(worth);
             }
             bool in = lane < a.groups && rank < a.top_groups;
-            if (!by_logit) {
+            if (!by_logit && __any_sync(FULL_MASK, close && lane < a.groups)) {
                 // the border between the last group in and the first one out
                 const float last = unordered(~warp_max(in ? ~ordered(worth) : 0u));
                 const float next = unordered(warp_max(lane < a.groups && !in ? ordered(worth) : 0u));
                 if (last - next <= 2.f * tau_s + 0x1p-20f * fmaxf(fabsf(last), fabsf(next))) {
                     row64();
                     double b64 = -INFINITY, s64 = -INFINITY;
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < NV; ++i) sk[e0 + i] = key[i];
+                    __syncwarp();
                     if (lane < a.groups)
                         for (int i = 0; i < gsize; ++i) {
                             const int e = lane * gsize + i;
-                            if (sk[e] == -INFINITY) continue;
+                            if (sk[e] == 0u) continue;
                             const double v = score64(a, logit_at<DT>(row, e), m64, total64) + (same_bias ? 0. : (double)a.bias[e]);
                             s64 = fmax(s64, fmin(b64, v));
                             b64 = fmax(b64, v);
@@ -191,43 +281,60 @@ __global__ void __launch_bounds__(RG_WARPS * 32) router_grouped_kernel(const __g
                 }
             }
             const uint32_t kept = __ballot_sync(FULL_MASK, in);
+            if (whole_lanes) {
+                const bool mine_in = kept >> min(31, lane / q) & 1u;
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (!(kept >> min(31, (e0 + i) / gsize) & 1u)) key[i] = 0u;
+                for (int i = 0; i < NV; ++i) key[i] = mine_in ? key[i] : 0u;
+            } else {
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    if (!(kept >> min(31, (e0 + i) / gsize) & 1u)) key[i] = 0u;
+            }
         }
 
-        // the picks: lane j keeps the j-th largest key
-        uint32_t mine = 0;
+        // the picks: lane j keeps the j-th largest key, whose it is and its place in that lane's list
+        uint32_t mine;
+        {
+            uint32_t v[NV];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) mine = max(mine, key[i]);
+            for (int i = 0; i < NV; ++i) v[i] = key[i];
+            sort_down(v);
+            mine = v[0];
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < NV; ++i) list[i] = v[i];
+#pragma unroll
+            for (int i = 0; i < NV; ++i) sk[i * 32 + lane] = key[i];
+            __syncwarp();
+        }
         uint32_t pick_key = 0;
-        int pick = -1, n = 0;
-        auto next_pick = [&]() -> uint32_t {
+        int from = 0, place = 0, taken = 0, n = 0;
+        auto next_pick = [&]() {  // false: none is left
             const uint32_t top = warp_max(mine);
-            if (top == 0u) return 0u;
+            if (top == 0u) return false;
             const int owner = __ffs(__ballot_sync(FULL_MASK, mine == top)) - 1;
-            int at = 0;
-            if (lane == owner) {
-                bool gone = false;
-                mine = 0;
-#pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    if (!gone && key[i] == top) {
-                        gone = true;
-                        at = e0 + i;
-                        key[i] = 0u;
-                    }
-                    mine = max(mine, key[i]);
-                }
-            }
-            at = __shfl_sync(FULL_MASK, at, owner);
-            if (lane == n) pick_key = top, pick = at;
+            const int at = __shfl_sync(FULL_MASK, taken, owner);
+            if (lane == owner) mine = list[++taken];
+            if (lane == n) pick_key = top, from = owner, place = at;
             ++n;
-            return top;
+            return true;
+        };
+        // the expert of this lane's pick: keys of a lane's list that are equal
+        // come in the order of their experts
+        auto expert = [&]() {
+            int above = 0;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) above += sk[i * 32 + from] > pick_key;
+            int skip = place - above, e = -1;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (sk[i * 32 + from] == pick_key && skip-- == 0) e = from * NV + i;
+            return e;
         };
         const int want = same_bias ? k : min(k + 1, 32);
         while (n < want && next_pick()) {
         }
+        int pick = lane < n ? expert() : -1;
         float px = pick >= 0 ? logit_at<DT>(row, pick) : 0.f;
         if (!same_bias && n > 1) {
             // neighbours within tau of each other that are not the same values
@@ -238,24 +345,23 @@ __global__ void __launch_bounds__(RG_WARPS * 32) router_grouped_kernel(const __g
             const float tau = 2.f * tau_s + 0x1p-22f * fmaxf(fabsf(f), fabsf(f0));
             const bool close = lane > 0 && lane < n && f0 - f <= tau;
             bool look = __any_sync(FULL_MASK, close && !(px == x0 && pb == b0));
+            const float fk = __shfl_sync(FULL_MASK, f, min(k, n) - 1);
+            const float edge = fk - (2.f * tau_s + 0x1p-22f * fabsf(fk));  // what may belong before the k-th
             if (!look && k < 32 && (__ballot_sync(FULL_MASK, close) >> k & 1u)) {
                 // the last one in and the first one out are the same values: anything else as near?
-                const float fk = __shfl_sync(FULL_MASK, f, k), xk = __shfl_sync(FULL_MASK, px, k), bk = __shfl_sync(FULL_MASK, pb, k);
+                const float xk = __shfl_sync(FULL_MASK, px, k), bk = __shfl_sync(FULL_MASK, pb, k);
 #pragma unroll
-                for (int i = 0; i < NV; ++i)
-                    if (key[i] != 0u && fk - unordered(key[i]) <= 2.f * tau_s + 0x1p-22f * fabsf(fk) &&
-                        !(x[i] == xk && bias[i] == bk))
-                        look = true;
+                for (int i = 0; i < NV; ++i) {
+                    const float fi = unordered(key[i]);
+                    if (key[i] != 0u && fi <= fk && fi >= edge && !(x[i] == xk && bias[i] == bk)) look = true;
+                }
                 look = __any_sync(FULL_MASK, look);
             } else if (!look && k == 32 && n == 32) {  // (no lane is left for the first one out)
-                const float fk = __shfl_sync(FULL_MASK, f, 31);
                 const uint32_t top = warp_max(mine);
-                look = top != 0u && fk - unordered(top) <= 2.f * tau_s + 0x1p-22f * fabsf(fk);
+                look = top != 0u && unordered(top) >= edge;
             }
             if (look) {
-                // candidates: all within tau of the k-th
-                float fk = unordered(__shfl_sync(FULL_MASK, pick_key, min(k, n) - 1));
-                float edge = fk - (2.f * tau_s + 0x1p-22f * fabsf(fk));
+                // candidates: all from the edge on
                 bool full = false;
                 while (true) {
                     const uint32_t top = warp_max(mine);
@@ -268,6 +374,7 @@ __global__ void __launch_bounds__(RG_WARPS * 32) router_grouped_kernel(const __g
                 }
                 row64();
                 if (!full) {
+                    pick = lane < n ? expert() : -1;
                     double d = -INFINITY;
                     if (pick >= 0) d = score64(a, logit_at<DT>(row, pick), m64, total64) + (double)a.bias[pick];
                     int rank = 0;
@@ -277,22 +384,16 @@ __global__ void __launch_bounds__(RG_WARPS * 32) router_grouped_kernel(const __g
                         rank += o > d || (o == d && oi < pick);
                     }
                     // lane `rank` takes it
-                    int from = lane;
+                    int src = lane;
                     for (int j = 0; j < n; ++j)
-                        if (__shfl_sync(FULL_MASK, rank, j) == lane && lane < n) from = j;
-                    pick = __shfl_sync(FULL_MASK, pick, from);
+                        if (__shfl_sync(FULL_MASK, rank, j) == lane && lane < n) src = j;
+                    pick = __shfl_sync(FULL_MASK, pick, src);
                 } else {
                     // more than 32 candidates: every key of the row in 64 bits, k passes over them
-                    __syncwarp();
-#pragma unroll
-                    for (int i = 0; i < NV; ++i) sk[e0 + i] = key[i] == 0u ? 0.f : 1.f;
-                    __syncwarp();
-                    if (pick >= 0) sk[pick] = 1.f;
-                    __syncwarp();
                     double d[NV];
 #pragma unroll
                     for (int i = 0; i < NV; ++i)
-                        d[i] = sk[e0 + i] == 0.f ? -INFINITY : score64(a, x[i], m64, total64) + (double)bias[i];
+                        d[i] = key[i] == 0u ? -INFINITY : score64(a, x[i], m64, total64) + (double)bias[i];
                     pick = -1;
                     for (int j = 0; j < k; ++j) {
                         double bd = -INFINITY;
@@ -341,9 +442,10 @@ __global__ void __launch_bounds__(RG_WARPS * 32) router_grouped_kernel(const __g
 
 template <int NV, int DT>
 static cudaError_t launch_rg(const RouterGroupedArgs& a, const DeviceInfo& di, cudaStream_t st) {
-    const int64_t blocks = (a.T + RG_WARPS - 1) / RG_WARPS;
-    return launch_after(router_grouped_kernel<NV, DT>, dim3((unsigned)std::min<int64_t>(blocks, di.sm_count * 8)),
-                        RG_WARPS * 32, 0, st, a);
+    constexpr int WARPS = rg_warps(NV);
+    const int64_t blocks = (a.T + WARPS - 1) / WARPS;
+    return launch_after(router_grouped_kernel<NV, DT>, dim3((unsigned)std::min<int64_t>(blocks, di.sm_count * 8)), WARPS * 32,
+                        0, st, a);
 }
 
 template <int DT>
@@ -359,6 +461,8 @@ cudaError_t launch_router_grouped(RouterGroupedArgs a, int dtype, cudaStream_t s
     const cudaError_t e = device_info(&di);
     if (e != cudaSuccess) return e;
     a.err = di.err_word;
+    const int64_t four = dtype == MOE_F32 ? 16 : 8;  // bytes
+    a.vec = a.E % 4 == 0 && a.stride % 4 == 0 && reinterpret_cast<uintptr_t>(a.logits) % four == 0;
     if (dtype == MOE_F32) return launch_rg_dt<MOE_F32>(a, di, st);
     return dtype == MOE_BF16 ? launch_rg_dt<MOE_BF16>(a, di, st) : launch_rg_dt<MOE_F16>(a, di, st);
 }
