@@ -61,8 +61,10 @@ constexpr int px_code_stages(int db, bool e4) { return !e4 ? 0 : db == 1 ? 3 : 2
 // two before that is over.
 constexpr int px_masks(int db, bool e4) { return px_stages(db, e4) + px_code_stages(db, e4) + 4; }
 
+constexpr int PX_PAGES = 2048;  // entries of a block's part of the page table that shared memory holds
+
 struct PxLayout {
-    uint32_t k, v, codes, koff, voff, live, back, bars, slot, abort, total;
+    uint32_t k, v, codes, pages, koff, voff, live, back, bars, slot, abort, total;
 };
 constexpr PxLayout px_layout(int db, bool e4) {
     PxLayout L{};
@@ -70,6 +72,7 @@ constexpr PxLayout px_layout(int db, bool e4) {
     L.k = off;     off += px_stages(db, e4) * px_half(db);
     L.v = off;     off += px_stages(db, e4) * px_half(db);
     L.codes = off; off += 2 * px_code_stages(db, e4) * (px_half(db) / 2);
+    L.pages = off; off += PX_PAGES * 4;
     L.koff = off;  off += 2 * 128 * 8;
     L.voff = off;  off += 2 * 128 * 8;
     L.live = off;  off += px_masks(db, e4) * 16;
@@ -230,6 +233,15 @@ __device__ __forceinline__ float2 rest2(float2 p, uint32_t h) {
             : "f"(p.x), "f"(p.y), "r"(h));
     return r;
 }
+// With the lane `bit` away: a lane whose bit is clear gives b and gets the
+// other's a in its place, the other one the reverse.
+__device__ __forceinline__ void exchange(uint32_t& a, uint32_t& b, bool upper, int bit) {
+    const uint32_t got = __shfl_xor_sync(FULL_MASK, upper ? a : b, bit);
+    if (upper)
+        a = got;
+    else
+        b = got;
+}
 __device__ __forceinline__ float finite_or_zero(float m) { return m == -INFINITY ? 0.f : m; }
 // The barrier gets an arrival of this thread when its copies so far have landed.
 __device__ __forceinline__ void arrive_after_copies(uint64_t* bar) {
@@ -344,15 +356,20 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attention_kernel(const _
         const int per = CH <= 8 ? 8 : CH <= 16 ? 16 : 32;  // lanes of a row
         const int c = lane & (per - 1);
         auto place = [&](int r) { return sm + ((r >> 7) * DB + (c >> 3)) * (PX_ROWS * 128) + swz(r & 127, c & 7); };
-        auto source = [&](int row) {
-            const int b = row / a.G, h = kvh * a.G + (row - b * a.G);
-            return static_cast<const uint16_t*>(a.q) + (int64_t)b * a.q_sb + (int64_t)h * a.q_sh + c * 8;
+        const int rstep = PX_SOFT * 32 / per, db = rstep / a.G, dg = rstep - db * a.G;
+        int b = (row0 + tid / per) / a.G, g = row0 + tid / per - b * a.G;  // of the next row
+        auto next_source = [&]() {
+            const uint16_t* const at = static_cast<const uint16_t*>(a.q) + b * a.q_sb + (kvh * a.G + g) * a.q_sh + c * 8;
+            b += db, g += dg;
+            if (g >= a.G) g -= a.G, ++b;
+            return at;
         };
         if constexpr (E4 && QBF) {
 #pragma unroll 8
-            for (int r = tid / per; r < MT * PX_ROWS; r += PX_SOFT * 32 / per) {
+            for (int r = tid / per; r < MT * PX_ROWS; r += rstep) {
                 uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                if (row0 + r < R && c < CH) v = ld_128_l2(source(row0 + r));
+                const uint16_t* const from = next_source();
+                if (row0 + r < R && c < CH) v = ld_128_l2(from);
                 uint32_t w[4] = {v.x, v.y, v.z, v.w};
                 float amax = 0.f;
 #pragma unroll
@@ -375,11 +392,11 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attention_kernel(const _
             }
             mbar_arrive(q_full);
         } else {
-            for (int r = tid / per; r < MT * PX_ROWS; r += PX_SOFT * 32 / per)
-                if (c < CH) {
-                    const bool have = row0 + r < R;
-                    cp_async_16_zfill(place(r), have ? source(row0 + r) : a.q, have ? 16 : 0);
-                }
+            for (int r = tid / per; r < MT * PX_ROWS; r += rstep) {
+                const bool have = row0 + r < R;
+                const uint16_t* const from = next_source();
+                if (c < CH) cp_async_16_zfill(place(r), have ? from : a.q, have ? 16 : 0);
+            }
             arrive_after_copies(q_full);
         }
     }
@@ -444,6 +461,7 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attention_kernel(const _
         if (NS == 2 || warp < 4) {
             const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
             const uint32_t o_at = tmem + lanes + 256 + s * 128;
+            constexpr int HC = KT / 64;  // chunks of 32 keys in half a tile
             float m = -INFINITY;  // m: a whole number, so that its steps scale exactly
             float2 l2 = make_float2(0.f, 0.f);
             int c = 0;            // jobs of this stream so far
@@ -459,33 +477,48 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attention_kernel(const _
                 fence_after();
                 const uint32_t s_at = tmem + lanes + (j & 1) * 128;
                 const uint32_t* mask = live + (t % MASKS) * 4;
-                // 32 keys, read a chunk ahead, become weights in their place
-                auto weights = [&](int i, uint32_t(&x)[32]) {
+                // half of the tile's keys at a time become weights in their
+                // place (a round trip to tensor memory, a maximum and a vote
+                // take some 300 cycles whatever they are of)
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t h_at = s_at + h * (KT / 2);
+                    uint32_t x[HC][32];
+#pragma unroll
+                    for (int i = 0; i < HC; ++i) tm_ld32(h_at + i * 32, x[i]);
+#pragma unroll
+                    for (int i = 0; i < HC; ++i) tm_wait32(x[i]);
                     if (flip)
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) x[e] ^= 0x80000000u;
-                    const uint32_t on = mask[i];
-                    if (on != FULL_MASK)
+                        for (int i = 0; i < HC; ++i)
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) x[e] = on >> e & 1u ? x[e] : 0xff800000u;
-                    float m0 = __uint_as_float(x[0]), m1 = __uint_as_float(x[1]);
+                            for (int e = 0; e < 32; ++e) x[i][e] ^= 0x80000000u;
+                    float mx = -INFINITY;
 #pragma unroll
-                    for (int e = 2; e < 30; e += 4) {
-                        m0 = max3(m0, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-                        m1 = max3(m1, __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
+                    for (int i = 0; i < HC; ++i) {
+                        const uint32_t on = mask[h * HC + i];
+                        if (on != FULL_MASK)
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) x[i][e] = on >> e & 1u ? x[i][e] : 0xff800000u;
+                        float m0 = __uint_as_float(x[i][0]), m1 = __uint_as_float(x[i][1]);
+#pragma unroll
+                        for (int e = 2; e < 30; e += 4) {
+                            m0 = max3(m0, __uint_as_float(x[i][e]), __uint_as_float(x[i][e + 1]));
+                            m1 = max3(m1, __uint_as_float(x[i][e + 2]), __uint_as_float(x[i][e + 3]));
+                        }
+                        m0 = max3(m0, __uint_as_float(x[i][30]), __uint_as_float(x[i][31]));
+                        mx = max3(mx, m0, m1);
                     }
-                    const float mx = max3(m0, m1, fmaxf(__uint_as_float(x[30]), __uint_as_float(x[31]))) * sl;
+                    mx *= sl;
                     if (__any_sync(FULL_MASK, mx > m + SLACK)) {
-                        // m moves up: so do l, O as far as it goes, and the weights of this half
+                        // m moves up: so do l and O as far as it goes
                         const float mn = fmaxf(m, ceilf(mx));
                         const float f = exp2_fast(m - finite_or_zero(mn));
                         m = mn;
                         l2.x *= f, l2.y *= f;
-                        constexpr int HC = KT / 64;  // chunks of a half
-                        const bool second = i >= HC;
-                        if (second || c > 0) {
-                            ok = ok && __all_sync(FULL_MASK, second ? mbar_wait_abort(&h_done[s], c & 1, abort)
-                                                                    : mbar_wait_abort(&o_done[s], (c - 1) & 1, abort));
+                        if (h || c > 0) {
+                            ok = ok && __all_sync(FULL_MASK, h ? mbar_wait_abort(&h_done[s], c & 1, abort)
+                                                               : mbar_wait_abort(&o_done[s], (c - 1) & 1, abort));
                             fence_after();
                             for (int d = 0; d < D; d += 16) {
                                 uint32_t w[16];
@@ -495,64 +528,32 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attention_kernel(const _
                                 tm_st16(o_at + d, w);
                             }
                         }
-                        if (HC == 2 && (i & 1))
-                            for (int d = 0; d < 32; d += 16) {
-                                uint32_t w[16];
-                                tm_ld16(s_at + (i - 1) * 32 + d, w);
-#pragma unroll
-                                for (int e = 0; e < 16; ++e) {
-                                    const float2 u = unpack2<BF>(w[e]);
-                                    w[e] = pack2<BF>(u.x * f, u.y * f);
-                                }
-                                tm_st16(s_at + (i - 1) * 32 + d, w);
-                            }
                     }
                     const float mu = finite_or_zero(m) - P_SHIFT;
-                    uint32_t w[LO ? 32 : 16];
                     const float2 sl2 = make_float2(sl, sl), mu2 = make_float2(-mu, -mu);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        float2 p = __ffma2_rn(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), sl2, mu2);
-                        p = make_float2(exp2_fast(p.x), exp2_fast(p.y));
-                        l2 = __fadd2_rn(l2, p);
-                        w[e] = pack2<BF>(p.x, p.y);
-                        if constexpr (LO) {
-                            const float2 r = rest2<BF>(p, w[e]);
-                            w[16 + e] = pack2<BF>(r.x, r.y);
+                    for (int i = 0; i < HC; ++i) {
+                        uint32_t w[LO ? 32 : 16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            float2 p = __ffma2_rn(make_float2(__uint_as_float(x[i][2 * e]), __uint_as_float(x[i][2 * e + 1])), sl2, mu2);
+                            p = make_float2(exp2_fast(p.x), exp2_fast(p.y));
+                            l2 = __fadd2_rn(l2, p);
+                            w[e] = pack2<BF>(p.x, p.y);
+                            if constexpr (LO) {
+                                const float2 r = rest2<BF>(p, w[e]);
+                                w[16 + e] = pack2<BF>(r.x, r.y);
+                            }
                         }
+                        if constexpr (LO)
+                            tm_st32(h_at + i * 32, w);
+                        else
+                            tm_st16(h_at + i * 32, w);
                     }
-                    if constexpr (LO)
-                        tm_st32(s_at + i * 32, w);
-                    else
-                        tm_st16(s_at + i * 32, w);
-                };
-                auto half_done = [&](int h) {
                     wait_st();
                     fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&p_full[2 * (j & 1) + h]);
-                };
-                uint32_t x[32], y[32];
-                tm_ld32(s_at, x);
-                if constexpr (KT == 128) {
-#pragma unroll 1
-                    for (int h = 0; h < 2; ++h) {
-                        tm_wait32(x);
-                        tm_ld32(s_at + h * 64 + 32, y);
-                        weights(2 * h, x);
-                        tm_wait32(y);
-                        if (h == 0) tm_ld32(s_at + 64, x);
-                        weights(2 * h + 1, y);
-                        half_done(h);
-                    }
-                } else {
-                    tm_wait32(x);
-                    tm_ld32(s_at + 32, y);
-                    weights(0, x);
-                    half_done(0);
-                    tm_wait32(y);
-                    weights(1, y);
-                    half_done(1);
                 }
             }
             const float l = l2.x + l2.y;
@@ -566,17 +567,39 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attention_kernel(const _
             if (ok && c > 0) {
                 fence_after();
                 float* out = a.ws_o + at * D;
-                for (int d = 0; d < D; d += 16) {
-                    uint32_t o[16];
-                    tm_ld16(o_at + d, o);
-                    if (row < R) {
+                // (32 rows of 32 bytes are 32 lines to the load-store unit; four
+                // lanes exchange their blocks and write one row's 128 bytes)
+                const int lane0 = row - (lane & 3);
+                for (int d = 0; d < D; d += 32) {
+                    uint32_t o[32];
+                    if (d + 32 <= D) {
+                        tm_ld32(o_at + d, o);
+                        tm_wait32(o);
+                    } else {
+                        uint32_t u[16];
+                        tm_ld16(o_at + d, u);
 #pragma unroll
-                        for (int e = 0; e < 16; e += 8)  // whole sectors
-                            asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(out + d + e), "r"(o[e]),
-                                         "r"(o[e + 1]), "r"(o[e + 2]), "r"(o[e + 3]), "r"(o[e + 4]), "r"(o[e + 5]),
-                                         "r"(o[e + 6]), "r"(o[e + 7])
-                                         : "memory");
+                        for (int e = 0; e < 16; ++e) o[e] = u[e], o[16 + e] = 0u;
                     }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        exchange(o[e], o[8 + e], lane & 1, 1);
+                        exchange(o[16 + e], o[24 + e], lane & 1, 1);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        exchange(o[e], o[16 + e], lane & 2, 2);
+                        exchange(o[8 + e], o[24 + e], lane & 2, 2);
+                    }
+                    // block n is now row lane0 + n's dims d + 8 (lane & 3) ..
+                    const int dim = d + 8 * (lane & 3);
+#pragma unroll
+                    for (int n = 0; n < 4; ++n)
+                        if (lane0 + n < R && dim < D)
+                            asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(out + (n - (lane & 3)) * D + dim),
+                                         "r"(o[8 * n]), "r"(o[8 * n + 1]), "r"(o[8 * n + 2]), "r"(o[8 * n + 3]),
+                                         "r"(o[8 * n + 4]), "r"(o[8 * n + 5]), "r"(o[8 * n + 6]), "r"(o[8 * n + 7])
+                                         : "memory");
                 }
             }
         }
@@ -593,27 +616,30 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attention_kernel(const _
         const int64_t sp = (is_v ? a.v_sp : a.k_sp) * ES, stt = (is_v ? a.v_st : a.k_st) * ES;
         const uint8_t* const src = static_cast<const uint8_t*>(is_v ? a.v : a.k) + (int64_t)kvh * (is_v ? a.v_sh : a.k_sh) * ES;
 
-        // Thread i finds the rows of keys i, i + 64, a tile ahead of their use.
-        int pg[KEYS], off[KEYS];
-        auto find = [&](int t) {
-            if (t >= tiles) return;
-#pragma unroll
-            for (int i = 0; i < KEYS; ++i) {
-                const int key = min((tile0 + t) * KT + i * PX_BRING + pt, a.len - 1);
-                const int pi = (int)(((uint64_t)(uint32_t)key * a.page_mul) >> a.page_shift);
-                off[i] = key - pi * a.page;
-                pg[i] = __ldcg(a.table + pi);
-            }
-        };
-        // Offsets of tile t's rows (-1: not live) to all that bring.
+        // The block's part of the page table, so that no tile waits for a
+        // lookup (where it is too long, of many small pages, they are read tile
+        // by tile)
+        int32_t* const pages = reinterpret_cast<int32_t*>(sm + L.pages);
+        auto page_of = [&](int key) { return (int)(((uint64_t)(uint32_t)key * a.page_mul) >> a.page_shift); };
+        const int page0 = page_of(tile0 * KT);
+        const int n_pages = page_of(min((tile0 + tiles) * KT, a.len) - 1) - page0 + 1;
+        const bool held = n_pages <= PX_PAGES;
+        if (held) {
+            for (int i = tid - PX_KW * 32; i < n_pages; i += 2 * PX_BRING) pages[i] = __ldcg(a.table + page0 + i);
+            asm volatile("bar.sync 3, %0;" ::"n"(2 * PX_BRING) : "memory");
+        }
+        // Offsets of tile t's rows (far below 0: not live) to all that bring.
         auto publish = [&](int t) {
 #pragma unroll
             for (int i = 0; i < KEYS; ++i) {
-                const bool known = pg[i] >= 0 && pg[i] < a.num_pages;
-                if (!known) atomicOr(a.err, MOE_DEVERR_PAGE);
                 const int at = i * PX_BRING + pt;
+                const int key = min((tile0 + t) * KT + at, a.len - 1);
+                const int pi = page_of(key);
+                const int pg = held ? pages[pi - page0] : __ldcg(a.table + pi);
+                const bool known = pg >= 0 && pg < a.num_pages;
+                if (!known) atomicOr(a.err, MOE_DEVERR_PAGE);
                 const bool have = known && (tile0 + t) * KT + at < a.len;
-                offs[(t & 1) * 128 + at] = have ? pg[i] * sp + off[i] * stt : -1;
+                offs[(t & 1) * 128 + at] = have ? pg * sp + (key - pi * a.page) * stt : -(int64_t(1) << 40);
                 const uint32_t word = __ballot_sync(FULL_MASK, have);
                 if (!is_v && lane == 0) live[(t % MASKS) * 4 + (at >> 5)] = word;
             }
@@ -622,7 +648,6 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attention_kernel(const _
             else
                 bringers_sync<1>();
         };
-        find(0);
         bool ok = true;
         if constexpr (!E4) {
             const int CH = D / 8, per = PX_BRING / CH;  // rows that the two warps copy at once
@@ -630,17 +655,23 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attention_kernel(const _
             const uint32_t col = (c >> 3) * (KT * 128);
             for (int t = 0; t < tiles; ++t) {
                 publish(t);
-                find(t + 1);
                 const int st = t % ST;
                 if (t >= ST && ok) ok = __all_sync(FULL_MASK, mbar_wait_abort(&empty[st], ((t / ST) - 1) & 1, abort));
                 if (!ok) continue;  // (the two warps stay together at publish)
                 uint8_t* const dst = ring + st * HALF + col;
                 const int64_t* const o = offs + (t & 1) * 128;
+                // (eight rows' offsets are read before their copies, which order
+                // the shared memory accesses around them)
                 if (r0 < per)
-#pragma unroll 8
-                    for (int row = r0; row < KT; row += per) {
-                        const int64_t at = o[row];
-                        cp_async_16_zfill(dst + swz(row, c & 7), src + (at < 0 ? 0 : at) + c * 16, at < 0 ? 0 : 16);
+                    for (int row = r0; row < KT; row += 8 * per) {
+                        int64_t at[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) at[i] = o[min(row + i * per, KT - 1)];  // (no branch: all at once)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (row + i * per < KT)
+                                cp_async_16_zfill(dst + swz(row + i * per, c & 7), src + (at[i] < 0 ? 0 : at[i]) + c * 16,
+                                                  at[i] < 0 ? 0 : 16);
                     }
                 arrive_after_copies(&full[st]);
             }
@@ -659,18 +690,21 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attention_kernel(const _
             auto copy = [&](int t) {
                 if (t < tiles) {
                     publish(t);
-                    find(t + 1);
                     const int64_t* const o = offs + (t & 1) * 128;
                     uint8_t* const to = codes + (t % RS) * (HALF / 2);
                     int row = row0, c = c0;
+                    // (the offsets are read before the copies, which order the
+                    // accesses around them, and without branches: all at once)
+                    int64_t at[PER];
 #pragma unroll
                     for (int i = 0; i < PER; ++i) {
-                        if (row < KT) {
-                            const int64_t at = o[row];
-                            cp_async_16_zfill(to + i * (PX_BRING * 16), src + (at < 0 ? 0 : at) + c * 16, at < 0 ? 0 : 16);
-                        }
+                        at[i] = o[min(row, KT - 1)] + (row < KT ? c * 16 : 0);  // (negative stays so)
+                        at[i] = row < KT ? at[i] : -1;
                         step(row, c);
                     }
+#pragma unroll
+                    for (int i = 0; i < PER; ++i)
+                        cp_async_16_zfill(to + i * (PX_BRING * 16), src + max(at[i], (int64_t)0), at[i] < 0 ? 0 : 16);
                 }
                 cp_async_commit();
             };
@@ -685,20 +719,26 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attention_kernel(const _
                 const uint8_t* const from = codes + (t % RS) * (HALF / 2);
                 uint8_t* const dst = ring + st * HALF;
                 int row = row0, c = c0;
+                constexpr int BATCH = PER < 8 ? PER : 8;  // pieces that are read before any of them is written
 #pragma unroll
-                for (int i = 0; i < PER; ++i) {
-                    if (row < KT) {
-                        const uint4 x = *reinterpret_cast<const uint4*>(from + i * (PX_BRING * 16));
+                for (int i0 = 0; i0 < PER; i0 += BATCH) {
+                    uint4 x[BATCH];
+#pragma unroll
+                    for (int i = 0; i < BATCH; ++i) x[i] = *reinterpret_cast<const uint4*>(from + (i0 + i) * (PX_BRING * 16));
+#pragma unroll
+                    for (int i = 0; i < BATCH; ++i) {
                         uint32_t w[8];
-                        e4m3x4_to_f16(x.x, w[0], w[1]);
-                        e4m3x4_to_f16(x.y, w[2], w[3]);
-                        e4m3x4_to_f16(x.z, w[4], w[5]);
-                        e4m3x4_to_f16(x.w, w[6], w[7]);
-                        uint8_t* const d = dst + (c >> 2) * (KT * 128);
-                        *reinterpret_cast<uint4*>(d + swz(row, (2 * c) & 7)) = make_uint4(w[0], w[1], w[2], w[3]);
-                        *reinterpret_cast<uint4*>(d + swz(row, (2 * c + 1) & 7)) = make_uint4(w[4], w[5], w[6], w[7]);
+                        e4m3x4_to_f16(x[i].x, w[0], w[1]);
+                        e4m3x4_to_f16(x[i].y, w[2], w[3]);
+                        e4m3x4_to_f16(x[i].z, w[4], w[5]);
+                        e4m3x4_to_f16(x[i].w, w[6], w[7]);
+                        if (row < KT) {
+                            uint8_t* const d = dst + (c >> 2) * (KT * 128);
+                            *reinterpret_cast<uint4*>(d + swz(row, (2 * c) & 7)) = make_uint4(w[0], w[1], w[2], w[3]);
+                            *reinterpret_cast<uint4*>(d + swz(row, (2 * c + 1) & 7)) = make_uint4(w[4], w[5], w[6], w[7]);
+                        }
+                        step(row, c);
                     }
-                    step(row, c);
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&full[st]);
