@@ -29,6 +29,7 @@
 // Bound: HBM for few rows (the prefix once), the tensor pipe and the softmax
 // for many.
 #include <algorithm>
+#include <type_traits>
 
 #include "block_common.cuh"
 #include "decode_common.cuh"
@@ -56,15 +57,15 @@ constexpr int px_half(int db) { return db * px_keys(db) * 128; }  // bytes of a 
 // when the softmax between two uses is over.
 constexpr int px_stages(int db, bool e4) { return db == 1 ? (e4 ? 2 : 4) : (e4 ? 1 : 2); }
 constexpr int px_code_stages(int db, bool e4) { return !e4 ? 0 : db == 1 ? 3 : 2; }
-// Masks of live keys that are kept: when tile t's is written, the scores of
-// tile t - (both kinds of stages) have been issued, so the softmax of the tile
-// two before that is over.
+// Masks of live keys that are kept: when tile t's is written, the scores of the
+// tile a stage count before it have been issued, so the softmax of the tile two
+// before that is over.
 constexpr int px_masks(int db, bool e4) { return px_stages(db, e4) + px_code_stages(db, e4) + 4; }
 
-constexpr int PX_PAGES = 2048;  // entries of a block's part of the page table that shared memory holds
+constexpr int PX_PAGES = 1024;  // pages, of K and of V, whose places shared memory holds
 
 struct PxLayout {
-    uint32_t k, v, codes, pages, koff, voff, live, back, bars, slot, abort, total;
+    uint32_t k, v, codes, pages, rows, live, back, bars, slot, abort, total;
 };
 constexpr PxLayout px_layout(int db, bool e4) {
     PxLayout L{};
@@ -72,9 +73,8 @@ constexpr PxLayout px_layout(int db, bool e4) {
     L.k = off;     off += px_stages(db, e4) * px_half(db);
     L.v = off;     off += px_stages(db, e4) * px_half(db);
     L.codes = off; off += 2 * px_code_stages(db, e4) * (px_half(db) / 2);
-    L.pages = off; off += PX_PAGES * 4;
-    L.koff = off;  off += 2 * 128 * 8;
-    L.voff = off;  off += 2 * 128 * 8;
+    L.pages = off; off += 2 * PX_PAGES * 8;
+    L.rows = off;  off += 2 * 2 * 128 * 8;
     L.live = off;  off += px_masks(db, e4) * 16;
     L.back = off;  off += 2 * PX_ROWS * 4;
     L.bars = off;  off += (4 * px_stages(db, e4) + 12) * 8;
@@ -254,11 +254,6 @@ __device__ __forceinline__ uint4 ld_128_l2(const void* p) {
     asm volatile("ld.global.cg.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p) : "memory");
     return r;
 }
-template <int ID>
-__device__ __forceinline__ void bringers_sync() {
-    asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(PX_BRING) : "memory");
-}
-
 }  // namespace
 
 // A block: one key-value head, one group of row tiles, one run of key tiles.
@@ -321,7 +316,7 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attention_kernel(const _
 
     if (tid == 0) {
         for (int i = 0; i < ST; ++i) {
-            mbar_init(&k_full[i], E4 ? 2 : PX_BRING);
+            mbar_init(&k_full[i], E4 ? 2 : PX_BRING + 2);
             mbar_init(&k_empty[i], 1);
             mbar_init(&v_full[i], E4 ? 2 : PX_BRING);
             mbar_init(&v_empty[i], 1);
@@ -609,141 +604,180 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attention_kernel(const _
         const int pt = tid - (is_v ? PX_VW : PX_KW) * 32;  // 0 .. 63
         uint64_t* const full = is_v ? v_full : k_full;
         uint64_t* const empty = is_v ? v_empty : k_empty;
-        int64_t* const offs = reinterpret_cast<int64_t*>(sm + (is_v ? L.voff : L.koff));
         uint8_t* const ring = sm + (is_v ? L.v : L.k);
         constexpr int ES = E4 ? 1 : 2;
-        constexpr int KEYS = KT / PX_BRING;  // keys a thread looks up
         const int64_t sp = (is_v ? a.v_sp : a.k_sp) * ES, stt = (is_v ? a.v_st : a.k_st) * ES;
         const uint8_t* const src = static_cast<const uint8_t*>(is_v ? a.v : a.k) + (int64_t)kvh * (is_v ? a.v_sh : a.k_sh) * ES;
 
-        // The block's part of the page table, so that no tile waits for a
-        // lookup (where it is too long, of many small pages, they are read tile
-        // by tile)
-        int32_t* const pages = reinterpret_cast<int32_t*>(sm + L.pages);
+        // The places of the next pages, so that no tile waits for a lookup: a
+        // window of the page table that moves on when a tile passes its end.
+        // (Reading the rows' places below has no branch: all at once.)
+        constexpr int64_t NONE = INT64_MIN;
+        int64_t* const places = reinterpret_cast<int64_t*>(sm + L.pages) + (is_v ? PX_PAGES : 0);
         auto page_of = [&](int key) { return (int)(((uint64_t)(uint32_t)key * a.page_mul) >> a.page_shift); };
-        const int page0 = page_of(tile0 * KT);
-        const int n_pages = page_of(min((tile0 + tiles) * KT, a.len) - 1) - page0 + 1;
-        const bool held = n_pages <= PX_PAGES;
-        if (held) {
-            for (int i = tid - PX_KW * 32; i < n_pages; i += 2 * PX_BRING) pages[i] = __ldcg(a.table + page0 + i);
-            asm volatile("bar.sync 3, %0;" ::"n"(2 * PX_BRING) : "memory");
-        }
-        // Offsets of tile t's rows (far below 0: not live) to all that bring.
-        auto publish = [&](int t) {
-#pragma unroll
-            for (int i = 0; i < KEYS; ++i) {
-                const int at = i * PX_BRING + pt;
-                const int key = min((tile0 + t) * KT + at, a.len - 1);
-                const int pi = page_of(key);
-                const int pg = held ? pages[pi - page0] : __ldcg(a.table + pi);
+        const int key0 = tile0 * KT, key_end = min((tile0 + tiles) * KT, a.len), last_page = page_of(key_end - 1);
+        int page0 = 0, held_to = -1;  // pages page0 .. held_to
+        auto together = [&]() {
+            if (is_v)
+                asm volatile("bar.sync 2, %0;" ::"n"(PX_BRING) : "memory");
+            else
+                asm volatile("bar.sync 1, %0;" ::"n"(PX_BRING) : "memory");
+        };
+        auto hold_pages = [&](int t) {  // those of tile t
+            const int first = key0 + t * KT;
+            if (page_of(min(first + KT, key_end) - 1) <= held_to) return;
+            together();
+            page0 = page_of(first);
+            held_to = min(page0 + PX_PAGES - 1, last_page);
+            for (int i = page0 + pt; i <= held_to; i += PX_BRING) {
+                const int pg = __ldcg(a.table + i);
                 const bool known = pg >= 0 && pg < a.num_pages;
                 if (!known) atomicOr(a.err, MOE_DEVERR_PAGE);
-                const bool have = known && (tile0 + t) * KT + at < a.len;
-                offs[(t & 1) * 128 + at] = have ? pg * sp + (key - pi * a.page) * stt : -(int64_t(1) << 40);
-                const uint32_t word = __ballot_sync(FULL_MASK, have);
-                if (!is_v && lane == 0) live[(t % MASKS) * 4 + (at >> 5)] = word;
+                places[i - page0] = known ? pg * sp : NONE;
             }
-            if (is_v)
-                bringers_sync<2>();
-            else
-                bringers_sync<1>();
+            together();
         };
-        bool ok = true;
-        if constexpr (!E4) {
-            const int CH = D / 8, per = PX_BRING / CH;  // rows that the two warps copy at once
-            const int c = pt % CH, r0 = pt / CH;
-            const uint32_t col = (c >> 3) * (KT * 128);
-            for (int t = 0; t < tiles; ++t) {
-                publish(t);
-                const int st = t % ST;
-                if (t >= ST && ok) ok = __all_sync(FULL_MASK, mbar_wait_abort(&empty[st], ((t / ST) - 1) & 1, abort));
-                if (!ok) continue;  // (the two warps stay together at publish)
-                uint8_t* const dst = ring + st * HALF + col;
-                const int64_t* const o = offs + (t & 1) * 128;
-                // (eight rows' offsets are read before their copies, which order
-                // the shared memory accesses around them)
-                if (r0 < per)
-                    for (int row = r0; row < KT; row += 8 * per) {
-                        int64_t at[8];
+        auto place_of = [&](int key) {  // bytes from the head's first row; NONE behind the end
+            const int pi = page_of(min(key, key_end - 1));
+            const int64_t at = places[pi - page0];
+            const int64_t row = at + (int64_t)((uint64_t)(uint32_t)(key - pi * a.page) * (uint64_t)stt);
+            return key < key_end && at != NONE ? row : NONE;
+        };
+        // Tile t's rows, found once for the lanes that share them; and by the K
+        // warps the masks of those that are live.
+        int64_t* const rows_of = reinterpret_cast<int64_t*>(sm + L.rows) + (is_v ? 256 : 0);
+        auto find_rows = [&](int t) {
+            hold_pages(t);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) at[i] = o[min(row + i * per, KT - 1)];  // (no branch: all at once)
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            if (row + i * per < KT)
-                                cp_async_16_zfill(dst + swz(row + i * per, c & 7), src + (at[i] < 0 ? 0 : at[i]) + c * 16,
-                                                  at[i] < 0 ? 0 : 16);
-                    }
-                arrive_after_copies(&full[st]);
-            }
-        } else {
-            // 16 codes at a time; a thread widens the pieces that it has copied
-            // itself, and piece i of all threads lies together
-            constexpr int PER = KT * DB * 4 / PX_BRING, RS = px_code_stages(DB, E4);
-            uint8_t* const codes = sm + L.codes + (is_v ? RS * (HALF / 2) : 0) + pt * 16;
-            const int CH = D / 16;
-            const int row0 = pt / CH, c0 = pt - row0 * CH, dr = PX_BRING / CH, dc = PX_BRING - dr * CH;
-            auto step = [&](int& row, int& c) {  // to the thread's next piece
-                row += dr;
-                c += dc;
-                if (c >= CH) c -= CH, ++row;
-            };
-            auto copy = [&](int t) {
-                if (t < tiles) {
-                    publish(t);
-                    const int64_t* const o = offs + (t & 1) * 128;
-                    uint8_t* const to = codes + (t % RS) * (HALF / 2);
-                    int row = row0, c = c0;
-                    // (the offsets are read before the copies, which order the
-                    // accesses around them, and without branches: all at once)
-                    int64_t at[PER];
-#pragma unroll
-                    for (int i = 0; i < PER; ++i) {
-                        at[i] = o[min(row, KT - 1)] + (row < KT ? c * 16 : 0);  // (negative stays so)
-                        at[i] = row < KT ? at[i] : -1;
-                        step(row, c);
-                    }
-#pragma unroll
-                    for (int i = 0; i < PER; ++i)
-                        cp_async_16_zfill(to + i * (PX_BRING * 16), src + max(at[i], (int64_t)0), at[i] < 0 ? 0 : 16);
+            for (int i = 0; i < KT / PX_BRING; ++i) {
+                const int key = i * PX_BRING + pt;
+                const int64_t at = place_of(key0 + t * KT + key);
+                rows_of[(t & 1) * 128 + key] = at;
+                if (!is_v) {
+                    const uint32_t word = __ballot_sync(FULL_MASK, at != NONE);
+                    if (lane == 0) live[(t % MASKS) * 4 + (key >> 5)] = word;
                 }
-                cp_async_commit();
-            };
+            }
+            together();
+        };
+        // `whole`: the head fills its blocks of 64 dims (D = 64 DB), so that the
+        // steps from a thread's piece to its next are constants.
+        auto bring = [&](auto whole) {
+            constexpr bool W = decltype(whole)::value;
+            bool ok = true;
+            if constexpr (!E4) {
+                const int CH = W ? DB * 8 : D / 8, per = PX_BRING / CH;  // rows that the two warps copy at once
+                const int c = pt % CH, r0 = pt / CH;
+                const uint32_t col = (c >> 3) * (KT * 128);
+                const uint8_t* const from = src + c * 16;
+                for (int t = 0; t < tiles; ++t) {
+                    const int st = t % ST;
+                    find_rows(t);
+                    if (t >= ST && ok) ok = __all_sync(FULL_MASK, mbar_wait_abort(&empty[st], ((t / ST) - 1) & 1, abort));
+                    if (!ok) continue;  // (the two warps stay together in find_rows)
+                    uint8_t* const dst = ring + st * HALF + col;
+                    const int64_t* const o = rows_of + (t & 1) * 128 + r0;
+                    // (eight rows' places are read before their copies, which
+                    // order the accesses to shared memory around them)
+                    if (W || r0 < per)
 #pragma unroll 1
-            for (int t = 0; t < RS - 1; ++t) copy(t);
-            for (int t = 0; t < tiles; ++t) {
-                const int st = t % ST;
-                copy(t + RS - 1);
-                cp_async_wait<RS - 1>();
-                if (t >= ST && ok) ok = __all_sync(FULL_MASK, mbar_wait_abort(&empty[st], ((t / ST) - 1) & 1, abort));
-                if (!ok) continue;  // (the two warps stay together at publish)
-                const uint8_t* const from = codes + (t % RS) * (HALF / 2);
-                uint8_t* const dst = ring + st * HALF;
-                int row = row0, c = c0;
-                constexpr int BATCH = PER < 8 ? PER : 8;  // pieces that are read before any of them is written
+                        for (int row = 0; row < KT; row += 8 * per) {
+                            int64_t at[8];
 #pragma unroll
-                for (int i0 = 0; i0 < PER; i0 += BATCH) {
-                    uint4 x[BATCH];
+                            for (int i = 0; i < 8; ++i) at[i] = o[W ? row + i * per : min(row + i * per, KT - 1 - r0)];
 #pragma unroll
-                    for (int i = 0; i < BATCH; ++i) x[i] = *reinterpret_cast<const uint4*>(from + (i0 + i) * (PX_BRING * 16));
-#pragma unroll
-                    for (int i = 0; i < BATCH; ++i) {
-                        uint32_t w[8];
-                        e4m3x4_to_f16(x[i].x, w[0], w[1]);
-                        e4m3x4_to_f16(x[i].y, w[2], w[3]);
-                        e4m3x4_to_f16(x[i].z, w[4], w[5]);
-                        e4m3x4_to_f16(x[i].w, w[6], w[7]);
-                        if (row < KT) {
-                            uint8_t* const d = dst + (c >> 2) * (KT * 128);
-                            *reinterpret_cast<uint4*>(d + swz(row, (2 * c) & 7)) = make_uint4(w[0], w[1], w[2], w[3]);
-                            *reinterpret_cast<uint4*>(d + swz(row, (2 * c + 1) & 7)) = make_uint4(w[4], w[5], w[6], w[7]);
+                            for (int i = 0; i < 8; ++i)
+                                if (W || r0 + row + i * per < KT)
+                                    cp_async_16_zfill(dst + swz(r0 + row + i * per, c & 7), at[i] == NONE ? from : from + at[i],
+                                                      at[i] == NONE ? 0 : 16);
                         }
-                        step(row, c);
-                    }
+                    arrive_after_copies(&full[st]);
+                    if (!is_v && lane == 0) mbar_arrive(&full[st]);  // (carries the masks)
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&full[st]);
+            } else {
+                // 16 codes at a time; a thread widens the pieces that it has
+                // copied itself, and piece i of all threads lies together.  Of a
+                // whole head eight lanes take 4 pieces of each of two rows, so
+                // that they write the 8 different 16-byte columns of the swizzle;
+                // else they go row by row.
+                constexpr int PER = KT * DB * 4 / PX_BRING, RS = px_code_stages(DB, E4);  // pieces of a thread at most
+                constexpr int BATCH = PER < 8 ? PER : 8;  // pieces that are read before any of them is written
+                uint8_t* const codes = sm + L.codes + (is_v ? RS * (HALF / 2) : 0) + pt * 16;
+                const int CH = W ? DB * 4 : D / 16, unit = pt >> 3;
+                const int row0 = W ? 2 * (unit / DB) + (pt >> 2 & 1) : pt / CH, c0 = W ? 4 * (unit % DB) + (pt & 3) : pt % CH;
+                const int dr = W ? 16 / DB : PX_BRING / CH, dc = W ? 0 : PX_BRING % CH;
+                auto step = [&](int& row, int& c) {  // to the thread's next piece
+                    row += dr;
+                    if (!W) {
+                        c += dc;
+                        if (c >= CH) c -= CH, ++row;
+                    }
+                };
+                auto copy = [&](int t) {
+                    if (t < tiles) {
+                        find_rows(t);
+                        const int64_t* const o = rows_of + (t & 1) * 128;
+                        uint8_t* const to = codes + (t % RS) * (HALF / 2);
+                        int row = row0, c = c0;
+                        if (!W) asm volatile("" : "+r"(row), "+r"(c));  // (16 pieces' steps are not worth registers)
+#pragma unroll
+                        for (int i0 = 0; i0 < PER; i0 += BATCH) {
+                            int64_t at[BATCH];  // (as above)
+#pragma unroll
+                            for (int i = 0; i < BATCH; ++i) {
+                                at[i] = o[W ? row : min(row, KT - 1)];
+                                if (!W) at[i] = row < KT && at[i] != NONE ? at[i] + c * 16 : NONE;
+                                step(row, c);
+                            }
+#pragma unroll
+                            for (int i = 0; i < BATCH; ++i)
+                                cp_async_16_zfill(to + (i0 + i) * (PX_BRING * 16),
+                                                  (at[i] == NONE ? src : src + at[i]) + (W ? c0 * 16 : 0), at[i] == NONE ? 0 : 16);
+                        }
+                    }
+                    cp_async_commit();
+                };
+#pragma unroll 1
+                for (int t = 0; t < RS - 1; ++t) copy(t);
+                for (int t = 0; t < tiles; ++t) {
+                    const int st = t % ST;
+                    copy(t + RS - 1);
+                    cp_async_wait<RS - 1>();
+                    if (t >= ST && ok) ok = __all_sync(FULL_MASK, mbar_wait_abort(&empty[st], ((t / ST) - 1) & 1, abort));
+                    if (!ok) continue;
+                    const uint8_t* const from = codes + (t % RS) * (HALF / 2);
+                    uint8_t* const dst = ring + st * HALF;
+                    int row = row0, c = c0;
+                    if (!W) asm volatile("" : "+r"(row), "+r"(c));
+#pragma unroll
+                    for (int i0 = 0; i0 < PER; i0 += BATCH) {
+                        uint4 x[BATCH];
+#pragma unroll
+                        for (int i = 0; i < BATCH; ++i) x[i] = *reinterpret_cast<const uint4*>(from + (i0 + i) * (PX_BRING * 16));
+#pragma unroll
+                        for (int i = 0; i < BATCH; ++i) {
+                            uint32_t w[8];
+                            e4m3x4_to_f16(x[i].x, w[0], w[1]);
+                            e4m3x4_to_f16(x[i].y, w[2], w[3]);
+                            e4m3x4_to_f16(x[i].z, w[4], w[5]);
+                            e4m3x4_to_f16(x[i].w, w[6], w[7]);
+                            if (W || row < KT) {
+                                uint8_t* const d = dst + (c >> 2) * (KT * 128);
+                                *reinterpret_cast<uint4*>(d + swz(row, (2 * c) & 7)) = make_uint4(w[0], w[1], w[2], w[3]);
+                                *reinterpret_cast<uint4*>(d + swz(row, (2 * c + 1) & 7)) = make_uint4(w[4], w[5], w[6], w[7]);
+                            }
+                            step(row, c);
+                        }
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&full[st]);
+                }
             }
-        }
+        };
+        if (D == DB * 64)
+            bring(std::true_type{});
+        else
+            bring(std::false_type{});
     }
     cp_async_commit();
     cp_async_wait<0>();  // no copy still in flight on any exit
