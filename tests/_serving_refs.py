@@ -20,29 +20,31 @@ def router(logits, k, bias, score, groups, top_groups, group_score, renorm, scal
         flat = bool((b == b[0]).all()) and np.isfinite(b[0])
         key = x.copy() if flat else p + b  # (one bias for all: the logits' own order)
         key[(x == -np.inf) | np.isnan(key)] = -np.inf
-    ids, w = np.full((T, k), -1, dtype=np.int64), np.zeros((T, k))
     size = E // groups
-    for t in range(T):
-        live = np.ones(E, dtype=bool)
-        if top_groups < groups:
-            by = (p[t] + b if flat and group_score == "top2" else key[t]).copy()
-            by[key[t] == -np.inf] = -np.inf
-            by = np.sort(by.reshape(groups, size), -1)
-            worth = by[:, -1] + by[:, -2] if group_score == "top2" else by[:, -1]
-            worth = np.where(np.isnan(worth), -np.inf, worth)
-            best = np.argsort(-worth, kind="stable")[:top_groups]
-            live = np.isin(np.arange(E) // size, best)
-        row = np.where(live, key[t], -np.inf)
-        order = np.argsort(-row, kind="stable")[:k]
-        order = order[row[order] > -np.inf]
-        ids[t, :len(order)] = order
-        v = p[t, order]
-        if renorm and len(order):
-            if score == "sigmoid" and v.sum() < 1e-200:   # only the ratios of tiny scores are left
-                v = np.exp(x[t, order] - x[t, order].max())
-            v = v / v.sum()
-        w[t, :len(order)] = v * scale
-    return ids, w
+    live = np.ones((T, E), dtype=bool)
+    if top_groups < groups:
+        by = (p + b if flat and group_score == "top2" else key).copy()
+        by[key == -np.inf] = -np.inf
+        by = np.sort(by.reshape(T, groups, size), -1)
+        with np.errstate(all="ignore"):
+            worth = by[..., -1] + by[..., -2] if group_score == "top2" else by[..., -1]
+        worth = np.where(np.isnan(worth), -np.inf, worth)
+        chosen = np.zeros((T, groups), dtype=bool)
+        np.put_along_axis(chosen, np.argsort(-worth, axis=-1, kind="stable")[:, :top_groups], True, -1)
+        live = np.repeat(chosen, size, axis=1)
+    row = np.where(live, key, -np.inf)
+    ids = np.argsort(-row, axis=-1, kind="stable")[:, :k]
+    there = np.take_along_axis(row, ids, -1) > -np.inf
+    v, xs = np.take_along_axis(p, ids, -1), np.take_along_axis(x, ids, -1)
+    if renorm:
+        if score == "sigmoid":   # the ratios of scores that are all tiny are those of their exponentials
+            tiny = np.where(there, v, 0).sum(-1) < 1e-200
+            top = np.max(np.where(there, xs, -np.inf), -1, keepdims=True, initial=-1e300)
+            with np.errstate(all="ignore"):
+                v = np.where(tiny[:, None], np.exp(xs - top), v)
+        with np.errstate(all="ignore"):
+            v = v / np.where(there, v, 0).sum(-1, keepdims=True)
+    return np.where(there, ids, -1), np.where(there, v * scale, 0.0)
 
 
 def plan(past, new, table, free, n_free, page, T, shared=(), shares=None):

@@ -176,3 +176,52 @@ def test_captured_and_on_another_stream(cuda_device):
     torch.cuda.synchronize()
     for o in (other, got):
         assert torch.equal(o[0], want[0]) and torch.equal(o[1], want[1])
+
+
+MANY = 5003   # rows for all SMs' warps: eight lanes a row where the shape allows
+
+
+@pytest.mark.parametrize("E,k,groups,top", [(32, 8, 1, 1), (32, 2, 8, 3), (64, 6, 4, 2), (96, 5, 1, 1), (128, 8, 8, 4), (160, 7, 4, 1),
+                                            (224, 1, 2, 1), (256, 8, 8, 4), (256, 8, 1, 1), (256, 3, 16, 3)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+def test_many_rows(cuda_device, E, k, groups, top, dtype):
+    x = randn(MANY, E, seed=E + k, dtype=dtype)
+    for score, gs, bias, renorm in (("sigmoid", "top2", True, True), ("softmax", "max", True, False), ("sigmoid", "top2", False, False),
+                                    ("softmax", "top2", False, True), ("sigmoid", "max", False, True)):
+        b = randn(E, seed=E, std=0.1 if score == "sigmoid" else 0.3 / E) if bias else None
+        check(cuda_device, x, k, b, score, groups, top, gs, renorm, 2.5, f"{score} {gs} bias={bias}")
+
+
+def test_many_rows_with_ties_absences_and_near_keys(cuda_device):
+    g = torch.Generator().manual_seed(11)
+    E = 256
+    steps = (torch.randint(-3, 4, (E,), generator=g) * 0.001).float()
+    ties = torch.randint(0, 5, (MANY, E), generator=g).float()
+    few = randn(MANY, E, seed=12)
+    few[::7, 3:] = float("-inf")
+    few[1::7, ::2] = float("nan")
+    hole = randn(E, seed=13, std=0.1)
+    hole[64:200] = float("-inf")
+    p = torch.sigmoid(few[0:1].nan_to_num(0, neginf=0)).double()
+    near = few[0:1].nan_to_num(0, neginf=0) + 1e-6 * randn(MANY, E, seed=14)
+    nb = (0.75 - p[0]).float()
+    for groups, top in ((1, 1), (8, 4)):
+        check(cuda_device, ties, 8, None, "sigmoid", groups, top, what="ties")
+        check(cuda_device, ties, 8, steps, "softmax", groups, top, "max", what="ties and steps")
+        check(cuda_device, ties.bfloat16(), 4, torch.zeros(E), "sigmoid", groups, top, what="ties, zeros")
+        check(cuda_device, near, 8, nb, "sigmoid", groups, top, what="near")
+        check(cuda_device, randn(MANY, E, seed=15), 8, hole, "sigmoid", groups, top, "max", what="hole")
+        assert moe.device_error(cuda_device) == 0
+        check(cuda_device, few, 8, None, "softmax", groups, top, "max", what="few")
+        assert moe.device_error(cuda_device) == 0x4
+
+
+def test_many_rows_with_a_row_stride(cuda_device):
+    base = randn(MANY, 300, seed=16)
+    for at, E in ((0, 256), (4, 128), (1, 64)):
+        x = base[:, at:at + E]
+        b = randn(E, seed=E, std=0.1)
+        ids, w = moe.router_grouped_topk(base.to(cuda_device)[:, at:at + E], 6, b.to(cuda_device), "sigmoid", 4, 2)
+        rid, rw = refs.router(x, 6, b, "sigmoid", 4, 2, "top2", True, 1.0)
+        assert np.array_equal(ids.cpu().numpy(), rid)
+        np.testing.assert_allclose(w.cpu().numpy(), rw, rtol=2.0 ** -20)
