@@ -68,8 +68,12 @@ __device__ __forceinline__ float rcp_fast(float x) {
 }
 
 // Descending order by odd-even merges.
-template <int N>
-__device__ __forceinline__ void sort_down(uint32_t (&v)[N]) {
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return max(a, b); }
+__device__ __forceinline__ uint32_t smaller(uint32_t a, uint32_t b) { return min(a, b); }
+__device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ float smaller(float a, float b) { return fminf(a, b); }
+template <int N, class T>
+__device__ __forceinline__ void sort_down(T (&v)[N]) {
 #pragma unroll
     for (int p = 1; p < N; p *= 2)
 #pragma unroll
@@ -79,9 +83,9 @@ __device__ __forceinline__ void sort_down(uint32_t (&v)[N]) {
 #pragma unroll
                 for (int i = 0; i < k; ++i)
                     if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
-                        const uint32_t a = v[i + j], b = v[i + j + k];
-                        v[i + j] = max(a, b);
-                        v[i + j + k] = min(a, b);
+                        const T a = v[i + j], b = v[i + j + k];
+                        v[i + j] = larger(a, b);
+                        v[i + j + k] = smaller(a, b);
                     }
 }
 
@@ -115,6 +119,14 @@ __device__ __forceinline__ void load_logits(const void* row, int e0, int E, bool
 #pragma unroll
     for (int i = 0; i < NV; ++i) x[i] = fmaxf(x[i], -INFINITY);  // (of NaN: -inf)
 }
+
+// What FP32 scores are off by at most, in units of 2^-24.  Sigmoid, of a value
+// s <= 1: 2 for the quotient, 1 for the sum 1 + e, and s (1 - s) times the
+// relative error of e, 4 of exp2 and 1.5 |x| of its argument: 1 + 0.4; under
+// 5.5.  Softmax, relative to a score of at most 1 / total: 4 of exp2, as much of
+// the sum's terms, 37 of its additions, 2 of the quotient, and 0.37 * 1.5 of
+// the exponent (s |x - m| is at most 0.37 / total); under 48.
+__device__ __forceinline__ float score_error(bool softmax, float total) { return softmax ? 0x30p-24f / total : 0x5.8p-24f; }
 
 // A score in 64 bits; `m` and `total` are the row's (softmax).
 __device__ __forceinline__ double score64(const RouterGroupedArgs& a, float x, double m, double total) {
@@ -184,11 +196,7 @@ __device__ __forceinline__ void route_row(const RouterGroupedArgs& a, int64_t t,
 #pragma unroll
         for (int i = 0; i < NV; ++i) s[i] = rcp_fast(1.f + exp2_fast(x[i] * -1.44269504f));
     }
-    // FP32 scores are off by less than this (the sigmoid: exp2, sum and
-    // quotient of a value of at most 1; the softmax: 2^-22 each of exp2 and
-    // quotient, NV + 6 half steps of the sum, 2 |x - m| half steps of the
-    // exponent, relative to a score of at most 1 / total)
-    const float tau_s = softmax ? 0x1p-17f / total : 0x1p-20f;
+    const float tau_s = score_error(softmax, total);
     uint32_t key[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -248,33 +256,42 @@ __device__ __forceinline__ void route_row(const RouterGroupedArgs& a, int64_t t,
         float worth = top2 ? best + second : best;
         if (!(worth >= -INFINITY)) worth = -INFINITY;
         int rank = 0;
-        bool close = false;
         for (int g = 0; g < a.groups; ++g) {
             const float o = __shfl_sync(FULL_MASK, worth, g);
             rank += o > worth || (o == worth && g < lane);
-            close |= g != lane && fabsf(o - worth) <= 2.f * tau_s + 0x1p-20f * fabsf(worth);
         }
         bool in = lane < a.groups && rank < a.top_groups;
-        if (!by_logit && __any_sync(FULL_MASK, close && lane < a.groups)) {
+        if (!by_logit) {
             // the border between the last group in and the first one out
             const float last = unordered(~warp_max(in ? ~ordered(worth) : 0u));
             const float next = unordered(warp_max(lane < a.groups && !in ? ordered(worth) : 0u));
-            if (last - next <= 2.f * tau_s + 0x1p-20f * fmaxf(fabsf(last), fabsf(next))) {
+            const float tol = 4.f * tau_s + 0x1p-21f * fmaxf(fabsf(last), fabsf(next));
+            if (last - next <= tol) {
+                // the groups about it in 64 bits, the others are clearly in or out
                 row64();
-                double b64 = -INFINITY, s64 = -INFINITY;
                 __syncwarp();
 #pragma unroll
                 for (int i = 0; i < NV; ++i) sk[e0 + i] = key[i];
                 __syncwarp();
-                if (lane < a.groups)
-                    for (int i = 0; i < gsize; ++i) {
-                        const int e = lane * gsize + i;
-                        if (sk[e] == 0u) continue;
-                        const double v = score64(a, logit_at<DT>(row, e), m64, total64) + (same_bias ? 0. : (double)a.bias[e]);
-                        s64 = fmax(s64, fmin(b64, v));
-                        b64 = fmax(b64, v);
+                double w64 = worth > last + tol ? INFINITY : -INFINITY;
+                const bool near = lane < a.groups && worth >= next - tol && worth <= last + tol;
+                for (uint32_t todo = __ballot_sync(FULL_MASK, near); todo; todo &= todo - 1u) {
+                    const int g = __ffs(todo) - 1;
+                    double b64 = -INFINITY, s64 = -INFINITY;
+                    for (int e = g * gsize + lane; e < (g + 1) * gsize; e += 32)
+                        if (sk[e] != 0u) {
+                            const double v = score64(a, logit_at<DT>(row, e), m64, total64) + (same_bias ? 0. : (double)a.bias[e]);
+                            s64 = fmax(s64, fmin(b64, v));
+                            b64 = fmax(b64, v);
+                        }
+#pragma unroll
+                    for (int o = 16; o; o >>= 1) {
+                        const double b2 = __shfl_xor_sync(FULL_MASK, b64, o), s2 = __shfl_xor_sync(FULL_MASK, s64, o);
+                        s64 = fmax(fmax(s64, s2), fmin(b64, b2));
+                        b64 = fmax(b64, b2);
                     }
-                const double w64 = top2 ? b64 + s64 : b64;
+                    if (lane == g) w64 = top2 ? b64 + s64 : b64;
+                }
                 rank = 0;
                 for (int g = 0; g < a.groups; ++g) {
                     const double o = __shfl_sync(FULL_MASK, w64, g);
@@ -488,7 +505,6 @@ template <int NE, int DT>
 __global__ void __launch_bounds__(RO_WARPS * 32, NE == 32 ? 4 : 6) router_octets_kernel(const __grid_constant__ RouterGroupedArgs a) {
     using Buffers = OctetBuffers<NE, DT>;
     constexpr int ES = Buffers::ES, NS = NE / 8, LP = RO_LIST(NE);
-    constexpr uint32_t ABSENT = 0x007fffffu;  // the key of -inf
     extern __shared__ __align__(16) uint8_t ro_smem[];
     const int lane = threadIdx.x & 31, warp = warp_index();
     Buffers& buf = reinterpret_cast<Buffers*>(ro_smem)[warp];
@@ -557,9 +573,9 @@ __global__ void __launch_bounds__(RO_WARPS * 32, NE == 32 ? 4 : 6) router_octets
         __syncwarp();
         fetch(t0 + step);
 
-        // scores and keys, as in route_row
-        float m = 0.f, total = 1.f, inv = 1.f;
-        if (softmax) {
+        // scores and keys, as in route_row; keys stay floats, -inf for absent
+        float m = 0.f, total = 1.f;
+        if (softmax && (!same_bias || (narrow && top2) || !a.renorm)) {
             m = x[0];
 #pragma unroll
             for (int i = 1; i < NE; ++i) m = fmaxf(m, x[i]);
@@ -570,23 +586,32 @@ __global__ void __launch_bounds__(RO_WARPS * 32, NE == 32 ? 4 : 6) router_octets
             for (int i = 0; i < NE; ++i) total += exp2_fast((x[i] - m) * 1.44269504f);
 #pragma unroll
             for (int o = 1; o < 8; o *= 2) total += __shfl_xor_sync(FULL_MASK, total, o);
-            inv = 1.f / total;
         }
-        const float tau_s = softmax ? 0x1p-17f / total : 0x1p-20f;
-        uint32_t key[NE];
+        const float inv = 1.f / total, tau_s = score_error(softmax, total);
         float best = -INFINITY, second = -INFINITY;
+        auto see = [&](float v) {
+            second = fmaxf(second, fminf(best, v));
+            best = fmaxf(best, v);
+        };
+        if (!same_bias) {
+            if (softmax)
 #pragma unroll
-        for (int i = 0; i < NE; ++i) {
-            const float s = softmax ? exp2_fast((x[i] - m) * 1.44269504f) * inv : rcp_fast(1.f + exp2_fast(x[i] * -1.44269504f));
-            const bool there = x[i] > -INFINITY;
-            const float f = !there ? -INFINITY : same_bias ? x[i] : s + bias[i];
-            key[i] = ordered(f);
-            if (narrow) {
-                const float v = by_logit || !there ? f : same_bias ? s : f;
-                second = fmaxf(second, fminf(best, v));
-                best = fmaxf(best, v);
-            }
+                for (int i = 0; i < NE; ++i)
+                    x[i] = x[i] > -INFINITY ? fmaf(exp2_fast((x[i] - m) * 1.44269504f), inv, bias[i]) : -INFINITY;
+            else
+#pragma unroll
+                for (int i = 0; i < NE; ++i)
+                    x[i] = x[i] > -INFINITY ? rcp_fast(1.f + exp2_fast(x[i] * -1.44269504f)) + bias[i] : -INFINITY;
+        } else if (narrow && top2) {  // (the order is the logits', a group's worth is of scores)
+#pragma unroll
+            for (int i = 0; i < NE; ++i)
+                see(x[i] == -INFINITY ? -INFINITY
+                    : softmax         ? exp2_fast((x[i] - m) * 1.44269504f) * inv
+                                      : rcp_fast(1.f + exp2_fast(x[i] * -1.44269504f)));
         }
+        if (narrow && (!same_bias || !top2))
+#pragma unroll
+            for (int i = 0; i < NE; ++i) see(x[i]);
         bool again = false;  // this row is left to route_row
         if (narrow) {
             for (int o = 1; o < q; o *= 2) {
@@ -601,43 +626,50 @@ __global__ void __launch_bounds__(RO_WARPS * 32, NE == 32 ? 4 : 6) router_octets
                 const float o = __shfl_sync(FULL_MASK, worth, lane0 + g);
                 const bool other = g != (sub & -q);
                 rank += other && (o > worth || (o == worth && g < sub));
-                again |= !by_logit && other && fabsf(o - worth) <= 2.f * tau_s + 0x1p-20f * fabsf(worth);
+            }
+            if (!by_logit) {  // the border between the last group in and the first one out
+                float last = rank < a.top_groups ? worth : INFINITY, next = rank < a.top_groups ? -INFINITY : worth;
+#pragma unroll
+                for (int o = 1; o < 8; o *= 2) {
+                    last = fminf(last, __shfl_xor_sync(FULL_MASK, last, o));
+                    next = fmaxf(next, __shfl_xor_sync(FULL_MASK, next, o));
+                }
+                again = last - next <= 4.f * tau_s + 0x1p-21f * fmaxf(fabsf(last), fabsf(next));
             }
             if (rank >= a.top_groups)
 #pragma unroll
-                for (int i = 0; i < NE; ++i) key[i] = 0u;
+                for (int i = 0; i < NE; ++i) x[i] = -INFINITY;
         }
 
         // lists of eight
-        uint32_t head[NS];
-        {
-            uint32_t* const list = buf.lists + lane * LP;
-            uint32_t* const orig = buf.keys + lane * LP;
+        float* const lists = reinterpret_cast<float*>(buf.lists);
+        float* const keys = reinterpret_cast<float*>(buf.keys);
+        float head[NS];
 #pragma unroll
-            for (int l = 0; l < NS; ++l) {
-                uint32_t v[8];
+        for (int l = 0; l < NS; ++l) {
+            float v[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = key[l * 8 + i];
-                *reinterpret_cast<uint4*>(orig + l * 8) = make_uint4(v[0], v[1], v[2], v[3]);
-                *reinterpret_cast<uint4*>(orig + l * 8 + 4) = make_uint4(v[4], v[5], v[6], v[7]);
-                sort_down(v);
-                head[l] = v[0];
-                *reinterpret_cast<uint4*>(list + l * 8) = make_uint4(v[0], v[1], v[2], v[3]);
-                *reinterpret_cast<uint4*>(list + l * 8 + 4) = make_uint4(v[4], v[5], v[6], v[7]);
-            }
+            for (int i = 0; i < 8; ++i) v[i] = x[l * 8 + i];
+            *reinterpret_cast<float4*>(keys + lane * LP + l * 8) = make_float4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<float4*>(keys + lane * LP + l * 8 + 4) = make_float4(v[4], v[5], v[6], v[7]);
+            sort_down(v);
+            head[l] = v[0];
+            *reinterpret_cast<float4*>(lists + lane * LP + l * 8) = make_float4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<float4*>(lists + lane * LP + l * 8 + 4) = make_float4(v[4], v[5], v[6], v[7]);
         }
         __syncwarp();
-        uint32_t pick_key = 0u, beyond = 0u, taken = 0u;  // taken: a byte for each list
+        float pick_key = -INFINITY, beyond = -INFINITY;
+        uint32_t taken = 0u;  // a byte for each list
         int from = 0, which = 0;
         const int want = same_bias ? k : k + 1;
 #pragma unroll 1
         for (int j = 0; j < want; ++j) {
-            uint32_t mine = head[0];
+            float mine = head[0];
 #pragma unroll
-            for (int l = 1; l < NS; ++l) mine = max(mine, head[l]);
-            uint32_t top = mine;
+            for (int l = 1; l < NS; ++l) mine = fmaxf(mine, head[l]);
+            float top = mine;
 #pragma unroll
-            for (int o = 1; o < 8; o *= 2) top = max(top, __shfl_xor_sync(FULL_MASK, top, o));
+            for (int o = 1; o < 8; o *= 2) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, o));
             const uint32_t has = __ballot_sync(FULL_MASK, mine == top) >> lane0 & 0xffu;
             const int owner = __ffs(has) - 1;
             int l = NS - 1;
@@ -648,7 +680,7 @@ __global__ void __launch_bounds__(RO_WARPS * 32, NE == 32 ? 4 : 6) router_octets
             if (sub == owner) {
                 const uint32_t at = (taken >> 8 * l & 0xffu) + 1u;
                 taken += 1u << 8 * l;
-                const uint32_t next = at < 8u ? buf.lists[lane * LP + l * 8 + at] : 0u;
+                const float next = at < 8u ? lists[lane * LP + l * 8 + at] : -INFINITY;
 #pragma unroll
                 for (int i = 0; i < NS; ++i)
                     if (i == l) head[i] = next;
@@ -657,11 +689,11 @@ __global__ void __launch_bounds__(RO_WARPS * 32, NE == 32 ? 4 : 6) router_octets
             if (j == k) beyond = top;
         }
         const bool mine = sub < k;
-        again |= mine && pick_key <= ABSENT;  // fewer than k experts
+        again |= mine && pick_key == -INFINITY;  // fewer than k experts
         // which of the list's eight experts: equal keys come in their order
         int skip = 0;
         {
-            const uint32_t key_before = __shfl_up_sync(FULL_MASK, pick_key, 1, 8);
+            const float key_before = __shfl_up_sync(FULL_MASK, pick_key, 1, 8);
             const int list_before = __shfl_up_sync(FULL_MASK, from * 8 + which, 1, 8);
             const bool twin = sub > 0 && mine && key_before == pick_key && list_before == from * 8 + which;
             if (__any_sync(FULL_MASK, twin))
@@ -672,9 +704,9 @@ __global__ void __launch_bounds__(RO_WARPS * 32, NE == 32 ? 4 : 6) router_octets
         }
         int pick = 0;
         {
-            const uint4 lo = *reinterpret_cast<const uint4*>(buf.keys + from * LP + which * 8);
-            const uint4 hi = *reinterpret_cast<const uint4*>(buf.keys + from * LP + which * 8 + 4);
-            const uint32_t v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+            const float4 lo = *reinterpret_cast<const float4*>(keys + from * LP + which * 8);
+            const float4 hi = *reinterpret_cast<const float4*>(keys + from * LP + which * 8 + 4);
+            const float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
             int at = 0;
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -682,14 +714,13 @@ __global__ void __launch_bounds__(RO_WARPS * 32, NE == 32 ? 4 : 6) router_octets
             pick = (from & 7) * per + which * 8 + at;
         }
         if (!same_bias) {
-            const float f = unordered(pick_key);
-            float fn = __shfl_down_sync(FULL_MASK, f, 1, 8);
-            if (sub == k - 1) fn = beyond > ABSENT ? unordered(beyond) : -INFINITY;
-            again |= mine && f - fn <= 2.f * tau_s + 0x1p-22f * fmaxf(fabsf(f), fabsf(fn));
+            float after = __shfl_down_sync(FULL_MASK, pick_key, 1, 8);
+            if (sub == k - 1) after = beyond;
+            again |= mine && pick_key - after <= 2.f * tau_s + 0x1p-22f * fmaxf(fabsf(pick_key), fabsf(after));
         }
         // weights, as in route_row (all lanes take part in the exchanges)
         {
-            const bool there = mine && t < a.T && pick_key > ABSENT;
+            const bool there = mine && t < a.T && pick_key > -INFINITY;
             const void* const row = static_cast<const uint8_t*>(a.logits) + t * a.stride * ES;
             const float px = there ? logit_at<DT>(row, pick) : -INFINITY;
             float ref = m, w = 0.f;
