@@ -31,24 +31,25 @@ __device__ __forceinline__ Pair operator+(Pair x, Pair y) { return {x.a + y.a, x
 
 // Exclusive sums over the block's threads of v, in order; *all gets the total.
 __device__ __forceinline__ Pair block_exclusive(Pair v, Pair* all) {
-    __shared__ Pair part[PG_THREADS / 32 + 1];
+    __shared__ Pair part[PG_THREADS / 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    Pair s = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const Pair u = {__shfl_up_sync(FULL_MASK, s.a, o), __shfl_up_sync(FULL_MASK, s.b, o)};
-        if (lane >= o) s = s + u;
-    }
+    auto scan = [&](Pair s, int width) {  // inclusive, over `width` lanes
+        for (int o = 1; o < width; o <<= 1) {
+            const Pair u = {__shfl_up_sync(FULL_MASK, s.a, o), __shfl_up_sync(FULL_MASK, s.b, o)};
+            if (lane >= o) s = s + u;
+        }
+        return s;
+    };
+    const Pair s = scan(v, 32);
     __syncthreads();  // (the last use of part is over)
     if (lane == 31) part[warp] = s;
     __syncthreads();
-    Pair before = {0, 0}, sum = {0, 0};
-#pragma unroll
-    for (int w = 0; w < PG_THREADS / 32; ++w) {
-        if (w == warp) before = sum;
-        sum = sum + part[w];
-    }
-    *all = sum;
+    // every warp scans the warps' sums for itself
+    constexpr int WARPS = PG_THREADS / 32;
+    const Pair t = scan(part[lane < WARPS ? lane : 0], WARPS);
+    *all = {__shfl_sync(FULL_MASK, t.a, WARPS - 1), __shfl_sync(FULL_MASK, t.b, WARPS - 1)};
+    Pair before = {__shfl_sync(FULL_MASK, t.a, warp > 0 ? warp - 1 : 0), __shfl_sync(FULL_MASK, t.b, warp > 0 ? warp - 1 : 0)};
+    if (warp == 0) before = {0, 0};
     return {before.a + s.a - v.a, before.b + s.b - v.b};
 }
 
