@@ -7,7 +7,11 @@ page slots and lengths live on the device and move on inside it.  Three things
 are torch calls: the router's small projection, the slots and lengths of the new
 tokens, and the conversion of the 32-bit stream for the first norm.
 
-    python examples/decode_block.py [--batch 8] [--context 4096] [--steps 64]
+With --shared N the sequences begin with the same N tokens and live in a pool of
+pages: SharedBlock plans pages, slots and lengths on the device, reads the shared
+prefix once for all sequences, and routes with a balancing bias within groups.
+
+    python examples/decode_block.py [--batch 8] [--context 4096] [--steps 64] [--shared 0]
 
 Random weights of a Qwen3-style block (E=128, top-8, d=2048, I=768; 32 query
 and 4 key-value heads of 128).
@@ -78,12 +82,23 @@ class DecodeBlock:
         self.lens = torch.zeros(batch, dtype=torch.int32, device=device)
         self.workspace = moe.attention_workspace(Hq, Hkv, D, device)
 
-    def step(self, resid: torch.Tensor) -> torch.Tensor:
-        """One new token for every sequence: resid float32 [B, d] in and out (in place)."""
-        B = resid.shape[0]
+    def place(self, B: int):
+        """Positions and slots of the new tokens; the lengths move on."""
         positions = self.lens.clone()
         slots = cache_slots(self.first, positions, self.page)
         self.lens += 1
+        return positions, slots
+
+    def attend(self, q: torch.Tensor) -> torch.Tensor:
+        return moe.paged_attention(q, self.k_cache, self.v_cache, self.table, self.lens, workspace=self.workspace)
+
+    def route(self, logits: torch.Tensor):
+        return moe.router_topk(logits, self.cfg.k)
+
+    def step(self, resid: torch.Tensor) -> torch.Tensor:
+        """One new token for every sequence: resid float32 [B, d] in and out (in place)."""
+        B = resid.shape[0]
+        positions, slots = self.place(B)
 
         # (the first norm has nothing to add: the residual stream is its input)
         x = moe.norm_residual(resid.to(BF), pre=self.attn_norm)
@@ -93,13 +108,63 @@ class DecodeBlock:
         q = moe.norm_residual(q, pre=self.q_norm).view(B, self.Hq, self.D)
         k = moe.norm_residual(k, pre=self.k_norm).view(B, self.Hkv, self.D)
         q = moe.rope_append(q, k, v, positions, slots, self.freqs, self.k_cache, self.v_cache, q_out=q)
-        a = moe.paged_attention(q, self.k_cache, self.v_cache, self.table, self.lens, workspace=self.workspace)
+        a = self.attend(q)
         o = moe.matvec4(a.view(B, -1), self.wo)
         _, x = moe.norm_residual(o, resid, pre=self.moe_norm, resid_out=resid)
-        ids, w = moe.router_topk(x.float() @ self.router.T, self.cfg.k)
+        ids, w = self.route(x.float() @ self.router.T)
         y = moe.layer(x, ids, w, *self.experts)
         moe.norm_residual(y, resid, resid_out=resid)
         return resid
+
+
+class SharedBlock(DecodeBlock):
+    """The block for sequences that begin with the same `shared` tokens (whole pages), over a pool of pages.
+
+    begin() starts a sequence behind the prefix, or without it; end() marks those whose pages go back to the pool at
+    the next step.  The prefix's keys and values are the pages self.shared of the caches."""
+
+    def __init__(self, cfg: inputs.LayerConfig, Hq: int, Hkv: int, D: int, batch: int, capacity: int, shared: int,
+                 page: int = 64, device="cuda", seed: int = 0, group: int = 128, groups: int = 1, top_groups: int = 1):
+        super().__init__(cfg, Hq, Hkv, D, batch, capacity, page, device, seed, group)
+        assert shared % page == 0 and shared <= capacity
+        i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=device)  # noqa: E731
+        n = shared // page
+        order = self.table.flatten()
+        self.shared, self.shared_len, self.batch = order[:n].contiguous(), shared, batch
+        self.free, self.n_free = torch.cat((order[n:], order[:n])), i32([order.numel() - n])
+        self.table = torch.full_like(self.table, -1)
+        self.new = torch.zeros(batch, dtype=torch.int32, device=device)   # a token a step of those that run
+        self.shares = torch.ones(batch, dtype=torch.bool, device=device)
+        self.ended = torch.zeros(batch, dtype=torch.bool, device=device)
+        self.workspace = moe.shared_prefix_workspace(batch, Hq, Hkv, D, device)
+        self.groups, self.top_groups = groups, top_groups
+        self.bias = torch.zeros(cfg.E, device=device)
+
+    def begin(self, b: int, shares: bool = True):
+        self.shares[b], self.new[b] = shares, 1
+        self.lens[b] = self.shared_len if shares else 0
+
+    def end(self, b: int):
+        self.ended[b] = True
+        self.new[b] = 0
+
+    def place(self, B: int):
+        moe.release_pages(self.table, self.lens, self.ended, self.free, self.n_free, self.page, shared=self.shared.numel(),
+                          shares=self.shares, seq_lens_out=self.lens, n_free_out=self.n_free)
+        self.ended.zero_()
+        # one row a sequence: those that do not run bring no token, and their rows behind the last token are padding
+        p = moe.plan_pages(self.lens, self.new, self.table, self.free, self.n_free, self.page, B, shared_pages=self.shared,
+                           shares=self.shares, seq_lens=self.lens, n_free_out=self.n_free)
+        at = p.starts[:-1].long().clamp(max=B - 1)   # (the block's rows are the sequences', not the plan's tokens)
+        runs = p.starts[1:] > p.starts[:-1]
+        return torch.where(runs, p.positions[at], 0), torch.where(runs, p.slots[at], -1)
+
+    def attend(self, q: torch.Tensor) -> torch.Tensor:
+        return moe.shared_prefix_attention(q, self.k_cache, self.v_cache, self.shared, self.shared_len, self.table, self.lens,
+                                           shares=self.shares, workspace=self.workspace)
+
+    def route(self, logits: torch.Tensor):
+        return moe.router_grouped_topk(logits, self.cfg.k, self.bias, "softmax", self.groups, self.top_groups)
 
 
 def main():
@@ -107,18 +172,26 @@ def main():
     ap.add_argument("--batch", type=int, default=8)
     ap.add_argument("--context", type=int, default=4096, help="tokens in the cache before the first step")
     ap.add_argument("--steps", type=int, default=64)
+    ap.add_argument("--shared", type=int, default=0, help="tokens of a shared prefix that the sequences begin with")
     a = ap.parse_args()
-    block = DecodeBlock(inputs.QWEN3, 32, 4, 128, a.batch, a.context + a.steps + 16)
+    if a.shared:
+        block = SharedBlock(inputs.QWEN3, 32, 4, 128, a.batch, a.shared + a.steps + 128, a.shared // 64 * 64)
+        start = lambda: [block.begin(b) for b in range(a.batch)]  # noqa: E731
+        a.context = block.shared_len
+    else:
+        block = DecodeBlock(inputs.QWEN3, 32, 4, 128, a.batch, a.context + a.steps + 16)
+        start = lambda: block.lens.fill_(a.context)  # noqa: E731
     block.k_cache.normal_()
     block.v_cache.normal_()
     resid = torch.randn(a.batch, inputs.QWEN3.d, device="cuda")
-    block.lens.fill_(a.context)
+    start()
     for _ in range(3):
         block.step(resid)
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         block.step(resid)
-    block.lens.fill_(a.context)
+    if not a.shared:
+        start()
     graph.replay()
     begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
     begin.record()
