@@ -562,7 +562,9 @@ int moe_matvec4(const void* x, int64_t x_stride, int T, int K, int dtype, const 
  *   more) and head layout, 256-byte aligned, its first MOE_ATTN_COUNTER_BYTES
  *   zero before the first call and left zero by every call; one that is kept
  *   may serve moe_paged_attention calls too, one after the other.
- * Launches: three (own keys, prefix, join), or one where nothing is shared.
+ * Launches: three (own keys, prefix, join), or one of moe_paged_attention's where
+ * little would be saved (shared_len below 512, or (B - 1) * shared_len * Hkv * D
+ * keys' and values' elements, twice, below 12 million; 32 million of E4M3).
  * Limits as there; shared_len <= n_shared * page_size and <= max_pages *
  * page_size.
  */

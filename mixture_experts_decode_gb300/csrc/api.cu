@@ -567,7 +567,8 @@ int moe_shared_prefix_attention(const void* q, int64_t q_stride, int64_t q_head_
                                    block_table, table_stride, max_pages, seq_lens, scale, 0, 0, workspace, workspace_bytes,
                                    need, out, lse, &a);
     if (bad) return bad;
-    if (shared_len == 0 || num_pages == 0)  // nothing is shared, or no page holds a token
+    // (no page holds a token, or each sequence's own row is the shorter way to the prefix)
+    if (num_pages == 0 || !prefix_pays(B, Hkv, D, shared_len, cache_dtype == MOE_E4M3))
         return cuda_status(launch_paged_attention(a, dtype, cache_dtype, workspace, (cudaStream_t)stream));
     PrefixArgs p{};
     p.q = a.q, p.q_sb = a.q_sb, p.q_sh = a.q_sh;

@@ -179,6 +179,7 @@ struct PrefixArgs {
     int* err;
 };
 size_t prefix_workspace_bytes(int B, int Hq, int Hkv, int D);
+bool prefix_pays(int B, int Hkv, int D, int len, bool e4);
 cudaError_t launch_shared_prefix(PrefixArgs a, const AttnArgs& own, int dtype, int cache_dtype, void* ws, cudaStream_t st);
 
 struct RopeArgs {

@@ -259,17 +259,20 @@ __device__ __forceinline__ uint4 ld_128_l2(const void* p) {
 // A block: one key-value head, one group of row tiles, one run of key tiles.
 // Roles: softmax warps 0 .. 7 (they also bring Q), the MMA warp, two warps that
 // bring K tiles and two that bring V tiles (rows of pages by 16-byte
-// asynchronous copies into the swizzle; E4M3 codes through registers, widened).
+// asynchronous copies into the swizzle; E4M3 codes into a stage of their own,
+// widened from there).
 // Job j: scores and products of one row tile with one key tile, on score
-// buffer j & 1; the MMA warp issues S(0) S(1) PV(0) S(2) PV(1) S(3) ...: the
-// products of one thread run in order, so S(j + 2) may take the buffer that
-// PV(j) reads.  PV comes in two halves of the keys, each as soon as its
-// weights are there.  Barriers: q_full, k_full / v_full (those that bring;
-// their writes are generic, so the MMA warp fences before the tensor cores
-// read), k_empty / v_empty (commits), s_full (commit, and an arrival of the
-// MMA warp that carries what it saw of the tile's live keys), p_full (softmax
-// warps, per half), h_done / o_done (commits of PV's halves).  Every wait is
-// bounded; one that gives up raises `abort`, and every role goes to the end.
+// buffer j & 1.  The MMA warp issues S(0) S(1) PV(0) S(2) PV(1) S(3) ..., PV in
+// two halves of the keys, each as soon as its weights are there, and S(j + 2)
+// when PV(j), which reads its weights from the same buffer, is done (products
+// of different shapes and accumulators are not promised to run in order; the
+// wait costs 162 -> 180 us at 64 x 65536 tokens).
+// Barriers: q_full, k_full / v_full (those that bring; their writes are generic,
+// so the MMA warp fences before the tensor cores read), k_empty / v_empty
+// (commits), s_full (commit, and an arrival of the MMA warp that carries what it
+// saw of the tile's live keys), p_full (softmax warps, per half), h_done /
+// o_done (commits of PV's halves).  Every wait is bounded; one that gives up
+// raises `abort`, and every role goes to the end.
 // The kernel does not wait for its predecessor, the own keys' kernel, which
 // lets it start after everything before that one has completed; it does so at
 // its end, so that the join behind it finds both.
@@ -445,7 +448,10 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attention_kernel(const _
             }
             if (!ok) break;
             if (MT == 1 || (j & 1)) mma_commit(lead, &v_empty[st]);
-            if (j + 2 < jobs) ok = scores(j + 2);
+            if (j + 2 < jobs) {  // into the buffer that PV(j) reads: not before it is done
+                const int c = NS == 2 ? j >> 1 : j;
+                ok = __all_sync(FULL_MASK, mbar_wait_abort(&o_done[s], c & 1, abort)) && scores(j + 2);
+            }
         }
         // products already issued finish before tensor memory is freed
         mma_commit(lead, drained);
@@ -512,8 +518,11 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attention_kernel(const _
                         m = mn;
                         l2.x *= f, l2.y *= f;
                         if (h || c > 0) {
-                            ok = ok && __all_sync(FULL_MASK, h ? mbar_wait_abort(&h_done[s], c & 1, abort)
-                                                               : mbar_wait_abort(&o_done[s], (c - 1) & 1, abort));
+                            // (phase by phase: a wait for one that comes after the next would
+                            // pass at once.  S(c) was issued when PV(c - 2), with two streams
+                            // PV(c - 1), was done)
+                            if (c > 0) ok = ok && __all_sync(FULL_MASK, mbar_wait_abort(&o_done[s], (c - 1) & 1, abort));
+                            if (h) ok = ok && __all_sync(FULL_MASK, mbar_wait_abort(&h_done[s], c & 1, abort));
                             fence_after();
                             for (int d = 0; d < D; d += 16) {
                                 uint32_t w[16];
@@ -553,6 +562,7 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attention_kernel(const _
             }
             const float l = l2.x + l2.y;
             // the piece: (m, l) and O of this row, O only where some job ran
+            if (NS == 1 && ok && c > 1) ok = __all_sync(FULL_MASK, mbar_wait_abort(&o_done[s], (c - 2) & 1, abort));
             if (ok && c > 0) ok = __all_sync(FULL_MASK, mbar_wait_abort(&o_done[s], (c - 1) & 1, abort));
             const int row = row0 + r;
             const int piece = MT == 1 && NS == 2 ? 2 * split + s : split;
@@ -889,6 +899,21 @@ __global__ void __launch_bounds__(PJ_THREADS, 5) prefix_join_kernel(const __grid
 
 static int px_db(int D) { return D <= 64 ? 1 : D <= 128 ? 2 : 4; }
 static int px_group_rows(int D) { return px_streams(px_db(D)) * PX_ROWS; }
+
+// Whether the prefix is worth its own launch and the join: reading it by each
+// sequence costs (B - 1) more times its keys and values, the three launches and
+// the pieces some 3 to 10 us.  Measured (us, this form / one launch of the paged
+// kernel, B sequences with 60 own tokens):
+//   32 / 4 heads of 128, BF16: 128 x 128 19.0 / 12.7, 8 x 512 11.0 / 11.3,
+//     8 x 4096 17.5 / 19.9, 64 x 4096 28.5 / 50.0, 2 x 16384 17.7 / 18.9
+//   the same, E4M3: 64 x 1024 25.6 / 23.6, 8 x 4096 18.7 / 18.8, 4 x 16384 20.2 / 23.1
+//   8 / 8 of 64, FP16: 16 x 512 11.9 / 9.9, 64 x 512 13.5 / 17.7, 4 x 4096 13.2 / 13.8
+// so by what is saved, from four key tiles on; codes have to be widened first,
+// which the paged kernel does on its way.
+bool prefix_pays(int B, int Hkv, int D, int len, bool e4) {
+    const double saved = 2.0 * (B - 1) * len * Hkv * D;  // elements
+    return len >= 512 && saved >= (e4 ? 32e6 : 12e6);
+}
 
 // Runs that the prefix is cut into: the number that ends first, when a block's
 // time is its key tiles and about four of them for beginning and end, and

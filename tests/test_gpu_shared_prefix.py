@@ -76,6 +76,11 @@ def check(c, scale=None, ws=None, what=""):
     return out, lse
 
 
+def enough(Hkv, D, prefix, cache):
+    """Sequences from which the prefix is read by itself (below, each reads its own row)."""
+    return max(2, math.ceil((32e6 if cache == E4 else 12e6) / (2 * prefix * Hkv * D)) + 1)
+
+
 @pytest.fixture(autouse=True)
 def no_device_error(cuda_device):
     yield
@@ -85,43 +90,52 @@ def no_device_error(cuda_device):
 @pytest.mark.parametrize("dtype,cache", [(BF, BF), (HF, HF), (BF, E4), (HF, E4)])
 @pytest.mark.parametrize("D", [16, 48, 64, 80, 128, 144, 192, 256])
 def test_head_sizes(cuda_device, D, dtype, cache):
-    check(make(cuda_device, 5, 6, 3, D, 24, 24 * 17, [0, 7, 70, 1, 30], dtype, cache, seed=D, others=(3,)), what=f"D={D}")
+    prefix = 24 * 130
+    B = enough(3, D, prefix, cache)
+    check(make(cuda_device, B, 6, 3, D, 24, prefix, [(i * 7) % 40 for i in range(B)], dtype, cache, seed=D, others=(1,)),
+          what=f"D={D}")
 
 
-@pytest.mark.parametrize("prefix", [1, 15, 16, 63, 64, 65, 127, 128, 129, 255, 256, 257, 511, 777, 3001])
+@pytest.mark.parametrize("prefix", [1, 64, 511, 512, 513, 575, 576, 577, 639, 640, 641, 777, 1151, 1152, 3001])
 @pytest.mark.parametrize("dtype,cache", [(BF, BF), (HF, E4)])
 def test_prefix_lengths(cuda_device, prefix, dtype, cache):
-    check(make(cuda_device, 3, 8, 2, 64, 16, prefix, [0, 33, 5], dtype, cache, seed=prefix), what=f"prefix={prefix}")
+    B = min(enough(4, 128, prefix, cache), 80)
+    check(make(cuda_device, B, 8, 4, 128, 16, prefix, [(i * 11) % 50 for i in range(B)], dtype, cache, seed=prefix),
+          what=f"prefix={prefix}")
 
 
 @pytest.mark.parametrize("Hq,Hkv", [(1, 1), (4, 4), (8, 1), (9, 3), (20, 1), (40, 8), (64, 4), (128, 1)])
-@pytest.mark.parametrize("B", [1, 2, 13, 40])
+@pytest.mark.parametrize("B", [2, 13, 40])
 def test_rows_of_a_head(cuda_device, Hq, Hkv, B):
-    """1 to 5120 rows a key-value head: parts of a tile, one tile, two, and several groups of them."""
+    """2 to 5120 rows a key-value head: parts of a tile, one tile, two, and several groups of them."""
+    prefix = max(512, math.ceil(12e6 / (2 * (B - 1) * Hkv * 64)))
     own = [(i * 7) % 20 for i in range(B)]
-    check(make(cuda_device, B, Hq, Hkv, 64, 16, 300, own, HF, seed=Hq + B, others=(1,) if B > 2 else ()), what=f"{Hq}/{Hkv} B={B}")
+    check(make(cuda_device, B, Hq, Hkv, 64, 16, prefix, own, HF, seed=Hq + B, others=(1,) if B > 2 else ()), what=f"{Hq}/{Hkv} B={B}")
 
 
 @pytest.mark.parametrize("D,cache", [(128, BF), (256, BF), (128, E4), (256, E4)])
 def test_many_rows_of_wide_heads(cuda_device, D, cache):
-    check(make(cuda_device, 33, 16, 1, D, 32, 700, [i % 9 for i in range(33)], BF, cache, seed=D), what=f"D={D}")
+    check(make(cuda_device, 33, 16, 1, D, 32, 4100, [i % 9 for i in range(33)], BF, cache, seed=D), what=f"D={D}")
 
 
 @pytest.mark.parametrize("page", [1, 3, 8, 13, 100, 256])
 def test_page_sizes(cuda_device, page):
-    check(make(cuda_device, 4, 4, 2, 128, page, 999, [1, 99, 0, 31], BF, seed=page), what=f"page={page}")
+    B = enough(2, 128, 999, BF)
+    check(make(cuda_device, B, 4, 2, 128, page, 999, [(i * 37) % 100 for i in range(B)], BF, seed=page), what=f"page={page}")
 
 
 @pytest.mark.parametrize("cache", [BF, E4])
 def test_long_prefix(cuda_device, cache):
     check(make(cuda_device, 3, 16, 2, 128, 64, 40000, [5, 0, 300], BF, cache, seed=7, q_std=3.0), what="long")
+    if cache == BF:   # small pages: more of them than a block holds the places of
+        check(make(cuda_device, 2, 16, 1, 128, 1, 50000, [5, 9], BF, cache, seed=7), what="pages of one")
 
 
 def test_growing_scores(cuda_device):
     """Keys that grow along the prefix move the reference of the exponents again and again; shrinking ones leave a long tail."""
     for dtype, cache in ((BF, BF), (HF, HF), (BF, E4)):
         for rising in (True, False):
-            c = make(cuda_device, 4, 4, 1, 128, 16, 2048, [3, 0, 40, 9], dtype, cache, seed=3)
+            c = make(cuda_device, 33, 4, 1, 128, 32, 4096, [(i * 5) % 41 for i in range(33)], dtype, cache, seed=3)
             flat = (c["k"].double() * c["ks"])
             for i, pg in enumerate(c["shared"].tolist()):
                 x = (i if rising else 127 - i) / 16
@@ -133,20 +147,22 @@ def test_growing_scores(cuda_device):
 @pytest.mark.parametrize("scale", [0.0, -0.3, 1e-3, 2.0])
 @pytest.mark.parametrize("cache", [HF, E4])
 def test_scales(cuda_device, scale, cache):
-    check(make(cuda_device, 3, 8, 2, 64, 16, 300, [3, 0, 20], HF, cache, seed=5), scale=scale, what=f"scale={scale}")
+    B = enough(2, 64, 1300, cache)
+    check(make(cuda_device, B, 8, 2, 64, 16, 1300, [(i * 3) % 21 for i in range(B)], HF, cache, seed=5), scale=scale,
+          what=f"scale={scale}")
 
 
 def test_sequences_that_end_inside_the_prefix_or_are_empty(cuda_device):
-    c = make(cuda_device, 6, 8, 2, 64, 16, 200, [0, 10, 20, 30, 0, 5], BF, seed=11, others=(4,))
-    c["lens"] = torch.tensor([199, 0, 220, 37, 0, 200], dtype=torch.int32, device=cuda_device)
-    c["table"][5, 13:] = 1 << 29       # never looked up
+    c = make(cuda_device, 6, 8, 2, 128, 16, 5000, [0, 10, 20, 30, 0, 5], BF, seed=11, others=(4,))
+    c["lens"] = torch.tensor([4999, 0, 5020, 37, 0, 5000], dtype=torch.int32, device=cuda_device)
+    c["table"][5, 313:] = 1 << 29       # never looked up
     out, lse = check(c)
     assert bool((out[1] == 0).all()) and bool((out[4] == 0).all()) and bool((lse[1] == -math.inf).all())
 
 
 @pytest.mark.parametrize("order", ["nhd", "hnd"])
 def test_strides(cuda_device, order):
-    c = make(cuda_device, 5, 8, 2, 128, 16, 333, [5, 0, 17, 40, 2], BF, seed=12, order=order)
+    c = make(cuda_device, 5, 8, 2, 128, 16, 6333, [5, 0, 17, 40, 2], BF, seed=12, order=order)
     want, _ = check(c)
     g = torch.zeros(5, 3, 8, 136, dtype=BF, device=cuda_device)
     g[:, 1, :, :128] = c["q"]
@@ -165,7 +181,7 @@ def test_strides(cuda_device, order):
 def test_masked_places_are_not_read(cuda_device):
     """Infinities and NaN behind the prefix's end, in rows that a sequence does not see, and in the prefix for those that do
     not share it."""
-    c = make(cuda_device, 4, 8, 2, 64, 16, 200, [10, 0, 33, 17], BF, seed=13, others=(2,))
+    c = make(cuda_device, 4, 8, 2, 128, 16, 8008, [10, 0, 33, 17], BF, seed=13, others=(2,))
     want, wl = check(c)
     last = int(c["shared"][-1])
     c["k"][last, 8:] = float("nan")
@@ -181,7 +197,7 @@ def test_masked_places_are_not_read(cuda_device):
 
 
 def test_a_page_outside_the_cache_is_left_out(cuda_device):
-    c = make(cuda_device, 4, 8, 2, 64, 16, 512, [10, 0, 33, 17], BF, seed=14)
+    c = make(cuda_device, 4, 8, 2, 128, 16, 8000, [10, 0, 33, 17], BF, seed=14)
     for bad in (-1, 1 << 30, c["k"].shape[0]):
         c["shared"][5] = bad
         c["table"][:, 5] = bad
@@ -194,14 +210,15 @@ def test_nothing_shared_is_paged_attention(cuda_device):
     out, lse = check(c)
     want, wl = moe.paged_attention(c["q"], c["k"], c["v"], c["table"], c["lens"], return_lse=True)
     assert torch.equal(out, want) and torch.equal(lse, wl)
-    c = make(cuda_device, 4, 8, 2, 64, 16, 64, [10, 0, 33, 170], BF, seed=15)
-    c["shares"] = torch.zeros(4, dtype=torch.uint8, device=cuda_device)
-    check(c)
+    for prefix in (64, 8192):
+        c = make(cuda_device, 4, 8, 2, 128, 16, prefix, [10, 0, 33, 170], BF, seed=15)
+        c["shares"] = torch.zeros(4, dtype=torch.uint8, device=cuda_device)
+        check(c)
 
 
 def test_a_kept_workspace_serves_both_calls(cuda_device):
     ws = moe.shared_prefix_workspace(64, 16, 2, 128, cuda_device)
-    for i, (B, prefix) in enumerate(((64, 500), (3, 5000), (1, 64), (40, 129))):
+    for i, (B, prefix) in enumerate(((64, 700), (3, 15000), (1, 64), (40, 129), (33, 1000), (2, 25000))):
         c = make(cuda_device, B, 16, 2, 128, 16, prefix, [(j * 37) % 400 for j in range(B)], BF, seed=i)
         out, lse = check(c, ws=ws)
         again, l2 = call(c, ws=ws)
@@ -233,12 +250,12 @@ def test_two_streams_and_two_graphs(cuda_device):
 
 
 def test_lengths_move_under_a_captured_call(cuda_device):
-    c = make(cuda_device, 6, 8, 2, 64, 16, 320, [100] * 6, BF, seed=21)
-    ws = moe.shared_prefix_workspace(6, 8, 2, 64, cuda_device)
+    c = make(cuda_device, 6, 8, 2, 128, 16, 4800, [100] * 6, BF, seed=21)
+    ws = moe.shared_prefix_workspace(6, 8, 2, 128, cuda_device)
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
         out, lse = call(c, ws=ws)
-    for lens in ([320, 321, 400, 420, 0, 100], [319, 420, 330, 340, 350, 360]):
+    for lens in ([4800, 4801, 4880, 4900, 0, 100], [4799, 4900, 4810, 4820, 4830, 4840]):
         c["lens"].copy_(torch.tensor(lens, dtype=torch.int32))
         g.replay()
         torch.cuda.synchronize()
@@ -247,7 +264,7 @@ def test_lengths_move_under_a_captured_call(cuda_device):
 
 
 def test_outputs_over_the_query(cuda_device):
-    c = make(cuda_device, 5, 8, 2, 64, 16, 333, [5, 0, 17, 40, 2], BF, seed=22)
+    c = make(cuda_device, 5, 8, 2, 128, 16, 6333, [5, 0, 17, 40, 2], BF, seed=22)
     want, _ = check(c)
     got, _ = call(c, out=c["q"])
     torch.cuda.synchronize()
