@@ -558,6 +558,7 @@ int moe_shared_prefix_attention(const void* q, int64_t q_stride, int64_t q_head_
     size_t need = 0;
     const int rc = moe_shared_prefix_workspace_bytes(B, Hq, Hkv, D, &need);
     if (rc) return rc;
+    if (shared_len > INT32_MAX - 256) return MOE_ERR_LIMIT;
     if (shared_len > (int64_t)n_shared * page_size || shared_len > (int64_t)max_pages * page_size) return MOE_ERR_SHAPE;
     if (B == 0) return MOE_OK;
     if (shared_len > 0 && !shared_pages) return MOE_ERR_ARG;

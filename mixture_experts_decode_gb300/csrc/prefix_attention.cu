@@ -804,8 +804,8 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attention_kernel(const _
 // Every output from its pieces: the sequence's own and, where it shares the
 // prefix, the prefix's.  A thread takes four dims of a row, and a.join_groups
 // threads with the same dims divide the row's pieces between them, four or so
-// each with all loads in flight; the groups are added in order.  A piece of
-// weight 0 may hold anything.
+// each with all loads in flight; the groups are added in order.  A piece without
+// a score above -inf is left out (its sums may hold anything).
 constexpr int PJ_THREADS = 256, PJ_FLIGHT = 4;
 template <bool QBF>
 __global__ void __launch_bounds__(PJ_THREADS, 5) prefix_join_kernel(const __grid_constant__ PrefixArgs a) {
@@ -827,8 +827,8 @@ __global__ void __launch_bounds__(PJ_THREADS, 5) prefix_join_kernel(const __grid
         sum.x *= old, sum.y *= old, sum.z *= old, sum.w *= old;
     };
     auto add = [&](float2 ml, const float4& v) {
+        if (ml.x == -INFINITY) return;
         const float f = exp2_fast(ml.x - finite_or_zero(m));
-        if (f == 0.f) return;
         l += f * ml.y;
         sum.x += f * v.x, sum.y += f * v.y, sum.z += f * v.z, sum.w += f * v.w;
     };
@@ -906,13 +906,14 @@ static int px_group_rows(int D) { return px_streams(px_db(D)) * PX_ROWS; }
 // kernel, B sequences with 60 own tokens):
 //   32 / 4 heads of 128, BF16: 128 x 128 19.0 / 12.7, 8 x 512 11.0 / 11.3,
 //     8 x 4096 17.5 / 19.9, 64 x 4096 28.5 / 50.0, 2 x 16384 17.7 / 18.9
-//   the same, E4M3: 64 x 1024 25.6 / 23.6, 8 x 4096 18.7 / 18.8, 4 x 16384 20.2 / 23.1
+//   the same, E4M3: 64 x 1024 25.6 / 23.6, 8 x 4096 18.7 / 18.8, 4 x 16384 20.2 / 23.1;
+//     12 / 12 of 80: 7 x 5016 25.6 / 21.7, of 192: 32 x 512 21.7 / 22.9
 //   8 / 8 of 64, FP16: 16 x 512 11.9 / 9.9, 64 x 512 13.5 / 17.7, 4 x 4096 13.2 / 13.8
 // so by what is saved, from four key tiles on; codes have to be widened first,
 // which the paged kernel does on its way.
 bool prefix_pays(int B, int Hkv, int D, int len, bool e4) {
     const double saved = 2.0 * (B - 1) * len * Hkv * D;  // elements
-    return len >= 512 && saved >= (e4 ? 32e6 : 12e6);
+    return len >= 512 && saved >= (e4 ? 64e6 : 12e6);
 }
 
 // Runs that the prefix is cut into: the number that ends first, when a block's

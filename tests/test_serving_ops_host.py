@@ -30,7 +30,7 @@ def _prefix(lib, q=0x20000, qs=256, qh=64, B=2, Hq=4, Hkv=2, D=64, dtype=0, k=No
     (dict(B=-1), ARG), (dict(Hq=0), ARG), (dict(Hkv=0), ARG), (dict(D=0), ARG), (dict(page=0), ARG), (dict(pages=-1), ARG),
     (dict(most=-1), ARG), (dict(ns=-1), ARG), (dict(n=-1), ARG), (dict(dtype=2), ARG), (dict(cdt=1), ARG), (dict(cdt=7), ARG),
     (dict(Hq=5), SHAPE), (dict(D=72), SHAPE), (dict(D=272), LIMIT), (dict(B=1025), LIMIT), (dict(n=49), SHAPE),
-    (dict(n=65, ns=9), SHAPE), (dict(shared=None), ARG), (dict(shared=0x25002), ALIGN), (dict(q=None), ARG), (dict(lens=None), ARG),
+    (dict(n=65, ns=9), SHAPE), (dict(n=2 ** 31 - 1, page=2 ** 30, ns=4, most=4), LIMIT), (dict(shared=None), ARG), (dict(shared=0x25002), ALIGN), (dict(q=None), ARG), (dict(lens=None), ARG),
     (dict(out=None), ARG), (dict(table=None), ARG), (dict(k=_kv(None)), ARG), (dict(ws=None), WORKSPACE),
     (dict(wsb=1000), WORKSPACE), (dict(ws=0x50080), ALIGN), (dict(q=0x20008), ALIGN), (dict(qs=260), ALIGN),
     (dict(v=_kv(token=260)), ALIGN), (dict(cdt=3, k=_kv(head=72)), ALIGN), (dict(out=0x60001), ALIGN), (dict(lse=0x70002), ALIGN),
