@@ -629,7 +629,8 @@ int moe_router_grouped_topk(const void* logits, int64_t stride, int T, int E, in
  *   pages of all up to it pass the stack (and it needs one), its row has no
  *   entry left for it, or a length is negative: it gets no tokens and no
  *   pages, keeps its length, and MOE_DEVERR_POOL is set; what it asked for
- *   still counts before those behind it.
+ *   still counts before those behind it.  A page below 0 (in the row or on the
+ *   stack) gives its tokens slot -1 and sets MOE_DEVERR_PAGE.
  * Arguments
  *   past_lens, new_lens int32 [B].  block_table int32 [B][max_pages], row
  *   stride table_stride, in and out.  free_pages int32 [capacity], n_free
@@ -655,7 +656,8 @@ int moe_plan_pages(const int32_t* past_lens, const int32_t* new_lens, int B, int
  * where shares[b] (NULL: all).  *n_free_out gets the stack's new height and
  * seq_lens_out[b] = 0 for the ended, seq_lens[b] for the others.  Pages beyond
  * the stack's capacity are dropped and set MOE_DEVERR_POOL, as does a length
- * that is negative or beyond the row (cut).
+ * that is negative or beyond the row (cut); an entry below 0 is passed on and
+ * sets MOE_DEVERR_PAGE.
  *   seq_lens int32 [B], ended uint8 [B]; the others as in moe_plan_pages, with
  *   free_pages written from *n_free on.  seq_lens_out may be seq_lens and
  *   n_free_out may be n_free.

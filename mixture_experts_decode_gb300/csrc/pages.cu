@@ -66,7 +66,7 @@ __device__ __forceinline__ int last_at_most(const int32_t* begin, int n, int i) 
     return lo;
 }
 
-__device__ __forceinline__ int pages_of(int64_t tokens, int page) { return (int)((tokens + page - 1) / page); }
+__device__ __forceinline__ int64_t pages_of(int64_t tokens, int page) { return (tokens + page - 1) / page; }
 
 __device__ __forceinline__ int stack_height(const PagesArgs& a) {
     const int n = *a.n_free;
@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(PG_THREADS) plan_pages_kernel(const __grid_con
                 news[i] = -1;
             } else {
                 news[i] = n;
-                needs[i] = pages_of((int64_t)p + n, a.page) - pages_of(p, a.page);
+                needs[i] = (int)(pages_of((int64_t)p + n, a.page) - pages_of(p, a.page));  // at most n
                 sum = sum + Pair{n, needs[i]};
             }
         }
@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(PG_THREADS) plan_pages_kernel(const __grid_con
                 while (starts[b + 1] <= t) ++b;
                 const int p = past[b] + (t - starts[b]);
                 const int pi = p / a.page, off = p - pi * a.page;
-                const int have = pages_of(past[b], a.page);
+                const int have = (int)pages_of(past[b], a.page);
                 int32_t* const entry = a.table + b * a.table_stride + pi;
                 int pg;
                 if (pi < have) {
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(PG_THREADS) release_pages_kernel(const __grid_
             const int p = a.past[b];
             past[b] = p;
             if (a.ended[b]) {
-                const int64_t have = p < 0 ? 0 : ((int64_t)p + a.page - 1) / a.page;
+                const int64_t have = p < 0 ? 0 : pages_of(p, a.page);
                 if (p < 0 || have > a.max_pages) bad = true;
                 const int skip = !a.shares || a.shares[b] ? a.shared_n : 0;
                 goes[i] = max(0, (int)min(have, (int64_t)a.max_pages) - skip);

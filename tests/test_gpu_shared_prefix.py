@@ -216,6 +216,34 @@ def test_infinities_and_nan_among_visible_values(cuda_device):
             assert torch.equal(bad, seen) and torch.equal(out[~bad], want[~bad])
 
 
+def test_infinite_keys(cuda_device):
+    """A score of -inf leaves its key out, one of +inf makes its head's output NaN, in the shared part too."""
+    for dtype in (BF, HF):
+        for pg, row in ((0, 0), (100, 7), (511, 15)):
+            c = make(cuda_device, 17, 8, 2, 128, 16, 8192, [10 + i for i in range(17)], dtype, seed=29, others=(2,))
+            sign = torch.where(torch.rand(17, 4, device=cuda_device) < 0.5, -1.0, 1.0).to(dtype)
+            c["q"][:, 4:, 9] = sign
+            k = c["k"].clone()
+            c["k"][int(c["shared"][pg]), row, 1, 9] = 6e4    # (weight 0 where the query's value is -1)
+            want, _ = call(c)
+            k[int(c["shared"][pg]), row, 1, 9] = float("inf")
+            out, _ = call(dict(c, k=k))
+            torch.cuda.synchronize()
+            nan = torch.zeros_like(out, dtype=torch.bool)
+            nan[:, 4:] = (sign > 0)[..., None]
+            nan[2] = False
+            assert torch.equal(torch.isnan(out), nan) and torch.equal(out[~nan], want[~nan])
+
+
+def test_out_may_be_the_query(cuda_device):
+    for prefix in (100, 8000):
+        c = make(cuda_device, 9, 8, 2, 128, 16, prefix, [3 * i for i in range(9)], BF, seed=31)
+        want, wl = check(c)
+        out, lse = call(c, out=c["q"])
+        torch.cuda.synchronize()
+        assert out.data_ptr() == c["q"].data_ptr() and torch.equal(out, want) and torch.equal(lse, wl)
+
+
 def test_a_page_outside_the_cache_is_left_out(cuda_device):
     c = make(cuda_device, 4, 8, 2, 128, 16, 8000, [10, 0, 33, 17], BF, seed=14)
     for bad in (-1, 1 << 30, c["k"].shape[0]):
