@@ -52,17 +52,22 @@ constexpr int PX_THREADS = (PX_VW + 2) * 32;
 constexpr int px_streams(int db) { return db == 4 ? 1 : 2; }  // (two sums of 256 columns would leave no room for scores)
 constexpr int px_keys(int db) { return db == 4 ? 64 : 128; }  // keys of a tile
 constexpr int px_half(int db) { return db * px_keys(db) * 128; }  // bytes of a K (or V) tile of 16-bit values
-// Stages of 16-bit tiles, and for an E4M3 cache of codes in front of them: there
-// the codes' stages hide the latency, and a widened tile is wanted again only
-// when the softmax between two uses is over.
-constexpr int px_stages(int db, bool e4) { return db == 1 ? (e4 ? 2 : 4) : (e4 ? 1 : 2); }
-constexpr int px_code_stages(int db, bool e4) { return !e4 ? 0 : db == 1 ? 3 : 2; }
+// Stages of 16-bit tiles, and for an E4M3 cache of codes in front of them.  A
+// widened K tile is wanted again only when the softmax between two uses is over,
+// so one stage does where room is short; V's next tile is wanted as soon as the
+// last is let go, so it has two, and one of codes, which the whole time of a
+// tile is there to fill (64 x 65536 tokens: 166 us; with one of V and two of its
+// codes 182).
+constexpr int px_k_stages(int db, bool e4) { return db == 1 ? (e4 ? 2 : 4) : (e4 ? 1 : 2); }
+constexpr int px_v_stages(int db, bool e4) { return db == 1 && !e4 ? 4 : 2; }
+constexpr int px_k_codes(int db, bool e4) { return !e4 ? 0 : db == 1 ? 3 : 2; }
+constexpr int px_v_codes(int db, bool e4) { return !e4 ? 0 : db == 1 ? 3 : 1; }
 // Masks of live keys that are kept: when tile t's is written, the scores of the
 // tile a stage count before it have been issued, so the softmax of the tile two
 // before that is over.
-constexpr int px_masks(int db, bool e4) { return px_stages(db, e4) + px_code_stages(db, e4) + 4; }
+constexpr int px_masks(int db, bool e4) { return px_k_stages(db, e4) + px_k_codes(db, e4) + 4; }
 
-constexpr int PX_PAGES = 1024;  // pages, of K and of V, whose places shared memory holds
+constexpr int PX_PAGES = 512;  // pages, of K and of V, whose places shared memory holds
 
 struct PxLayout {
     uint32_t k, v, codes, pages, rows, live, back, bars, slot, abort, total;
@@ -70,14 +75,14 @@ struct PxLayout {
 constexpr PxLayout px_layout(int db, bool e4) {
     PxLayout L{};
     uint32_t off = (uint32_t)px_streams(db) * db * PX_ROWS * 128;  // Q first
-    L.k = off;     off += px_stages(db, e4) * px_half(db);
-    L.v = off;     off += px_stages(db, e4) * px_half(db);
-    L.codes = off; off += 2 * px_code_stages(db, e4) * (px_half(db) / 2);
+    L.k = off;     off += px_k_stages(db, e4) * px_half(db);
+    L.v = off;     off += px_v_stages(db, e4) * px_half(db);
+    L.codes = off; off += (px_k_codes(db, e4) + px_v_codes(db, e4)) * (px_half(db) / 2);
     L.pages = off; off += 2 * PX_PAGES * 8;
     L.rows = off;  off += 2 * 2 * 128 * 8;
     L.live = off;  off += px_masks(db, e4) * 16;
     L.back = off;  off += 2 * PX_ROWS * 4;
-    L.bars = off;  off += (4 * px_stages(db, e4) + 12) * 8;
+    L.bars = off;  off += (2 * px_k_stages(db, e4) + 2 * px_v_stages(db, e4) + 12) * 8;
     L.slot = off;  off += 8;
     L.abort = off; off += 8;
     L.total = off;
@@ -266,7 +271,7 @@ __device__ __forceinline__ uint4 ld_128_l2(const void* p) {
 // two halves of the keys, each as soon as its weights are there, and S(j + 2)
 // when PV(j), which reads its weights from the same buffer, is done (products
 // of different shapes and accumulators are not promised to run in order; the
-// wait costs 162 -> 180 us at 64 x 65536 tokens).
+// wait costs some 10 % at 64 x 65536 tokens).
 // Barriers: q_full, k_full / v_full (those that bring; their writes are generic,
 // so the MMA warp fences before the tensor cores read), k_empty / v_empty
 // (commits), s_full (commit, and an arrival of the MMA warp that carries what it
@@ -279,7 +284,8 @@ __device__ __forceinline__ uint4 ld_128_l2(const void* p) {
 template <int DB, int KV, bool QBF>
 __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attention_kernel(const __grid_constant__ PrefixArgs a) {
     constexpr bool E4 = KV == KV_E4M3;
-    constexpr int NS = px_streams(DB), KT = px_keys(DB), ST = px_stages(DB, E4), HALF = px_half(DB), MASKS = px_masks(DB, E4);
+    constexpr int NS = px_streams(DB), KT = px_keys(DB), HALF = px_half(DB), MASKS = px_masks(DB, E4);
+    constexpr int KS = px_k_stages(DB, E4), VS = px_v_stages(DB, E4);
     constexpr bool BF = KV == KV_BF16;          // operand type of the products
     constexpr bool LO = !(E4 && QBF);  // P as hi + lo
     constexpr float P_SHIFT = BF ? 0.f : 7.f;
@@ -289,10 +295,10 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attention_kernel(const _
     extern __shared__ __align__(1024) uint8_t px_smem[];
     uint8_t* const sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(px_smem) + 1023) & ~uintptr_t(1023));
     uint64_t* const k_full = reinterpret_cast<uint64_t*>(sm + L.bars);
-    uint64_t* const k_empty = k_full + ST;
-    uint64_t* const v_full = k_full + 2 * ST;
-    uint64_t* const v_empty = k_full + 3 * ST;
-    uint64_t* const s_full = k_full + 4 * ST;
+    uint64_t* const k_empty = k_full + KS;
+    uint64_t* const v_full = k_empty + KS;
+    uint64_t* const v_empty = v_full + VS;
+    uint64_t* const s_full = v_empty + VS;
     uint64_t* const p_full = s_full + 2;
     uint64_t* const o_done = s_full + 6;  // (p_full: [buffer][half])
     uint64_t* const h_done = s_full + 8;
@@ -318,9 +324,11 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attention_kernel(const _
     const int D = a.D;
 
     if (tid == 0) {
-        for (int i = 0; i < ST; ++i) {
+        for (int i = 0; i < KS; ++i) {
             mbar_init(&k_full[i], E4 ? 2 : PX_BRING + 2);
             mbar_init(&k_empty[i], 1);
+        }
+        for (int i = 0; i < VS; ++i) {
             mbar_init(&v_full[i], E4 ? 2 : PX_BRING);
             mbar_init(&v_empty[i], 1);
         }
@@ -407,8 +415,8 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attention_kernel(const _
         const int nk = D / 16;
         bool ok = __all_sync(FULL_MASK, mbar_wait_abort(q_full, 0, abort));
         auto scores = [&](int j) {
-            const int t = MT == 2 ? j >> 1 : j, st = t % ST;
-            if (!__all_sync(FULL_MASK, mbar_wait_abort(&k_full[st], (t / ST) & 1, abort))) return false;
+            const int t = MT == 2 ? j >> 1 : j, st = t % KS;
+            if (!__all_sync(FULL_MASK, mbar_wait_abort(&k_full[st], (t / KS) & 1, abort))) return false;
             fence_proxy_async();
             fence_after();
             const uint32_t q = q0 + (MT == 2 ? (j & 1) * (DB * PX_ROWS * 128 >> 4) : 0), k = k0 + st * (HALF >> 4);
@@ -425,8 +433,8 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attention_kernel(const _
         };
         for (int j = 0; j < 2 && j < jobs && ok; ++j) ok = scores(j);
         for (int j = 0; j < jobs && ok; ++j) {
-            const int t = MT == 2 ? j >> 1 : j, st = t % ST, s = NS == 2 ? j & 1 : 0;
-            if (!__all_sync(FULL_MASK, mbar_wait_abort(&v_full[st], (t / ST) & 1, abort))) {
+            const int t = MT == 2 ? j >> 1 : j, st = t % VS, s = NS == 2 ? j & 1 : 0;
+            if (!__all_sync(FULL_MASK, mbar_wait_abort(&v_full[st], (t / VS) & 1, abort))) {
                 ok = false;
                 break;
             }
@@ -616,6 +624,7 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attention_kernel(const _
         uint64_t* const empty = is_v ? v_empty : k_empty;
         uint8_t* const ring = sm + (is_v ? L.v : L.k);
         constexpr int ES = E4 ? 1 : 2;
+        const int stages = KS == VS ? KS : is_v ? VS : KS;
         const int64_t sp = (is_v ? a.v_sp : a.k_sp) * ES, stt = (is_v ? a.v_st : a.k_st) * ES;
         const uint8_t* const src = static_cast<const uint8_t*>(is_v ? a.v : a.k) + (int64_t)kvh * (is_v ? a.v_sh : a.k_sh) * ES;
 
@@ -681,9 +690,9 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attention_kernel(const _
                 const uint32_t col = (c >> 3) * (KT * 128);
                 const uint8_t* const from = src + c * 16;
                 for (int t = 0; t < tiles; ++t) {
-                    const int st = t % ST;
+                    const int st = t % stages;
                     find_rows(t);
-                    if (t >= ST && ok) ok = __all_sync(FULL_MASK, mbar_wait_abort(&empty[st], ((t / ST) - 1) & 1, abort));
+                    if (t >= stages && ok) ok = __all_sync(FULL_MASK, mbar_wait_abort(&empty[st], ((t / stages) - 1) & 1, abort));
                     if (!ok) continue;  // (the two warps stay together in find_rows)
                     uint8_t* const dst = ring + st * HALF + col;
                     const int64_t* const o = rows_of + (t & 1) * 128 + r0;
@@ -710,9 +719,11 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attention_kernel(const _
                 // whole head eight lanes take 4 pieces of each of two rows, so
                 // that they write the 8 different 16-byte columns of the swizzle;
                 // else they go row by row.
-                constexpr int PER = KT * DB * 4 / PX_BRING, RS = px_code_stages(DB, E4);  // pieces of a thread at most
+                constexpr int PER = KT * DB * 4 / PX_BRING;  // pieces of a thread at most
+                constexpr int KC = px_k_codes(DB, E4), VC = px_v_codes(DB, E4);
+                const int ahead = KC == VC ? KC : is_v ? VC : KC;
                 constexpr int BATCH = PER < 8 ? PER : 8;  // pieces that are read before any of them is written
-                uint8_t* const codes = sm + L.codes + (is_v ? RS * (HALF / 2) : 0) + pt * 16;
+                uint8_t* const codes = sm + L.codes + (is_v ? KC * (HALF / 2) : 0) + pt * 16;
                 const int CH = W ? DB * 4 : D / 16, unit = pt >> 3;
                 const int row0 = W ? 2 * (unit / DB) + (pt >> 2 & 1) : pt / CH, c0 = W ? 4 * (unit % DB) + (pt & 3) : pt % CH;
                 const int dr = W ? 16 / DB : PX_BRING / CH, dc = W ? 0 : PX_BRING % CH;
@@ -727,7 +738,7 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attention_kernel(const _
                     if (t < tiles) {
                         find_rows(t);
                         const int64_t* const o = rows_of + (t & 1) * 128;
-                        uint8_t* const to = codes + (t % RS) * (HALF / 2);
+                        uint8_t* const to = codes + (t % ahead) * (HALF / 2);
                         int row = row0, c = c0;
                         if (!W) asm volatile("" : "+r"(row), "+r"(c));  // (16 pieces' steps are not worth registers)
 #pragma unroll
@@ -748,14 +759,19 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attention_kernel(const _
                     cp_async_commit();
                 };
 #pragma unroll 1
-                for (int t = 0; t < RS - 1; ++t) copy(t);
+                for (int t = 0; t < ahead; ++t) copy(t);
                 for (int t = 0; t < tiles; ++t) {
-                    const int st = t % ST;
-                    copy(t + RS - 1);
-                    cp_async_wait<RS - 1>();
-                    if (t >= ST && ok) ok = __all_sync(FULL_MASK, mbar_wait_abort(&empty[st], ((t / ST) - 1) & 1, abort));
-                    if (!ok) continue;
-                    const uint8_t* const from = codes + (t % RS) * (HALF / 2);
+                    const int st = t % stages;
+                    if (KC == VC || !is_v)
+                        cp_async_wait<KC - 1>();
+                    else
+                        cp_async_wait<VC - 1>();
+                    if (t >= stages && ok) ok = __all_sync(FULL_MASK, mbar_wait_abort(&empty[st], ((t / stages) - 1) & 1, abort));
+                    if (!ok) {
+                        copy(t + ahead);  // (as above)
+                        continue;
+                    }
+                    const uint8_t* const from = codes + (t % ahead) * (HALF / 2);
                     uint8_t* const dst = ring + st * HALF;
                     int row = row0, c = c0;
                     if (!W) asm volatile("" : "+r"(row), "+r"(c));
@@ -781,6 +797,7 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attention_kernel(const _
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&full[st]);
+                    copy(t + ahead);
                 }
             }
         };
@@ -806,9 +823,9 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attention_kernel(const _
 // threads with the same dims divide the row's pieces between them, four or so
 // each with all loads in flight; the groups are added in order.  A piece without
 // a score above -inf is left out (its sums may hold anything).
-constexpr int PJ_THREADS = 256, PJ_FLIGHT = 4;
+constexpr int PJ_THREADS = 256, PJ_FLIGHT = 4, PJ_BLOCKS = 5;  // (blocks of an SM)
 template <bool QBF>
-__global__ void __launch_bounds__(PJ_THREADS, 5) prefix_join_kernel(const __grid_constant__ PrefixArgs a) {
+__global__ void __launch_bounds__(PJ_THREADS, PJ_BLOCKS) prefix_join_kernel(const __grid_constant__ PrefixArgs a) {
     __shared__ float4 sm_o[PJ_THREADS];
     __shared__ float2 sm_ml[PJ_THREADS];
     const int vecs = a.D / 4, per_row = vecs * a.join_groups;
@@ -997,9 +1014,14 @@ cudaError_t launch_shared_prefix(PrefixArgs a, const AttnArgs& own, int dtype, i
     else
         e = dtype == MOE_BF16 ? launch_px_kv<KV_BF16, true>(a, di, grid, st) : launch_px_kv<KV_F16, false>(a, di, grid, st);
     if (e != cudaSuccess) return e;
-    const int np = (a.B * a.G) % a.group_rows <= PX_ROWS ? a.pieces : a.splits, vecs = a.D / 4;
+    // (threads beyond what is resident at once would take another round: without
+    // that limit 32 x 8192 tokens 31.3 us in place of 29.4, 64 x 65536 166 for 161)
+    const int np = a.B * a.G <= PX_ROWS ? a.pieces : a.splits, vecs = a.D / 4;
+    const int64_t resident = (int64_t)di.sm_count * PJ_BLOCKS * PJ_THREADS;
     a.join_groups = 1;
-    while (a.join_groups * PJ_FLIGHT < np && 2 * a.join_groups * vecs <= PJ_THREADS) a.join_groups *= 2;
+    while (a.join_groups * PJ_FLIGHT < np && 2 * a.join_groups * vecs <= PJ_THREADS &&
+           2 * a.join_groups * (int64_t)vecs * (int64_t)rows <= resident)
+        a.join_groups *= 2;
     const int per_block = PJ_THREADS / (vecs * a.join_groups);
     const dim3 blocks((unsigned)((rows + per_block - 1) / per_block));
     return dtype == MOE_BF16 ? launch_after(prefix_join_kernel<true>, blocks, PJ_THREADS, 0, st, a)
