@@ -7,8 +7,9 @@
 // takes its share of the tokens (or pages), each found by a binary search in
 // the scan: nothing is handed from one block to another, so one launch does
 // all of it.  Lengths and the stack's height may be updated in place; a call
-// of several blocks then writes them in a launch of its own, behind the blocks
-// that read them.
+// of several blocks then writes them in a launch of its own, which begins when
+// all blocks have read them (it waits for what they still write at its end, so
+// that what follows finds everything).
 // Bound: latency for a decode step; for long prompts the 16 bytes written per
 // token.
 #include <algorithm>
@@ -66,7 +67,11 @@ __device__ __forceinline__ int last_at_most(const int32_t* begin, int n, int i) 
     return lo;
 }
 
-__device__ __forceinline__ int64_t pages_of(int64_t tokens, int page) { return (tokens + page - 1) / page; }
+// ceil(tokens / page), for all of 32 bits (64-bit quotients take several times as long).
+__device__ __forceinline__ uint32_t pages_of(uint32_t tokens, uint32_t page) {
+    const uint32_t q = tokens / page;
+    return q + (q * page != tokens);
+}
 
 __device__ __forceinline__ int stack_height(const PagesArgs& a) {
     const int n = *a.n_free;
@@ -82,7 +87,7 @@ __global__ void __launch_bounds__(PG_THREADS) plan_pages_kernel(const __grid_con
     int32_t* const starts = sm;             // [B + 1] first token
     int32_t* const past = starts + a.B + 1; // [B]
     int32_t* const base = past + a.B;       // [B] first new page, counted from the stack's top
-    after_previous();
+    if (a.parts != PAGES_STATE) after_previous();
     const int tid = threadIdx.x;
     const int height = stack_height(a);
     const int64_t cap = min((int64_t)a.max_pages * a.page, (int64_t)INT32_MAX);
@@ -104,13 +109,14 @@ __global__ void __launch_bounds__(PG_THREADS) plan_pages_kernel(const __grid_con
                 news[i] = -1;
             } else {
                 news[i] = n;
-                needs[i] = (int)(pages_of((int64_t)p + n, a.page) - pages_of(p, a.page));  // at most n
+                needs[i] = (int)(pages_of((uint32_t)p + (uint32_t)n, a.page) - pages_of(p, a.page));  // at most n
                 sum = sum + Pair{n, needs[i]};
             }
         }
     }
-    Pair at = block_exclusive(sum, &all);
-    Pair got = {0, 0};
+    const Pair first = block_exclusive(sum, &all);
+    Pair at = first, got = {0, 0};
+    bool dropped = false;
 #pragma unroll
     for (int i = 0; i < PG_ITEMS; ++i) {
         const int b = tid * per + i;
@@ -122,13 +128,17 @@ __global__ void __launch_bounds__(PG_THREADS) plan_pages_kernel(const __grid_con
             at = at + Pair{news[i], needs[i]};
             const bool fits = at.a <= a.T && (needs[i] == 0 || at.b <= height) && (int64_t)past[b] + news[i] <= cap;
             if (!fits) {
-                refused |= news[i] > 0;
+                dropped |= news[i] > 0;
                 news[i] = needs[i] = 0;
             }
             got = got + Pair{news[i], needs[i]};
         }
     }
-    at = block_exclusive(got, &all);
+    at = first;
+    if (__syncthreads_or(dropped)) {  // the sums of what is left
+        refused |= dropped;
+        at = block_exclusive(got, &all);
+    }
 #pragma unroll
     for (int i = 0; i < PG_ITEMS; ++i) {
         const int b = tid * per + i;
@@ -148,8 +158,12 @@ __global__ void __launch_bounds__(PG_THREADS) plan_pages_kernel(const __grid_con
             for (int b = tid; b < a.B; b += PG_THREADS) a.lens_out[b] = past[b] + starts[b + 1] - starts[b];
             if (tid == 0) *a.n_free_out = height - (int)all.b;
         }
-        if (!(a.parts & PAGES_ROWS)) return;
+        if (!(a.parts & PAGES_ROWS)) {
+            after_previous();
+            return;
+        }
     }
+    if (a.parts == PAGES_ROWS) let_next_start();  // (all that the state's launch writes has been read)
     if (blockIdx.x == 0)
         for (int b = tid; b <= a.B; b += PG_THREADS) a.starts[b] = starts[b];
     // requests that begin behind the shared prefix: its pages
@@ -166,24 +180,32 @@ __global__ void __launch_bounds__(PG_THREADS) plan_pages_kernel(const __grid_con
         int32_t pos[PG_GROUP], seq[PG_GROUP];
         int64_t slot[PG_GROUP];
         int b = t0 < total ? last_at_most(starts, a.B, (int)t0) : a.B;
+        int p = 0, pi = 0, off = 0, have = 0, pg = 0;
+        bool found = false;  // p .. have are of request b
 #pragma unroll
         for (int i = 0; i < PG_GROUP; ++i) {
             const int t = (int)t0 + i;
             pos[i] = 0, seq[i] = -1, slot[i] = -1;
             if (t0 + i < total) {
-                while (starts[b + 1] <= t) ++b;
-                const int p = past[b] + (t - starts[b]);
-                const int pi = p / a.page, off = p - pi * a.page;
-                const int have = (int)pages_of(past[b], a.page);
-                int32_t* const entry = a.table + b * a.table_stride + pi;
-                int pg;
-                if (pi < have) {
-                    pg = *entry;
-                } else {
-                    pg = a.free_pages[height - 1 - (base[b] + pi - have)];
-                    if (off == 0) *entry = pg;  // the page's first token puts it into the table
+                while (starts[b + 1] <= t) ++b, found = false;
+                if (!found) {
+                    p = past[b] + (t - starts[b]);
+                    pi = (int)((uint32_t)p / (uint32_t)a.page), off = p - pi * a.page;
+                    have = (int)pages_of(past[b], a.page);
+                } else if (++p, ++off == a.page) {
+                    off = 0, ++pi;
                 }
-                if (pg < 0) atomicOr(a.err, MOE_DEVERR_PAGE);
+                if (!found || off == 0) {
+                    int32_t* const entry = a.table + b * a.table_stride + pi;
+                    if (pi < have) {
+                        pg = *entry;
+                    } else {
+                        pg = a.free_pages[height - 1 - (base[b] + pi - have)];
+                        if (off == 0) *entry = pg;  // the page's first token puts it into the table
+                    }
+                    if (pg < 0) atomicOr(a.err, MOE_DEVERR_PAGE);
+                    found = true;
+                }
                 pos[i] = p, seq[i] = b;
                 slot[i] = pg < 0 ? -1 : (int64_t)pg * a.page + off;
             }
@@ -208,7 +230,7 @@ __global__ void __launch_bounds__(PG_THREADS) release_pages_kernel(const __grid_
     extern __shared__ int32_t sm[];
     int32_t* const begin = sm;            // [B + 1] first page among those that go
     int32_t* const past = sm + a.B + 1;   // [B]
-    after_previous();
+    if (a.parts != PAGES_STATE) after_previous();
     const int tid = threadIdx.x;
     const int height = stack_height(a);
     const int per = (a.B + PG_THREADS - 1) / PG_THREADS;
@@ -251,8 +273,12 @@ __global__ void __launch_bounds__(PG_THREADS) release_pages_kernel(const __grid_
             for (int b = tid; b < a.B; b += PG_THREADS) a.lens_out[b] = a.ended[b] ? 0 : past[b];
             if (tid == 0) *a.n_free_out = height + total;
         }
-        if (!(a.parts & PAGES_ROWS)) return;
+        if (!(a.parts & PAGES_ROWS)) {
+            after_previous();
+            return;
+        }
     }
+    if (a.parts == PAGES_ROWS) let_next_start();  // (all that the state's launch writes has been read)
     for (int64_t i0 = ((int64_t)blockIdx.x * PG_THREADS + tid) * PG_GROUP; i0 < total;
          i0 += (int64_t)gridDim.x * PG_THREADS * PG_GROUP) {
         int b = last_at_most(begin, a.B, (int)i0);
