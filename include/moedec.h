@@ -564,7 +564,8 @@ int moe_matvec4(const void* x, int64_t x_stride, int T, int K, int dtype, const 
  *   may serve moe_paged_attention calls too, one after the other.
  * Launches: three (own keys, prefix, join), or one of moe_paged_attention's where
  * little would be saved (shared_len below 512, or (B - 1) * shared_len * Hkv * D
- * keys' and values' elements, twice, below 12 million; 64 million of E4M3).
+ * keys' and values' elements, twice, below 12 million; of E4M3 64 million, or B
+ * below 3).
  * Limits as there; shared_len <= n_shared * page_size and <= max_pages *
  * page_size, and below 2^31 - 256.
  */

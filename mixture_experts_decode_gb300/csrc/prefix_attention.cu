@@ -26,8 +26,12 @@
 // of the output's rounding, and lo is left out.  A BF16 query against E4M3 keys
 // goes to FP16 by a power of two per row, as there.
 //
-// Bound: HBM for few rows (the prefix once), the tensor pipe and the softmax
-// for many.
+// Bound: HBM for few rows (the prefix once); for many the chain score product,
+// softmax, value product, score product of a stream, with the tensor pipe active
+// half of the time.  Measured, whole calls: 64 sequences over 65536 tokens, 64 /
+// 8 heads of 128, E4M3 161 us (857 TFLOP/s; one launch of the paged kernel 1010);
+// 32 over 8192, 32 / 4 of 128, BF16, chats of up to 1500 tokens 29.5 us (45); 300
+// over 9600, 16 / 2 of 64, FP16 48.5 us (142).
 #include <algorithm>
 #include <type_traits>
 
@@ -921,16 +925,17 @@ static int px_group_rows(int D) { return px_streams(px_db(D)) * PX_ROWS; }
 // sequence costs (B - 1) more times its keys and values, the three launches and
 // the pieces some 3 to 10 us.  Measured (us, this form / one launch of the paged
 // kernel, B sequences with 60 own tokens):
-//   32 / 4 heads of 128, BF16: 128 x 128 19.0 / 12.7, 8 x 512 11.0 / 11.3,
-//     8 x 4096 17.5 / 19.9, 64 x 4096 28.5 / 50.0, 2 x 16384 17.7 / 18.9
-//   the same, E4M3: 64 x 1024 25.6 / 23.6, 8 x 4096 18.7 / 18.8, 4 x 16384 20.2 / 23.1;
-//     12 / 12 of 80: 7 x 5016 25.6 / 21.7, of 192: 32 x 512 21.7 / 22.9
-//   8 / 8 of 64, FP16: 16 x 512 11.9 / 9.9, 64 x 512 13.5 / 17.7, 4 x 4096 13.2 / 13.8
+//   32 / 4 heads of 128, BF16: 128 x 128 19.0 / 12.7, 8 x 512 11.0 / 11.2, 32 x 512
+//     13.9 / 13.3, 8 x 4096 17.0 / 19.4, 64 x 4096 24.0 / 49.8, 2 x 16384 17.6 / 18.9
+//   the same, E4M3: 64 x 1024 23.3 / 23.5, 8 x 4096 18.5 / 18.5, 4 x 16384 19.8 / 23.0,
+//     32 x 4096 24.9 / 29.3, 2 x 65536 37.6 / 30.2
+//   12 / 12, E4M3: 7 x 5016 of 80 23.9 / 23.7, 32 x 512 of 192 20.8 / 23.8
+//   8 / 8 of 64, FP16: 16 x 512 12.2 / 9.9, 32 x 512 12.9 / 13.2, 64 x 512 13.7 / 17.3
 // so by what is saved, from four key tiles on; codes have to be widened first,
-// which the paged kernel does on its way.
+// which the paged kernel does on its way: they take more, and three sequences.
 bool prefix_pays(int B, int Hkv, int D, int len, bool e4) {
     const double saved = 2.0 * (B - 1) * len * Hkv * D;  // elements
-    return len >= 512 && saved >= (e4 ? 64e6 : 12e6);
+    return len >= 512 && saved >= (e4 ? 64e6 : 12e6) && !(e4 && B < 3);
 }
 
 // Runs that the prefix is cut into: the number that ends first, when a block's

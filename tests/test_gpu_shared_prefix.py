@@ -78,7 +78,7 @@ def check(c, scale=None, ws=None, what=""):
 
 def enough(Hkv, D, prefix, cache):
     """Sequences from which the prefix is read by itself (below, each reads its own row)."""
-    return max(2, math.ceil((64e6 if cache == E4 else 12e6) / (2 * prefix * Hkv * D)) + 1)
+    return max(3 if cache == E4 else 2, math.ceil((64e6 if cache == E4 else 12e6) / (2 * prefix * Hkv * D)) + 1)
 
 
 @pytest.fixture(autouse=True)
