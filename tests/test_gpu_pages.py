@@ -105,6 +105,11 @@ def test_lengths_whose_sum_passes_32_bits(cuda_device):
         check_plan(cuda_device, [0, top, 0, top - 1], [2, top, 2, top], [[5, 6]] * 4, [9, 8, 3], 3, page, 9)
 
 
+def test_slots_past_32_bits(cuda_device):
+    top = 2 ** 31 - 1
+    check_plan(cuda_device, [0, 70, 64], [100, 3, 1], [[-1, -1], [top - 7, top - 8], [5, -1]], [9, 8, top - 3, top, top - 1], 5, 64, 110)
+
+
 def test_a_stack_height_out_of_range_is_cut(cuda_device):
     for n, ok in ((-3, 0), (5, 2)):
         got = moe.plan_pages(i32(cuda_device, [0, 0]), i32(cuda_device, [1, 1]), i32(cuda_device, [[-1], [-1]]),

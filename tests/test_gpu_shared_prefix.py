@@ -235,6 +235,24 @@ def test_infinite_keys(cuda_device):
             assert torch.equal(torch.isnan(out), nan) and torch.equal(out[~nan], want[~nan])
 
 
+@pytest.mark.parametrize("cache", [BF, E4])
+def test_caches_whose_offsets_pass_32_bits(cuda_device, cache):
+    B = enough(2, 128, 640, cache)
+    c = make(cuda_device, B, 8, 2, 128, 64, 640, [(i * 5) % 64 for i in range(B)], BF, cache, seed=37)
+    want, wl = check(c)
+    pages = c["k"].shape[0]
+    step = -(-(2 ** 32 + 2 ** 28) // pages) // 16 * 16 + 16     # elements: the last pages begin behind 2^32
+    buf = torch.empty(2 * pages * step, dtype=torch.uint8 if cache == E4 else cache, device=cuda_device)
+    far = []
+    for i, t in enumerate((c["k"], c["v"])):
+        f = buf.as_strided(t.shape, (step, *t.stride()[1:]), i * pages * step)
+        f.copy_(t.view(torch.uint8) if cache == E4 else t)
+        far.append(f.view(E4) if cache == E4 else f)
+    out, lse = call(dict(c, k=far[0], v=far[1]))
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(lse, wl)
+
+
 def test_out_may_be_the_query(cuda_device):
     for prefix in (100, 8000):
         c = make(cuda_device, 9, 8, 2, 128, 16, prefix, [3 * i for i in range(9)], BF, seed=31)
