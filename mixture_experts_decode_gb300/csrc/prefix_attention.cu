@@ -86,7 +86,7 @@ constexpr PxLayout px_layout(int db, bool e4) {
     L.rows = off;  off += 2 * 2 * 128 * 8;
     L.live = off;  off += px_masks(db, e4) * 16;
     L.back = off;  off += 2 * PX_ROWS * 4;
-    L.bars = off;  off += (2 * px_k_stages(db, e4) + 2 * px_v_stages(db, e4) + 12) * 8;
+    L.bars = off;  off += (2 * px_k_stages(db, e4) + 2 * px_v_stages(db, e4) + 14) * 8;
     L.slot = off;  off += 8;
     L.abort = off; off += 8;
     L.total = off;
@@ -280,7 +280,9 @@ __device__ __forceinline__ uint4 ld_128_l2(const void* p) {
 // so the MMA warp fences before the tensor cores read), k_empty / v_empty
 // (commits), s_full (commit, and an arrival of the MMA warp that carries what it
 // saw of the tile's live keys), p_full (softmax warps, per half), h_done /
-// o_done (commits of PV's halves).  Every wait is bounded; one that gives up
+// o_done (commits of PV's halves), last (a commit behind a stream's last PV: at
+// the end o_done may be one phase or two past the one a warp has seen, and a
+// parity tells neither).  Every wait is bounded; one that gives up
 // raises `abort`, and every role goes to the end.
 // The kernel does not wait for its predecessor, the own keys' kernel, which
 // lets it start after everything before that one has completed; it does so at
@@ -308,6 +310,7 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attention_kernel(const _
     uint64_t* const h_done = s_full + 8;
     uint64_t* const q_full = s_full + 10;
     uint64_t* const drained = s_full + 11;
+    uint64_t* const last = s_full + 12;  // [stream], of one phase
     uint32_t* const live = reinterpret_cast<uint32_t*>(sm + L.live);  // [MASKS][4]
     float* const back = reinterpret_cast<float*>(sm + L.back);        // [rows]
     volatile int* const abort = reinterpret_cast<volatile int*>(sm + L.abort);
@@ -342,6 +345,7 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attention_kernel(const _
             mbar_init(&p_full[2 * i + 1], 4);
             mbar_init(&o_done[i], 1);
             mbar_init(&h_done[i], 1);
+            mbar_init(&last[i], 1);
         }
         mbar_init(q_full, PX_SOFT * 32);
         mbar_init(drained, 1);
@@ -459,6 +463,7 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attention_kernel(const _
                 mma_commit(lead, h ? &o_done[s] : &h_done[s]);
             }
             if (!ok) break;
+            if (j + NS >= jobs) mma_commit(lead, &last[s]);
             if (MT == 1 || (j & 1)) mma_commit(lead, &v_empty[st]);
             if (j + 2 < jobs) {  // into the buffer that PV(j) reads: not before it is done
                 const int c = NS == 2 ? j >> 1 : j;
@@ -531,8 +536,8 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attention_kernel(const _
                         l2.x *= f, l2.y *= f;
                         if (h || c > 0) {
                             // (phase by phase: a wait for one that comes after the next would
-                            // pass at once.  S(c) was issued when PV(c - 2), with two streams
-                            // PV(c - 1), was done)
+                            // pass at once.  S(c) was issued when PV(c - 2) of its stream, or
+                            // a later one, was done)
                             if (c > 0) ok = ok && __all_sync(FULL_MASK, mbar_wait_abort(&o_done[s], (c - 1) & 1, abort));
                             if (h) ok = ok && __all_sync(FULL_MASK, mbar_wait_abort(&h_done[s], c & 1, abort));
                             fence_after();
@@ -574,8 +579,7 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attention_kernel(const _
             }
             const float l = l2.x + l2.y;
             // the piece: (m, l) and O of this row, O only where some job ran
-            if (NS == 1 && ok && c > 1) ok = __all_sync(FULL_MASK, mbar_wait_abort(&o_done[s], (c - 2) & 1, abort));
-            if (ok && c > 0) ok = __all_sync(FULL_MASK, mbar_wait_abort(&o_done[s], (c - 1) & 1, abort));
+            if (ok && c > 0) ok = __all_sync(FULL_MASK, mbar_wait_abort(&last[s], 0, abort));
             const int row = row0 + r;
             const int piece = MT == 1 && NS == 2 ? 2 * split + s : split;
             const int64_t at = ((int64_t)kvh * a.pieces + piece) * R + row;

@@ -119,6 +119,20 @@ def test_many_rows_of_wide_heads(cuda_device, D, cache):
     check(make(cuda_device, 33, 16, 1, D, 32, prefix, [i % 9 for i in range(33)], BF, cache, seed=D), what=f"D={D}")
 
 
+@pytest.mark.parametrize("D,prefix,dtype,cache", [(64, 16000, HF, HF), (64, 16001, BF, E4), (128, 9000, BF, BF), (128, 9000, BF, E4),
+                                                  (256, 4000, HF, HF), (256, 4000, BF, E4)])
+@pytest.mark.parametrize("G", [1, 4, 6])
+def test_many_tiles_a_block(cuda_device, D, prefix, dtype, cache, G):
+    """A dozen key tiles and more for each block, and calls behind one another: the same bits every time."""
+    c = make(cuda_device, 50, 16 * G, 16, D, 32, prefix, [(i * 7) % 60 for i in range(50)], dtype, cache, seed=D + G)
+    want, wl = check(c, what=f"D={D}")
+    ws = moe.shared_prefix_workspace(50, 16 * G, 16, D)
+    outs = [call(c, ws=ws) for _ in range(20)]
+    torch.cuda.synchronize()
+    assert moe.device_error(cuda_device) == 0
+    assert all(torch.equal(o, want) and torch.equal(s, wl) for o, s in outs)
+
+
 @pytest.mark.parametrize("page", [1, 3, 8, 13, 100, 256])
 def test_page_sizes(cuda_device, page):
     B = enough(2, 128, 999, BF)
