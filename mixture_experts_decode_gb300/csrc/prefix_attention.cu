@@ -31,7 +31,7 @@
 // half of the time.  Measured, whole calls: 64 sequences over 65536 tokens, 64 /
 // 8 heads of 128, E4M3 161 us (857 TFLOP/s; one launch of the paged kernel 1010);
 // 32 over 8192, 32 / 4 of 128, BF16, chats of up to 1500 tokens 29.5 us (45); 300
-// over 9600, 16 / 2 of 64, FP16 48.5 us (142).
+// over 9600, 16 / 2 of 64, FP16 48.7 us (142).
 #include <algorithm>
 #include <type_traits>
 
