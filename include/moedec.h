@@ -556,6 +556,10 @@ int moe_matvec4(const void* x, int64_t x_stride, int T, int K, int dtype, const 
  *   sequence's row must be the shared pages too: which of the two is read for
  *   them is left open.  shared_len need not end with a page.
  *   What infinities, NaN, and pages outside the cache give is said there.
+ *   Weights are held as two 16-bit values here too.  With an FP16 or E4M3 cache
+ *   those of the prefix are kept down to 2^-31 of the largest among the keys that
+ *   one block reads (moe_paged_attention: 2^-38); smaller ones count in the sum
+ *   of the weights alone.
  * Arguments
  *   as in moe_paged_attention; shared_pages int32 [n_shared], shares uint8 [B]
  *   or NULL.  workspace >= moe_shared_prefix_workspace_bytes for this B (or

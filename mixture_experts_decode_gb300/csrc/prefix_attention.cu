@@ -21,15 +21,20 @@
 //
 // Rounding choices: scores, softmax and sums are FP32.  P is given to the
 // second product as hi + lo, two 16-bit values, as in attention.cu: one
-// rounding would cost as much as the output's own.  Where the output is BF16
-// and the operands are FP16 (an E4M3 cache) hi alone is within 2^-11, an eighth
-// of the output's rounding, and lo is left out.  A BF16 query against E4M3 keys
-// goes to FP16 by a power of two per row, as there.
+// rounding would cost as much as the output's own, and shows where values
+// cancel (a BF16 output over an E4M3 cache with hi alone, FP16, differed from
+// the plain form's by a relative 9e-4 in place of 1e-4; 64 x 65536 tokens then
+// took 161 us in place of 199).  FP16 operands hold 2^7 p, with room for a
+// reference that is 2^8 too low, so that weights below 2^-31 of the largest of a
+// block's run are lost; attention.cu keeps them to 2^-38, but there the
+// reference moves at every 2 that it is passed by, which is a round trip
+// through tensor memory here (64 x 65536: 235 us).  A BF16 query against E4M3
+// keys goes to FP16 by a power of two per row, as there.
 //
 // Bound: HBM for few rows (the prefix once); for many the chain score product,
 // softmax, value product, score product of a stream, with the tensor pipe active
 // half of the time.  Measured, whole calls: 64 sequences over 65536 tokens, 64 /
-// 8 heads of 128, E4M3 161 us (857 TFLOP/s; one launch of the paged kernel 1010);
+// 8 heads of 128, E4M3 199 us (691 TFLOP/s; one launch of the paged kernel 1010);
 // 32 over 8192, 32 / 4 of 128, BF16, chats of up to 1500 tokens 29.5 us (45); 300
 // over 9600, 16 / 2 of 64, FP16 48.7 us (142).
 #include <algorithm>
@@ -60,8 +65,8 @@ constexpr int px_half(int db) { return db * px_keys(db) * 128; }  // bytes of a 
 // widened K tile is wanted again only when the softmax between two uses is over,
 // so one stage does where room is short; V's next tile is wanted as soon as the
 // last is let go, so it has two, and one of codes, which the whole time of a
-// tile is there to fill (64 x 65536 tokens: 166 us; with one of V and two of its
-// codes 182).
+// tile is there to fill (64 x 65536 tokens, when a weight was one 16-bit value:
+// 166 us; with one of V and two of its codes 182).
 constexpr int px_k_stages(int db, bool e4) { return db == 1 ? (e4 ? 2 : 4) : (e4 ? 1 : 2); }
 constexpr int px_v_stages(int db, bool e4) { return db == 1 && !e4 ? 4 : 2; }
 constexpr int px_k_codes(int db, bool e4) { return !e4 ? 0 : db == 1 ? 3 : 2; }
@@ -293,7 +298,6 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attention_kernel(const _
     constexpr int NS = px_streams(DB), KT = px_keys(DB), HALF = px_half(DB), MASKS = px_masks(DB, E4);
     constexpr int KS = px_k_stages(DB, E4), VS = px_v_stages(DB, E4);
     constexpr bool BF = KV == KV_BF16;          // operand type of the products
-    constexpr bool LO = !(E4 && QBF);  // P as hi + lo
     constexpr float P_SHIFT = BF ? 0.f : 7.f;
     constexpr float SLACK = 8.f;  // (FP16 holds up to 2^15)
     constexpr PxLayout L = px_layout(DB, E4);
@@ -458,7 +462,7 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attention_kernel(const _
                 for (int kk = h * (KT / 32); kk < (h + 1) * (KT / 32); ++kk) {
                     const uint32_t pa = p + (kk >> 1) * 32 + (kk & 1) * 8;
                     mma_ts(lead, o, pa, v + kk * (2048 >> 4), id_o, kk > 0 ? 1u : more);
-                    if (LO) mma_ts(lead, o, pa + 16, v + kk * (2048 >> 4), id_o, 1u);
+                    mma_ts(lead, o, pa + 16, v + kk * (2048 >> 4), id_o, 1u);
                 }
                 mma_commit(lead, h ? &o_done[s] : &h_done[s]);
             }
@@ -554,22 +558,17 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attention_kernel(const _
                     const float2 sl2 = make_float2(sl, sl), mu2 = make_float2(-mu, -mu);
 #pragma unroll
                     for (int i = 0; i < HC; ++i) {
-                        uint32_t w[LO ? 32 : 16];
+                        uint32_t w[32];  // hi, then lo
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
                             float2 p = __ffma2_rn(make_float2(__uint_as_float(x[i][2 * e]), __uint_as_float(x[i][2 * e + 1])), sl2, mu2);
                             p = make_float2(exp2_fast(p.x), exp2_fast(p.y));
                             l2 = __fadd2_rn(l2, p);
                             w[e] = pack2<BF>(p.x, p.y);
-                            if constexpr (LO) {
-                                const float2 r = rest2<BF>(p, w[e]);
-                                w[16 + e] = pack2<BF>(r.x, r.y);
-                            }
+                            const float2 r = rest2<BF>(p, w[e]);
+                            w[16 + e] = pack2<BF>(r.x, r.y);
                         }
-                        if constexpr (LO)
-                            tm_st32(h_at + i * 32, w);
-                        else
-                            tm_st16(h_at + i * 32, w);
+                        tm_st32(h_at + i * 32, w);
                     }
                     wait_st();
                     fence_before();
@@ -1024,7 +1023,7 @@ cudaError_t launch_shared_prefix(PrefixArgs a, const AttnArgs& own, int dtype, i
         e = dtype == MOE_BF16 ? launch_px_kv<KV_BF16, true>(a, di, grid, st) : launch_px_kv<KV_F16, false>(a, di, grid, st);
     if (e != cudaSuccess) return e;
     // (threads beyond what is resident at once would take another round: without
-    // that limit 32 x 8192 tokens 31.3 us in place of 29.4, 64 x 65536 166 for 161)
+    // that limit 32 x 8192 tokens take 31.3 us in place of 29.4, 64 x 65536 five more)
     const int np = a.B * a.G <= PX_ROWS ? a.pieces : a.splits, vecs = a.D / 4;
     const int64_t resident = (int64_t)di.sm_count * PJ_BLOCKS * PJ_THREADS;
     a.join_groups = 1;

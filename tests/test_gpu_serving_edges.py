@@ -1,0 +1,68 @@
+"""Edges of the serving step's operators: weights that cancel or lie far below the largest, NaN queries, groups whose keys
+cancel, rows on the border of nothing, state updated in place call after call, slots that change hands between two steps."""
+import math
+
+import pytest
+import torch
+
+import mixture_experts_decode_gb300 as moe
+import _block_refs as refs
+from test_gpu_shared_prefix import BF, E4, HF, call, enough, make
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def no_device_error(cuda_device):
+    yield
+    assert moe.device_error(cuda_device) == 0
+
+
+def two_kinds(c, every, k_one, k_other, v_one, v_other):
+    """Every `every`-th key of the prefix is of one kind, the rest of the other: dim 0 of the keys, all dims of the values."""
+    page = c["k"].shape[1]
+    for t, one, other in ((c["k"], k_one, k_other), (c["v"], v_one, v_other)):
+        x = torch.zeros(c["prefix"], *t.shape[2:], device=t.device)
+        dims = slice(0, 1) if t is c["k"] else slice(None)
+        x[..., dims] = other
+        x[::every, :, dims] = one
+        for i, pg in enumerate(c["shared"].tolist()):
+            t[pg] = x[i * page:(i + 1) * page].to(t.dtype)
+    c["q"].zero_()
+    c["ks"] = c["vs"] = 1.0
+
+
+@pytest.mark.parametrize("dtype,cache", [(BF, BF), (HF, HF), (HF, E4), (BF, E4)])
+def test_weights_that_cancel(cuda_device, dtype, cache):
+    """Half of the keys have value 1 and weight 1, half -1 and a weight a little below it: the output is the difference of
+    two sums, so a weight's rounding shows beside it.  Bound: the output's rounding, 2^-17 + 2^-20 of the weights as in
+    _block_refs.attention, and half a step of FP32 for each of the keys in a sum."""
+    Hkv, D, prefix = 8, 128, 512
+    B = enough(Hkv, D, prefix, cache)
+    c = make(cuda_device, B, Hkv, Hkv, D, 16, prefix, 0, dtype, cache, seed=41)
+    two_kinds(c, 2, 1.0, 0.875, 1.0, -1.0)
+    c["q"][..., 0] = 1 + torch.arange(B * Hkv, device=cuda_device).view(B, Hkv) / (B * Hkv)
+    out, _ = call(c, scale=2.0 ** -8)
+    ro, _, _, _ = refs.attention(c["q"], c["k"], c["v"], c["table"], c["lens"], 2.0 ** -8)
+    bound = refs.half_step(dtype) * ro.abs() + 2.0 ** -17 + 2.0 ** -20 + 2 * 512 * 2.0 ** -24
+    err = ((out.double() - ro).abs() - bound).max()
+    assert err <= 0, f"beyond the bound by {float(err):.3g}"
+
+
+@pytest.mark.parametrize("dtype,cache,v_tail", [(BF, BF, 6e4), (HF, HF, 6e4), (HF, E4, 448.0), (BF, E4, 448.0)])
+@pytest.mark.parametrize("bits", [20, 28, 30])
+def test_weights_far_below_the_largest(cuda_device, dtype, cache, v_tail, bits):
+    """Keys of value 0 that take nearly all of the weight, 63 of 2^-bits behind each: the output is what is kept of those.
+    A weight is held to 2^-38 of the largest (paged_attention's promise; half a step of 2^-24 beside 2^14 times a weight
+    that the reference may halve), and FP16 outputs to 2^-25."""
+    Hkv, D, prefix = 8, 128, 2048
+    B = enough(Hkv, D, prefix, cache)
+    c = make(cuda_device, B, Hkv, Hkv, D, 16, prefix, 0, dtype, cache, seed=43)
+    two_kinds(c, 64, 8.0, 0.0, 0.0, v_tail)
+    c["q"][..., 0] = 1.0
+    scale = bits * math.log(2.0) / 8
+    out, _ = call(c, scale=scale)
+    ro, _, ob, _ = refs.attention(c["q"], c["k"], c["v"], c["table"], c["lens"], scale)
+    bound = ob + 2.0 ** -31 * v_tail * 63
+    err = ((out.double() - ro).abs() - bound).max()
+    assert err <= 0, f"beyond the bound by {float(err):.3g} of {float(ro.abs().max()):.3g}"
