@@ -828,8 +828,9 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attention_kernel(const _
 // Every output from its pieces: the sequence's own and, where it shares the
 // prefix, the prefix's.  A thread takes four dims of a row, and a.join_groups
 // threads with the same dims divide the row's pieces between them, four or so
-// each with all loads in flight; the groups are added in order.  A piece without
-// a score above -inf is left out (its sums may hold anything).
+// each with all loads in flight; the groups are added in order.  A piece whose
+// weights are all 0 is left out (its sums may hold anything); one whose scores
+// are all NaN has no maximum either, but a sum of NaN, which has to show.
 constexpr int PJ_THREADS = 256, PJ_FLIGHT = 4, PJ_BLOCKS = 5;  // (blocks of an SM)
 template <bool QBF>
 __global__ void __launch_bounds__(PJ_THREADS, PJ_BLOCKS) prefix_join_kernel(const __grid_constant__ PrefixArgs a) {
@@ -851,7 +852,7 @@ __global__ void __launch_bounds__(PJ_THREADS, PJ_BLOCKS) prefix_join_kernel(cons
         sum.x *= old, sum.y *= old, sum.z *= old, sum.w *= old;
     };
     auto add = [&](float2 ml, const float4& v) {
-        if (ml.x == -INFINITY) return;
+        if (ml.x == -INFINITY && ml.y == 0.f) return;
         const float f = exp2_fast(ml.x - finite_or_zero(m));
         l += f * ml.y;
         sum.x += f * v.x, sum.y += f * v.y, sum.z += f * v.z, sum.w += f * v.w;

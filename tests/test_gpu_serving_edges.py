@@ -66,3 +66,21 @@ def test_weights_far_below_the_largest(cuda_device, dtype, cache, v_tail, bits):
     bound = ob + 2.0 ** -31 * v_tail * 63
     err = ((out.double() - ro).abs() - bound).max()
     assert err <= 0, f"beyond the bound by {float(err):.3g} of {float(ro.abs().max()):.3g}"
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("dtype,cache", [(BF, BF), (HF, HF), (BF, E4)])
+@pytest.mark.parametrize("prefix", [256, 8192])
+def test_queries_that_are_not_finite(cuda_device, prefix, dtype, cache, bad):
+    """One value of a head: NaN where paged_attention has it (with and without the prefix), the rest as it was."""
+    c = make(cuda_device, 17, 8, 2, 128, 16, prefix, [10 + i for i in range(17)], dtype, cache, seed=47, others=(2,))
+    want, wl = call(c)
+    for b, h in ((0, 0), (2, 5), (16, 7)):
+        c["q"][b, h, 9] = bad
+    out, lse = call(c)
+    po, pl = moe.paged_attention(c["q"], c["k"], c["v"], c["table"], c["lens"], k_scale=c["ks"], v_scale=c["vs"], return_lse=True)
+    torch.cuda.synchronize()
+    assert torch.equal(torch.isnan(out), torch.isnan(po)) and torch.equal(torch.isnan(lse), torch.isnan(pl))
+    hit = torch.zeros_like(wl, dtype=torch.bool)
+    hit[0, 0] = hit[2, 5] = hit[16, 7] = True
+    assert bool(torch.isnan(out[hit]).all()) and torch.equal(out[~hit], want[~hit]) and torch.equal(lse[~hit], wl[~hit])
