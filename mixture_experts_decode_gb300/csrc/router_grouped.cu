@@ -489,7 +489,8 @@ __device__ __noinline__ void route_row_again(const RouterGroupedArgs& a, int64_t
 // rows at once; a lane holds NE consecutive logits, as sorted lists of eight.
 // Logits come by asynchronous copies, the next rows' while these are routed.
 // Rows in which two keys or groups that may matter lie closer than FP32 tells
-// apart, or with fewer than k experts, are left to route_row.
+// apart, with fewer than k experts or with a sum of scores that is not finite
+// are left to route_row.
 // (65536 rows of 256, 8 groups: 55 us; a warp a row took 107, of 1077 instructions.)
 constexpr int RO_WARPS = 4;
 constexpr int RO_LIST(int ne) { return ne + 4; }  // words of a lane's lists, an odd number of 16-byte columns
@@ -613,7 +614,8 @@ __global__ void __launch_bounds__(RO_WARPS * 32, NE == 32 ? 4 : 6) router_octets
         if (narrow && (!same_bias || !top2))
 #pragma unroll
             for (int i = 0; i < NE; ++i) see(x[i]);
-        bool again = false;  // this row is left to route_row
+        // this row is left to route_row; a sum of NaN (a logit of +inf) leaves no key that could be compared
+        bool again = !(total < INFINITY);
         if (narrow) {
             for (int o = 1; o < q; o *= 2) {
                 const float b2 = __shfl_xor_sync(FULL_MASK, best, o), s2 = __shfl_xor_sync(FULL_MASK, second, o);
@@ -635,7 +637,7 @@ __global__ void __launch_bounds__(RO_WARPS * 32, NE == 32 ? 4 : 6) router_octets
                     last = fminf(last, __shfl_xor_sync(FULL_MASK, last, o));
                     next = fmaxf(next, __shfl_xor_sync(FULL_MASK, next, o));
                 }
-                again = last - next <= 4.f * tau_s + 0x1p-21f * fmaxf(fabsf(last), fabsf(next));
+                again |= last - next <= 4.f * tau_s + 0x1p-21f * fmaxf(fabsf(last), fabsf(next));
             }
             if (rank >= a.top_groups)
 #pragma unroll
@@ -672,7 +674,7 @@ __global__ void __launch_bounds__(RO_WARPS * 32, NE == 32 ? 4 : 6) router_octets
 #pragma unroll
             for (int o = 1; o < 8; o *= 2) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, o));
             const uint32_t has = __ballot_sync(FULL_MASK, mine == top) >> lane0 & 0xffu;
-            const int owner = __ffs(has) - 1;
+            const int owner = __ffs(has | 0x80u) - 1;  // (none has a maximum of NaN: any lane, the row is done again)
             int l = NS - 1;
 #pragma unroll
             for (int i = NS - 2; i >= 0; --i)
@@ -690,7 +692,7 @@ __global__ void __launch_bounds__(RO_WARPS * 32, NE == 32 ? 4 : 6) router_octets
             if (j == k) beyond = top;
         }
         const bool mine = sub < k;
-        again |= mine && pick_key == -INFINITY;  // fewer than k experts
+        again |= mine && !(pick_key > -INFINITY);  // fewer than k experts
         // which of the list's eight experts: equal keys come in their order
         int skip = 0;
         {

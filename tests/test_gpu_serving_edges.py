@@ -7,6 +7,7 @@ import torch
 
 import mixture_experts_decode_gb300 as moe
 import _block_refs as refs
+from test_gpu_router_grouped import MANY, randn
 from test_gpu_shared_prefix import BF, E4, HF, call, enough, make
 
 pytestmark = pytest.mark.gpu
@@ -84,3 +85,23 @@ def test_queries_that_are_not_finite(cuda_device, prefix, dtype, cache, bad):
     hit = torch.zeros_like(wl, dtype=torch.bool)
     hit[0, 0] = hit[2, 5] = hit[16, 7] = True
     assert bool(torch.isnan(out[hit]).all()) and torch.equal(out[~hit], want[~hit]) and torch.equal(lse[~hit], wl[~hit])
+
+
+@pytest.mark.parametrize("E,groups,top", [(64, 1, 1), (64, 8, 3), (128, 2, 1), (256, 8, 8), (256, 8, 4)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_infinite_logits_of_many_rows(cuda_device, E, groups, top, score):
+    """As for few rows, whatever was in the outputs: with softmax and a bias such a row has no score, so no expert."""
+    x, bias = randn(MANY, E, seed=52), randn(E, seed=E, std=0.1)
+    x[::9, 3], x[1::50, E - 1] = math.inf, math.inf
+    x, k = x.to(cuda_device), 6
+    ids = torch.full((MANY, k), -12345, dtype=torch.int32, device=cuda_device)
+    w = torch.full((MANY, k), -7.0, device=cuda_device)
+    rest = (bias.to(cuda_device), score, groups, top)
+    moe.router_grouped_topk(x, k, *rest, topk_ids=ids, topk_w=w)
+    few = [moe.router_grouped_topk(part, k, *rest) for part in x.split(1000)]
+    torch.cuda.synchronize()
+    assert torch.equal(ids, torch.cat([f[0] for f in few]))
+    torch.testing.assert_close(w, torch.cat([f[1] for f in few]), rtol=2.0 ** -19, atol=0.0, equal_nan=True)
+    none = torch.isinf(x).any(1) & (score == "softmax")
+    assert bool((ids[none] == -1).all()) and bool((w[none] == 0).all()) and bool((ids[~none] >= 0).all())
+    assert moe.device_error(cuda_device) == (0x4 if score == "softmax" else 0)
