@@ -25,7 +25,9 @@ __device__ __forceinline__ int warp_index() { return __shfl_sync(FULL_MASK, (int
 // The kernels of the decode block are launched as programmatic dependents:
 // their blocks may be set up while the kernel before them in the stream ends,
 // and each begins with after_previous(), which waits until that kernel has
-// completed and its writes are visible.  A step is a chain of kernels of a few
+// completed and its writes are visible.  (Two begin earlier, behind a kernel
+// that has itself waited and lets them: the shared prefix's and the page plan's
+// second launch.  They read past L1 and wait at their end.)  A step is a chain of kernels of a few
 // microseconds; this takes about 2 us off the gap between two calls (attention
 // of 777 keys in a loop of calls 12.4 -> 9.9 us, 4-bit 16 x 4096 -> 7169 14.4
 // -> 12.3 us).  A block of such a kernel may be resident while its inputs are

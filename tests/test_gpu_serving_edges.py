@@ -7,6 +7,7 @@ import torch
 
 import mixture_experts_decode_gb300 as moe
 import _block_refs as refs
+import _serving_refs as srefs
 from test_gpu_router_grouped import MANY, randn
 from test_gpu_shared_prefix import BF, E4, HF, call, enough, make
 
@@ -105,3 +106,45 @@ def test_infinite_logits_of_many_rows(cuda_device, E, groups, top, score):
     none = torch.isinf(x).any(1) & (score == "softmax")
     assert bool((ids[none] == -1).all()) and bool((w[none] == 0).all()) and bool((ids[~none] >= 0).all())
     assert moe.device_error(cuda_device) == (0x4 if score == "softmax" else 0)
+
+
+def test_in_place_plans_and_releases_of_several_blocks_one_after_the_other(cuda_device):
+    """Each call reads what the one before has written; prompts and ends of some ten thousand tokens a call, eagerly and
+    from a graph."""
+    dev, page, most, B = cuda_device, 4, 1000, 48
+    g = torch.Generator().manual_seed(57)
+    pool = 12000
+    free = torch.randperm(pool, generator=g).tolist()
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=dev)  # noqa: E731
+    for graphs in (False, True):
+        lens, height, stack = i32([0] * B), i32([pool]), i32(free)
+        tab = torch.full((B, most), -1, dtype=torch.int32, device=dev)
+        news = [torch.randint(0, 200, (B,), generator=g).tolist() for _ in range(12)]
+        ends = [(torch.rand(B, generator=g) < 0.3).tolist() for _ in range(12)]
+        d_new, d_end = [i32(n) for n in news], [torch.tensor(e, device=dev) for e in ends]
+
+        def steps():
+            got = []
+            for n, e in zip(d_new, d_end):
+                moe.release_pages(tab, lens, e, stack, height, page, seq_lens_out=lens, n_free_out=height)
+                got.append(moe.plan_pages(lens, n, tab, stack, height, page, 10000, seq_lens=lens, n_free_out=height))
+                got.append(moe.plan_pages(lens, n, tab, stack, height, page, 10000, seq_lens=lens, n_free_out=height))
+            return got
+
+        if graphs:
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                plans = steps()
+            graph.replay()
+        else:
+            plans = steps()
+        torch.cuda.synchronize()
+        h_lens, h_tab, h_stack, h_free, refused = [0] * B, [[-1] * most for _ in range(B)], list(free), pool, False
+        for i, (n, e) in enumerate(zip(news, ends)):
+            h_stack, h_free, h_lens = srefs.release(h_tab, h_lens, e, h_stack, h_free, page)
+            for p in plans[2 * i:2 * i + 2]:
+                pos, slots, seqs, starts, h_lens, h_free, h_tab, r = srefs.plan(h_lens, n, h_tab, h_stack, h_free, page, 10000)
+                refused |= r
+                assert p.starts.tolist() == starts and p.positions.tolist() == pos and p.slots.tolist() == slots, i
+        assert lens.tolist() == h_lens and height.tolist() == [h_free] and tab.tolist() == h_tab and stack.tolist() == h_stack
+        assert not refused
