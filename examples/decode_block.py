@@ -121,7 +121,8 @@ class SharedBlock(DecodeBlock):
     """The block for sequences that begin with the same `shared` tokens (whole pages), over a pool of pages.
 
     begin() starts a sequence behind the prefix, or without it; end() marks those whose pages go back to the pool at
-    the next step.  The prefix's keys and values are the pages self.shared of the caches."""
+    the next step.  Both take effect there, the ends first, so that a slot may end and begin again between two steps.
+    The prefix's keys and values are the pages self.shared of the caches."""
 
     def __init__(self, cfg: inputs.LayerConfig, Hq: int, Hkv: int, D: int, batch: int, capacity: int, shared: int,
                  page: int = 64, device="cuda", seed: int = 0, group: int = 128, groups: int = 1, top_groups: int = 1):
@@ -136,22 +137,34 @@ class SharedBlock(DecodeBlock):
         self.new = torch.zeros(batch, dtype=torch.int32, device=device)   # a token a step of those that run
         self.shares = torch.ones(batch, dtype=torch.bool, device=device)
         self.ended = torch.zeros(batch, dtype=torch.bool, device=device)
+        # what begins at the next step: its length, -1 for none
+        self.next_lens = torch.full((batch,), -1, dtype=torch.int32, device=device)
+        self.next_shares = torch.ones(batch, dtype=torch.bool, device=device)
+        self.runs = [False] * batch
         self.workspace = moe.shared_prefix_workspace(batch, Hq, Hkv, D, device)
         self.groups, self.top_groups = groups, top_groups
         self.bias = torch.zeros(cfg.E, device=device)
 
     def begin(self, b: int, shares: bool = True):
-        self.shares[b], self.new[b] = shares, 1
-        self.lens[b] = self.shared_len if shares else 0
+        if self.runs[b]:
+            raise ValueError(f"sequence {b} runs: end it first")
+        self.runs[b] = True
+        self.next_shares[b], self.new[b] = shares, 1
+        self.next_lens[b] = self.shared_len if shares else 0
 
     def end(self, b: int):
+        self.runs[b] = False
         self.ended[b] = True
-        self.new[b] = 0
+        self.next_lens[b], self.new[b] = -1, 0
 
     def place(self, B: int):
         moe.release_pages(self.table, self.lens, self.ended, self.free, self.n_free, self.page, shared=self.shared.numel(),
                           shares=self.shares, seq_lens_out=self.lens, n_free_out=self.n_free)
         self.ended.zero_()
+        begins = self.next_lens >= 0
+        self.lens.copy_(torch.where(begins, self.next_lens, self.lens))
+        self.shares.copy_(torch.where(begins, self.next_shares, self.shares))
+        self.next_lens.fill_(-1)
         # one row a sequence: those that do not run bring no token, and their rows behind the last token are padding
         p = moe.plan_pages(self.lens, self.new, self.table, self.free, self.n_free, self.page, B, shared_pages=self.shared,
                            shares=self.shares, seq_lens=self.lens, n_free_out=self.n_free)

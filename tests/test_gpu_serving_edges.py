@@ -1,15 +1,21 @@
 """Edges of the serving step's operators: weights that cancel or lie far below the largest, NaN queries, groups whose keys
 cancel, rows on the border of nothing, state updated in place call after call, slots that change hands between two steps."""
 import math
+import os
+import sys
 
 import pytest
 import torch
 
 import mixture_experts_decode_gb300 as moe
+from mixture_experts_decode_gb300 import inputs
 import _block_refs as refs
 import _serving_refs as srefs
 from test_gpu_router_grouped import MANY, randn
 from test_gpu_shared_prefix import BF, E4, HF, call, enough, make
+
+sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+import decode_block  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -148,3 +154,40 @@ def test_in_place_plans_and_releases_of_several_blocks_one_after_the_other(cuda_
                 assert p.starts.tolist() == starts and p.positions.tolist() == pos and p.slots.tolist() == slots, i
         assert lens.tolist() == h_lens and height.tolist() == [h_free] and tab.tolist() == h_tab and stack.tolist() == h_stack
         assert not refused
+
+
+def test_a_slot_ends_and_begins_again_before_a_step(cuda_device):
+    """Between two steps a request ends and another takes its slot (behind the prefix, without it, and given up again):
+    the old one's pages go back, the new one begins with its prefix."""
+    b = decode_block.SharedBlock(inputs.TINY, 4, 2, 64, batch=3, capacity=112, shared=48, page=16, device=cuda_device, group=64)
+    pool = b.k_cache.shape[0] - 3
+    resid = torch.randn(3, inputs.TINY.d, device=cuda_device)
+
+    def pages():
+        used = []
+        for i, n in enumerate(b.lens.tolist()):
+            used += b.table[i, 3 if bool(b.shares[i]) else 0:-(-n // 16)].tolist()
+        left = b.free[:int(b.n_free)].tolist()
+        assert len(set(used + left)) == len(used) + len(left) == pool, "a page lost or held twice"
+
+    for i in range(3):
+        b.begin(i, shares=i != 1)
+    for _ in range(20):
+        b.step(resid)
+    assert b.lens.tolist() == [68, 20, 68]
+    pages()
+    b.end(0)
+    b.begin(0, shares=False)
+    b.end(1)
+    b.begin(1, shares=True)
+    b.end(2)
+    b.begin(2)
+    b.end(2)
+    b.step(resid)
+    assert b.lens.tolist() == [1, 49, 0]
+    pages()
+    b.step(resid)
+    assert b.lens.tolist() == [2, 50, 0]
+    pages()
+    with pytest.raises(ValueError, match="runs"):
+        b.begin(0)
