@@ -267,7 +267,8 @@ __device__ __forceinline__ void route_row(const RouterGroupedArgs& a, int64_t t,
             const float last = unordered(~warp_max(in ? ~ordered(worth) : 0u));
             const float next = unordered(warp_max(lane < a.groups && !in ? ordered(worth) : 0u));
             const float tol = 4.f * tau_s + 0x1p-21f * fmaxf(fabsf(last), fabsf(next));
-            if (last - next <= tol) {
+            const float gap = last - next;  // (infinite: what is out, or in, is so whatever its neighbours)
+            if (gap < INFINITY && gap <= tol) {
                 // the groups about it in 64 bits, the others are clearly in or out
                 row64();
                 __syncwarp();
@@ -364,7 +365,7 @@ __device__ __forceinline__ void route_row(const RouterGroupedArgs& a, int64_t t,
         const float f0 = __shfl_up_sync(FULL_MASK, f, 1), x0 = __shfl_up_sync(FULL_MASK, px, 1),
                     b0 = __shfl_up_sync(FULL_MASK, pb, 1);
         const float tau = 2.f * tau_s + 0x1p-22f * fmaxf(fabsf(f), fabsf(f0));
-        const bool close = lane > 0 && lane < n && f0 - f <= tau;
+        const bool close = lane > 0 && lane < n && f0 - f < INFINITY && f0 - f <= tau;
         bool look = __any_sync(FULL_MASK, close && !(px == x0 && pb == b0));
         const float fk = __shfl_sync(FULL_MASK, f, min(k, n) - 1);
         const float edge = fk - (2.f * tau_s + 0x1p-22f * fabsf(fk));  // what may belong before the k-th
@@ -637,7 +638,8 @@ __global__ void __launch_bounds__(RO_WARPS * 32, NE == 32 ? 4 : 6) router_octets
                     last = fminf(last, __shfl_xor_sync(FULL_MASK, last, o));
                     next = fmaxf(next, __shfl_xor_sync(FULL_MASK, next, o));
                 }
-                again |= last - next <= 4.f * tau_s + 0x1p-21f * fmaxf(fabsf(last), fabsf(next));
+                const float gap = last - next;  // (infinite: what is out, or in, is so whatever its neighbours)
+                again |= gap < INFINITY && gap <= 4.f * tau_s + 0x1p-21f * fmaxf(fabsf(last), fabsf(next));
             }
             if (rank >= a.top_groups)
 #pragma unroll
@@ -719,7 +721,8 @@ __global__ void __launch_bounds__(RO_WARPS * 32, NE == 32 ? 4 : 6) router_octets
         if (!same_bias) {
             float after = __shfl_down_sync(FULL_MASK, pick_key, 1, 8);
             if (sub == k - 1) after = beyond;
-            again |= mine && pick_key - after <= 2.f * tau_s + 0x1p-22f * fmaxf(fabsf(pick_key), fabsf(after));
+            const float gap = pick_key - after;  // (infinite: no key is left behind this one)
+            again |= mine && gap < INFINITY && gap <= 2.f * tau_s + 0x1p-22f * fmaxf(fabsf(pick_key), fabsf(after));
         }
         // weights, as in route_row (all lanes take part in the exchanges)
         {

@@ -114,6 +114,33 @@ def test_infinite_logits_of_many_rows(cuda_device, E, groups, top, score):
     assert moe.device_error(cuda_device) == (0x4 if score == "softmax" else 0)
 
 
+def best_us(f):
+    for _ in range(3):
+        f()
+    best = math.inf
+    for _ in range(10):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        torch.cuda.synchronize()
+        a.record()
+        f()
+        b.record()
+        torch.cuda.synchronize()
+        best = min(best, a.elapsed_time(b) * 1e3)
+    return best
+
+
+def test_rows_with_nothing_beyond_the_border_are_not_looked_at_again(cuda_device):
+    """Every key of the groups is chosen, or the groups left out are wholly masked: nothing lies close to what is left out."""
+    x, bias = randn(65536, 64, seed=53).to(cuda_device), randn(64, std=0.1).to(cuda_device)
+    usual = best_us(lambda: moe.router_grouped_topk(x, 7, bias, "sigmoid", 8, 1))
+    every = best_us(lambda: moe.router_grouped_topk(x, 8, bias, "sigmoid", 8, 1))
+    masked = bias.clone()
+    masked[32:] = -math.inf
+    none = best_us(lambda: moe.router_grouped_topk(x, 7, masked, "sigmoid", 8, 4))
+    print(f"usual {usual:.1f} every {every:.1f} masked {none:.1f} us")
+    assert every < 1.6 * usual and none < 1.6 * usual
+
+
 def test_in_place_plans_and_releases_of_several_blocks_one_after_the_other(cuda_device):
     """Each call reads what the one before has written; prompts and ends of some ten thousand tokens a call, eagerly and
     from a graph."""
