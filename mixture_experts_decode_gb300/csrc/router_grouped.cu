@@ -129,6 +129,13 @@ __device__ __forceinline__ void load_logits(const void* row, int e0, int E, bool
 // the exponent (s |x - m| is at most 0.37 / total); under 48.
 __device__ __forceinline__ float score_error(bool softmax, float total) { return softmax ? 0x30p-24f / total : 0x5.8p-24f; }
 
+// What a group's worth is off by at most: its keys' scores, and a rounding of
+// each key and of their sum.  The keys may cancel (biases of either sign), so
+// their sizes count and not their sum's.
+__device__ __forceinline__ float worth_error(float worth, float best, float second, float tau_s) {
+    return fabsf(worth) < INFINITY ? 2.f * tau_s + 0x1p-22f * (fabsf(best) + fabsf(second)) : 0.f;
+}
+
 // A score in 64 bits; `m` and `total` are the row's (softmax).
 __device__ __forceinline__ double score64(const RouterGroupedArgs& a, float x, double m, double total) {
     return a.score == MOE_ROUTER_SOFTMAX ? exp((double)x - m) / total : 1.0 / (1.0 + exp(-(double)x));
@@ -263,20 +270,20 @@ __device__ __forceinline__ void route_row(const RouterGroupedArgs& a, int64_t t,
         }
         bool in = lane < a.groups && rank < a.top_groups;
         if (!by_logit) {
-            // the border between the last group in and the first one out
-            const float last = unordered(~warp_max(in ? ~ordered(worth) : 0u));
-            const float next = unordered(warp_max(lane < a.groups && !in ? ordered(worth) : 0u));
-            const float tol = 4.f * tau_s + 0x1p-21f * fmaxf(fabsf(last), fabsf(next));
-            const float gap = last - next;  // (infinite: what is out, or in, is so whatever its neighbours)
-            if (gap < INFINITY && gap <= tol) {
+            // the border between the least that a group in may be worth and the
+            // most that one out may (infinite: whatever its neighbours)
+            const float err = worth_error(worth, best, top2 ? second : 0.f, tau_s);
+            const float last = unordered(~warp_max(in ? ~ordered(worth - err) : 0u));
+            const float next = unordered(warp_max(lane < a.groups && !in ? ordered(worth + err) : 0u));
+            if (last <= next && next > -INFINITY && last < INFINITY) {
                 // the groups about it in 64 bits, the others are clearly in or out
                 row64();
                 __syncwarp();
 #pragma unroll
                 for (int i = 0; i < NV; ++i) sk[e0 + i] = key[i];
                 __syncwarp();
-                double w64 = worth > last + tol ? INFINITY : -INFINITY;
-                const bool near = lane < a.groups && worth >= next - tol && worth <= last + tol;
+                double w64 = worth - err > next ? INFINITY : -INFINITY;
+                const bool near = lane < a.groups && worth - err <= next && worth + err >= last;
                 for (uint32_t todo = __ballot_sync(FULL_MASK, near); todo; todo &= todo - 1u) {
                     const int g = __ffs(todo) - 1;
                     double b64 = -INFINITY, s64 = -INFINITY;
@@ -632,14 +639,14 @@ __global__ void __launch_bounds__(RO_WARPS * 32, NE == 32 ? 4 : 6) router_octets
                 rank += other && (o > worth || (o == worth && g < sub));
             }
             if (!by_logit) {  // the border between the last group in and the first one out
-                float last = rank < a.top_groups ? worth : INFINITY, next = rank < a.top_groups ? -INFINITY : worth;
+                const float err = worth_error(worth, best, top2 ? second : 0.f, tau_s);
+                float last = rank < a.top_groups ? worth - err : INFINITY, next = rank < a.top_groups ? -INFINITY : worth + err;
 #pragma unroll
                 for (int o = 1; o < 8; o *= 2) {
                     last = fminf(last, __shfl_xor_sync(FULL_MASK, last, o));
                     next = fmaxf(next, __shfl_xor_sync(FULL_MASK, next, o));
                 }
-                const float gap = last - next;  // (infinite: what is out, or in, is so whatever its neighbours)
-                again |= gap < INFINITY && gap <= 4.f * tau_s + 0x1p-21f * fmaxf(fabsf(last), fabsf(next));
+                again |= last <= next && next > -INFINITY && last < INFINITY;
             }
             if (rank >= a.top_groups)
 #pragma unroll

@@ -11,7 +11,7 @@ import mixture_experts_decode_gb300 as moe
 from mixture_experts_decode_gb300 import inputs
 import _block_refs as refs
 import _serving_refs as srefs
-from test_gpu_router_grouped import MANY, randn
+from test_gpu_router_grouped import MANY, check as check_router, randn
 from test_gpu_shared_prefix import BF, E4, HF, call, enough, make
 
 sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
@@ -92,6 +92,17 @@ def test_queries_that_are_not_finite(cuda_device, prefix, dtype, cache, bad):
     hit = torch.zeros_like(wl, dtype=torch.bool)
     hit[0, 0] = hit[2, 5] = hit[16, 7] = True
     assert bool(torch.isnan(out[hit]).all()) and torch.equal(out[~hit], want[~hit]) and torch.equal(lse[~hit], wl[~hit])
+
+
+@pytest.mark.parametrize("T", [40, MANY])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_groups_whose_best_keys_cancel(cuda_device, T, score):
+    """Two keys near 1000 and -1000 a group: their sum is small, their FP32 roundings are not."""
+    E, groups = 64, 8
+    bias = torch.full((E,), -2000.0)
+    bias[0::8], bias[5::8] = 1000.0, -1000.0
+    for top in (1, 3):
+        check_router(cuda_device, randn(T, E, seed=51), 6 if top > 1 else 4, bias, score, groups, top, "top2")
 
 
 @pytest.mark.parametrize("E,groups,top", [(64, 1, 1), (64, 8, 3), (128, 2, 1), (256, 8, 8), (256, 8, 4)])
