@@ -124,10 +124,12 @@ __device__ __forceinline__ void load_logits(const void* row, int e0, int E, bool
 // What FP32 scores are off by at most, in units of 2^-24.  Sigmoid, of a value
 // s <= 1: 2 for the quotient, 1 for the sum 1 + e, and s (1 - s) times the
 // relative error of e, 4 of exp2 and 1.5 |x| of its argument: 1 + 0.4; under
-// 5.5.  Softmax, relative to a score of at most 1 / total: 4 of exp2, as much of
-// the sum's terms, 37 of its additions, 2 of the quotient, and 0.37 * 1.5 of
-// the exponent (s |x - m| is at most 0.37 / total); under 48.
-__device__ __forceinline__ float score_error(bool softmax, float total) { return softmax ? 0x30p-24f / total : 0x5.8p-24f; }
+// 5.5.  Softmax, relative to a score of at most 1 / total: 4 of exp2, and 2.23
+// |x - m| of its argument (a difference, a product and the constant's own 0.23;
+// a score times |x - m| is at most 0.37 / total); of the sum 4 of exp2, 2.23
+// times the mean of |x - m| by the scores (at most 4.44 for 1024 experts), 37 of
+// its additions; 2 of the quotient; under 58.
+__device__ __forceinline__ float score_error(bool softmax, float total) { return softmax ? 0x40p-24f / total : 0x5.8p-24f; }
 
 // What a group's worth is off by at most: its keys' scores, and a rounding of
 // each key and of their sum.  The keys may cancel (biases of either sign), so

@@ -1,7 +1,10 @@
 """Rules of the serving step's sources and documents that no run shows (no GPU)."""
 import ast
+import math
 import os
 import re
+
+import numpy as np
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "mixture_experts_decode_gb300", "csrc")
@@ -39,3 +42,25 @@ def test_the_readme_keeps_the_shared_pages():
             assert "shared" in calls["release_pages"], "the prefix's pages would go to the free stack"
             for name in ("release_pages", "plan_pages", "shared_prefix_attention"):
                 assert ("shares" in calls[name]) == ("shares" in calls["plan_pages"]), "the same sequences share in all calls"
+
+
+def test_the_softmax_scores_error_is_a_bound():
+    """In units of 2^-24, relative to the largest possible score 1 / total: exp2 within 2 units in the last place; its argument
+    from a difference and a product (a unit each) by a constant that is itself off; the sum's terms have the same errors, the
+    exponents' weighted by the scores; its additions are a lane's (32 of 1024 experts) and five steps; a reciprocal and a
+    product."""
+    unit, exp2 = 2.0 ** -24, 4.0
+    off = abs(float(np.float32(1.44269504)) / math.log2(math.e) - 1) / unit
+    argument = 2 + off
+    d = np.linspace(0, 40, 400001)
+    score_times = (np.exp(-d) * d).max()                     # of one expert, d below the largest
+    rest = 1023 * np.exp(-d)
+    mean = (rest * d / (1 + rest)).max()                     # sum p |x - m|: largest where all but one are equally far
+    rng = np.random.default_rng(1)
+    for _ in range(200):
+        x = -rng.gamma(rng.uniform(0.1, 8), rng.uniform(0.1, 8), 1024)
+        p = np.exp(x - x.max())
+        assert (p * (x.max() - x)).sum() / p.sum() <= mean
+    bound = exp2 + argument * score_times + exp2 + argument * mean + (32 + 5) + 2
+    held = re.search(r"softmax \? (0x[0-9a-f]+)p-24f / total", source("router_grouped.cu")).group(1)
+    assert bound <= int(held, 16), (bound, held)
