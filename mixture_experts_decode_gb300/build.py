@@ -59,7 +59,7 @@ def _block_commands():
     comp = [cxx, "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
             *[f"-isystem{d}" for d in inc], "-c", os.path.join(CSRC, "binding.cpp")]
     link = [cxx, "-shared", "-L" + os.path.join(root, "lib"), "-L" + PKG, "-Wl,-rpath,$ORIGIN"]
-    libs = ["-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda", "-l:libmoedec.so"]
+    libs = ["-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-l:libmoedec.so"]
     return comp, link, libs, torch.__version__
 
 

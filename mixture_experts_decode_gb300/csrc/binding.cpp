@@ -10,7 +10,6 @@
 // here: dtypes, devices, shapes and strides are checked, outputs allocated
 // and raw pointers handed to the C ABI with the current stream.
 #include <ATen/ATen.h>
-#include <ATen/cuda/EmptyTensor.h>
 #include <Python.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -161,15 +160,9 @@ PyObject* guarded(Py_ssize_t n, Py_ssize_t want, F&& f) {
     return nullptr;
 }
 
-// A new tensor on the device, past the dispatcher (0.5 us of the host's time
-// each, where a step's plan has six).
-Tensor fresh(at::IntArrayRef shape, const at::TensorOptions& opt) {
-    return Tensor(at::detail::empty_cuda(shape, c10::typeMetaToScalarType(opt.dtype()), opt.device(), std::nullopt));
-}
-
 // The caller's output tensor, or a new one.
 Tensor output(PyObject* o, const char* name, at::IntArrayRef shape, const at::TensorOptions& opt) {
-    if (o == Py_None) return fresh(shape, opt);
+    if (o == Py_None) return at::empty(shape, opt);
     const Tensor& t = tensor(o, name);
     is(t, name, c10::typeMetaToScalarType(opt.dtype()), opt.device(), (int64_t)shape.size());
     dense(t, name);

@@ -229,3 +229,25 @@ def test_a_slot_ends_and_begins_again_before_a_step(cuda_device):
     pages()
     with pytest.raises(ValueError, match="runs"):
         b.begin(0)
+
+
+def test_new_outputs_are_seen_by_dispatch_modes(cuda_device):
+    """Outputs that a call makes come from torch's allocating operator, which modes that count or fill memory watch."""
+    from torch.utils._python_dispatch import TorchDispatchMode
+
+    class Seen(TorchDispatchMode):
+        def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+            self.names.append(func.name())
+            return func(*args, **(kwargs or {}))
+
+    dev = cuda_device
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=dev)  # noqa: E731
+    y, x = torch.randn(4, 256, device=dev, dtype=BF), torch.randn(4, 64, device=dev)
+    lens, new, tab, stack, height = i32([0, 0]), i32([1, 1]), i32([[-1], [-1]]), i32([0, 1]), i32([2])
+    mode = Seen()
+    for what, made in ((lambda: moe.norm_residual(y, pre=moe.Norm(None)), 1), (lambda: moe.router_grouped_topk(x, 4), 2),
+                       (lambda: moe.plan_pages(lens, new, tab, stack, height, 4, 2), 6)):
+        mode.names = []
+        with mode:
+            what()
+        assert sum("aten::empty" in n for n in mode.names) >= made, mode.names

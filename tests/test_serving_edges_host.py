@@ -64,3 +64,8 @@ def test_the_softmax_scores_error_is_a_bound():
     bound = exp2 + argument * score_times + exp2 + argument * mean + (32 + 5) + 2
     held = re.search(r"softmax \? (0x[0-9a-f]+)p-24f / total", source("router_grouped.cu")).group(1)
     assert bound <= int(held, 16), (bound, held)
+
+
+def test_the_binding_allocates_by_torchs_operator_alone():
+    code = source("binding.cpp")
+    assert "at::detail" not in code and "at::empty(" in code
