@@ -568,8 +568,10 @@ int moe_matvec4(const void* x, int64_t x_stride, int T, int K, int dtype, const 
  *   may serve moe_paged_attention calls too, one after the other.
  * Launches: three (own keys, prefix, join), or one of moe_paged_attention's where
  * little would be saved (shared_len below 512, or (B - 1) * shared_len * Hkv * D
- * keys' and values' elements, twice, below 12 million; of E4M3 64 million, or B
- * below 3).
+ * keys' and values' elements, twice, below 12 million; with E4M3 below 48 million
+ * for D = 64 and 128 and 70 million for others, or B below 4).  All B sequences
+ * count there, and in the prefix's launch their rows are computed, whether or not
+ * they share: a batch of which few do is better given to moe_paged_attention.
  * Limits as there; shared_len <= n_shared * page_size and <= max_pages *
  * page_size, and below 2^31 - 256.
  */

@@ -928,18 +928,28 @@ static int px_group_rows(int D) { return px_streams(px_db(D)) * PX_ROWS; }
 // Whether the prefix is worth its own launch and the join: reading it by each
 // sequence costs (B - 1) more times its keys and values, the three launches and
 // the pieces some 3 to 10 us.  Measured (us, this form / one launch of the paged
-// kernel, B sequences with 60 own tokens):
-//   32 / 4 heads of 128, BF16: 128 x 128 19.0 / 12.7, 8 x 512 11.0 / 11.2, 32 x 512
-//     13.9 / 13.3, 8 x 4096 17.0 / 19.4, 64 x 4096 24.0 / 49.8, 2 x 16384 17.6 / 18.9
-//   the same, E4M3: 64 x 1024 23.3 / 23.5, 8 x 4096 18.5 / 18.5, 4 x 16384 19.8 / 23.0,
-//     32 x 4096 24.9 / 29.3, 2 x 65536 37.6 / 30.2
-//   12 / 12, E4M3: 7 x 5016 of 80 23.9 / 23.7, 32 x 512 of 192 20.8 / 23.8
-//   8 / 8 of 64, FP16: 16 x 512 12.2 / 9.9, 32 x 512 12.9 / 13.2, 64 x 512 13.7 / 17.3
+// kernel, * what is taken, B sequences with 60 own tokens, which all share; the
+// flags are on the device, so sequences that do not share count like the others):
+//   32 / 4 heads of 128, BF16: 128 x 128 18.2 / 12.6*, 8 x 512 10.8 / 11.5*, 32 x 512
+//     13.6* / 13.1, 8 x 4096 16.6* / 19.3, 64 x 4096 23.6* / 49.6, 2 x 16384 18.0* / 19.1
+//   8 / 8 of 64, FP16: 16 x 512 11.7 / 9.5*, 32 x 512 12.5* / 12.9, 64 x 512 13.0* / 17.4
+//   32 / 4 of 128, E4M3, BF16 query: 64 x 512 21.6 / 18.3*, 8 x 4096 18.4 / 18.1*,
+//     4 x 16384 20.6* / 23.1, 8 x 8192 20.3* / 22.8, 64 x 1024 23.4* / 22.9, 32 x 4096
+//     24.9* / 28.9, 2 x 65536 40.8 / 30.3*, 3 x 65536 41.1 / 38.3*; FP16 query: 4 x 16384
+//     19.7* / 22.2, 64 x 1024 18.6* / 22.2, 4 x 32768 27.4* / 30.3, 3 x 65536 39.5 / 37.5*
+//   other sizes, E4M3, FP16 query: 8 / 8 of 64, 8 x 8192 16.7* / 22.0; 64 / 8 of 128,
+//     8 x 2048 16.0 / 14.4*, 4 x 8192 20.2* / 21.9; 12 / 12 of 80, 7 x 5016 24.4 / 22.7*,
+//     20 x 2508 20.7* / 30.7; of 192, 8 x 2048 21.2 / 19.6*, 32 x 512 18.1* / 23.0;
+//     16 / 4 of 256, 16 x 2048 17.7 / 17.0*
 // so by what is saved, from four key tiles on; codes have to be widened first,
-// which the paged kernel does on its way: they take more, and three sequences.
+// which the paged kernel does on its way: they take more, most where a head does
+// not fill its blocks of 64 dims or two streams (D = 64 and 128 do), and four
+// sequences.
 bool prefix_pays(int B, int Hkv, int D, int len, bool e4) {
     const double saved = 2.0 * (B - 1) * len * Hkv * D;  // elements
-    return len >= 512 && saved >= (e4 ? 64e6 : 12e6) && !(e4 && B < 3);
+    if (len < 512) return false;
+    if (!e4) return saved >= 12e6;
+    return B >= 4 && saved >= (D == 64 || D == 128 ? 48e6 : 70e6);
 }
 
 // Runs that the prefix is cut into: the number that ends first, when a block's

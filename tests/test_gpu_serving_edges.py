@@ -12,7 +12,7 @@ from mixture_experts_decode_gb300 import inputs
 import _block_refs as refs
 import _serving_refs as srefs
 from test_gpu_router_grouped import MANY, check as check_router, randn
-from test_gpu_shared_prefix import BF, E4, HF, call, enough, make
+from test_gpu_shared_prefix import BF, E4, HF, call, check, enough, make
 
 sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
 import decode_block  # noqa: E402
@@ -251,3 +251,40 @@ def test_new_outputs_are_seen_by_dispatch_modes(cuda_device):
         with mode:
             what()
         assert sum("aten::empty" in n for n in mode.names) >= made, mode.names
+
+
+def reads_the_prefix_by_itself(c):
+    """Whether a call leaves pieces of the prefix in its workspace, behind what the paged kernel needs."""
+    B, Hq, D = c["q"].shape
+    Hkv = c["k"].shape[2]
+    ws = moe.shared_prefix_workspace(B, Hq, Hkv, D)
+    own = moe.attention_workspace_bytes(Hq, Hkv, D)
+    ws[own:] = 0xa5
+    call(c, ws=ws)
+    return not bool((ws[own:] == 0xa5).all())
+
+
+@pytest.mark.parametrize("B,prefix,Hq,Hkv,D,dtype,cache,by_itself", [
+    (4, 16384, 32, 4, 128, BF, E4, True), (4, 16384, 32, 4, 128, HF, E4, True), (3, 65536, 32, 4, 128, BF, E4, False),
+    (64, 512, 32, 4, 128, BF, E4, False), (8, 8192, 8, 8, 64, HF, E4, True), (7, 5016, 12, 12, 80, HF, E4, False),
+    (8, 2048, 12, 12, 192, HF, E4, False), (32, 512, 32, 4, 128, BF, BF, True), (8, 512, 32, 4, 128, BF, BF, False),
+    (16, 512, 8, 8, 64, HF, HF, False)])
+def test_the_faster_form_is_taken(cuda_device, B, prefix, Hq, Hkv, D, dtype, cache, by_itself):
+    """On either side of the rule, as measured beside it."""
+    assert reads_the_prefix_by_itself(make(cuda_device, B, Hq, Hkv, D, 8, prefix, 3, dtype, cache, seed=61)) == by_itself
+
+
+@pytest.mark.parametrize("D,dtype", [(16, BF), (48, HF), (80, BF), (80, HF), (144, HF), (192, BF), (256, HF)])
+def test_codes_of_heads_that_fill_no_block(cuda_device, D, dtype):
+    """E4M3 heads of all block numbers by the prefix's kernel."""
+    prefix = 24 * 130
+    B = math.ceil(70e6 / (2 * prefix * 3 * D)) + 1
+    c = make(cuda_device, B, 6, 3, D, 24, prefix, [(i * 7) % 40 for i in range(B)], dtype, E4, seed=D, others=(1,))
+    assert reads_the_prefix_by_itself(c)
+    check(c, what=f"D={D}")
+
+
+def test_a_long_prefix_of_codes(cuda_device):
+    c = make(cuda_device, 4, 16, 2, 128, 64, 70000, [5, 0, 300, 1], BF, E4, seed=7, q_std=3.0)
+    assert reads_the_prefix_by_itself(c)
+    check(c, what="long")
