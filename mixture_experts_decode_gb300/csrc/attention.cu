@@ -62,7 +62,6 @@ constexpr int ATT_LEAST = 3;
 // take less than a join (64 sequences of 200 keys: 10.0 us against 15.8; 11 of
 // 122 visible keys, D = 256: 8.1 against 12.2).
 constexpr int ATT_WHOLE = 4;
-constexpr int KV_BF16 = 0, KV_F16 = 1, KV_E4M3 = 2;
 
 // Blocks per SM that the registers are cut for, and stages per warp in their
 // share of the 228 KB: three blocks of two stages of D = 128 BF16 beat two of
@@ -104,33 +103,17 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 template <bool BF>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-    uint32_t r;
-    if (BF)
-        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    else
-        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-template <bool BF>
 __device__ __forceinline__ float2 unpack2(uint32_t v) {
     if (BF) return bf16x2_to_float2(v);
     __half2 h;
     memcpy(&h, &v, 4);
     return __half22float2(h);
 }
-// Two E4M3 codes in the low / high half of a word -> FP16 pair, exact.
-__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-    asm("{ .reg .b16 l, h;\n\t mov.b32 {l, h}, %2;\n\t cvt.rn.f16x2.e4m3x2 %0, l;\n\t cvt.rn.f16x2.e4m3x2 %1, h; }"
-        : "=r"(lo), "=r"(hi)
-        : "r"(w));
-}
 __device__ __forceinline__ float exp2_fast(float x) {
     float r;
     asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-__device__ __forceinline__ float finite_or_zero(float m) { return m == -INFINITY ? 0.f : m; }
 
 }  // namespace
 

@@ -1,4 +1,4 @@
-// block_common.cuh -- device helpers of the attention and 4-bit kernels.
+// block_common.cuh -- device helpers of the kernels around the expert layer.
 #pragma once
 
 #include "common.cuh"
@@ -17,6 +17,37 @@ __device__ __forceinline__ uint4 ld_128(const void* p) {
     asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p) : "memory");
     return r;
 }
+
+// Types of a key-value cache.
+constexpr int KV_BF16 = 0, KV_F16 = 1, KV_E4M3 = 2;
+
+// Two floats as 16-bit values of a word, lo in the lower half.
+template <bool BF>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    uint32_t r;
+    if (BF)
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Two E4M3 codes in the low / high half of a word -> FP16 pair, exact.
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    asm("{ .reg .b16 l, h;\n\t mov.b32 {l, h}, %2;\n\t cvt.rn.f16x2.e4m3x2 %0, l;\n\t cvt.rn.f16x2.e4m3x2 %1, h; }"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+}
+
+// 2^x within 2 units in the last place; results below 2^-126 are 0.
+__device__ __forceinline__ float exp2_ftz(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// The reference of weights whose scores are all -inf is 0.
+__device__ __forceinline__ float finite_or_zero(float m) { return m == -INFINITY ? 0.f : m; }
 
 // The warp's index in its block as a value the compiler knows to be the same
 // in all lanes: branches on it do not split the warp.

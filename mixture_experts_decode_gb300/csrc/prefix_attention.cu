@@ -48,7 +48,6 @@ namespace moedec {
 
 namespace {
 
-constexpr int KV_BF16 = 0, KV_F16 = 1, KV_E4M3 = 2;
 constexpr int PX_ROWS = 128;            // query rows of a tile (the MMA's M, a warpgroup's threads)
 constexpr int PX_SOFT = 8;              // softmax warps (two warpgroups)
 constexpr int PX_MMA = PX_SOFT;         // the warp that issues the products
@@ -200,32 +199,6 @@ __device__ __forceinline__ void tm_st16(uint32_t at, const uint32_t (&r)[16]) {
         : "memory");
 }
 
-template <bool BF>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-    uint32_t r;
-    if (BF)
-        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    else
-        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-template <bool BF>
-__device__ __forceinline__ float2 unpack2(uint32_t v) {
-    if (BF) return bf16x2_to_float2(v);
-    __half2 h;
-    memcpy(&h, &v, 4);
-    return __half22float2(h);
-}
-__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-    asm("{ .reg .b16 l, h;\n\t mov.b32 {l, h}, %2;\n\t cvt.rn.f16x2.e4m3x2 %0, l;\n\t cvt.rn.f16x2.e4m3x2 %1, h; }"
-        : "=r"(lo), "=r"(hi)
-        : "r"(w));
-}
-__device__ __forceinline__ float exp2_fast(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));  // (results below 2^-126 are 0)
-    return r;
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -256,7 +229,6 @@ __device__ __forceinline__ void exchange(uint32_t& a, uint32_t& b, bool upper, i
     else
         b = got;
 }
-__device__ __forceinline__ float finite_or_zero(float m) { return m == -INFINITY ? 0.f : m; }
 // The barrier gets an arrival of this thread when its copies so far have landed.
 __device__ __forceinline__ void arrive_after_copies(uint64_t* bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
@@ -535,7 +507,7 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attention_kernel(const _
                     if (__any_sync(FULL_MASK, mx > m + SLACK)) {
                         // m moves up: so do l and O as far as it goes
                         const float mn = fmaxf(m, ceilf(mx));
-                        const float f = exp2_fast(m - finite_or_zero(mn));
+                        const float f = exp2_ftz(m - finite_or_zero(mn));
                         m = mn;
                         l2.x *= f, l2.y *= f;
                         if (h || c > 0) {
@@ -562,7 +534,7 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attention_kernel(const _
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
                             float2 p = __ffma2_rn(make_float2(__uint_as_float(x[i][2 * e]), __uint_as_float(x[i][2 * e + 1])), sl2, mu2);
-                            p = make_float2(exp2_fast(p.x), exp2_fast(p.y));
+                            p = make_float2(exp2_ftz(p.x), exp2_ftz(p.y));
                             l2 = __fadd2_rn(l2, p);
                             w[e] = pack2<BF>(p.x, p.y);
                             const float2 r = rest2<BF>(p, w[e]);
@@ -846,14 +818,14 @@ __global__ void __launch_bounds__(PJ_THREADS, PJ_BLOCKS) prefix_join_kernel(cons
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
     float m = -INFINITY, l = 0.f;
     auto scale = [&](float mn) {
-        const float old = exp2_fast(m - finite_or_zero(mn));
+        const float old = exp2_ftz(m - finite_or_zero(mn));
         m = mn;
         l *= old;
         sum.x *= old, sum.y *= old, sum.z *= old, sum.w *= old;
     };
     auto add = [&](float2 ml, const float4& v) {
         if (ml.x == -INFINITY && ml.y == 0.f) return;
-        const float f = exp2_fast(ml.x - finite_or_zero(m));
+        const float f = exp2_ftz(ml.x - finite_or_zero(m));
         l += f * ml.y;
         sum.x += f * v.x, sum.y += f * v.y, sum.z += f * v.z, sum.w += f * v.w;
     };

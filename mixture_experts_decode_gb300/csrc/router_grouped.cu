@@ -57,11 +57,6 @@ __device__ __forceinline__ float logit_at(const void* row, int e) {
     return __half2float(__ushort_as_half(h));
 }
 
-__device__ __forceinline__ float exp2_fast(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
 __device__ __forceinline__ float rcp_fast(float x) {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -195,7 +190,7 @@ __device__ __forceinline__ void route_row(const RouterGroupedArgs& a, int64_t t,
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            s[i] = x[i] == -INFINITY ? 0.f : exp2_fast((x[i] - m) * 1.44269504f);
+            s[i] = x[i] == -INFINITY ? 0.f : exp2_ftz((x[i] - m) * 1.44269504f);
             sum += s[i];
         }
         total = warp_sum(sum);
@@ -204,7 +199,7 @@ __device__ __forceinline__ void route_row(const RouterGroupedArgs& a, int64_t t,
         for (int i = 0; i < NV; ++i) s[i] *= inv;
     } else {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) s[i] = rcp_fast(1.f + exp2_fast(x[i] * -1.44269504f));
+        for (int i = 0; i < NV; ++i) s[i] = rcp_fast(1.f + exp2_ftz(x[i] * -1.44269504f));
     }
     const float tau_s = score_error(softmax, total);
     uint32_t key[NV];
@@ -595,7 +590,7 @@ __global__ void __launch_bounds__(RO_WARPS * 32, NE == 32 ? 4 : 6) router_octets
             for (int o = 1; o < 8; o *= 2) m = fmaxf(m, __shfl_xor_sync(FULL_MASK, m, o));
             total = 0.f;
 #pragma unroll
-            for (int i = 0; i < NE; ++i) total += exp2_fast((x[i] - m) * 1.44269504f);
+            for (int i = 0; i < NE; ++i) total += exp2_ftz((x[i] - m) * 1.44269504f);
 #pragma unroll
             for (int o = 1; o < 8; o *= 2) total += __shfl_xor_sync(FULL_MASK, total, o);
         }
@@ -609,17 +604,17 @@ __global__ void __launch_bounds__(RO_WARPS * 32, NE == 32 ? 4 : 6) router_octets
             if (softmax)
 #pragma unroll
                 for (int i = 0; i < NE; ++i)
-                    x[i] = x[i] > -INFINITY ? fmaf(exp2_fast((x[i] - m) * 1.44269504f), inv, bias[i]) : -INFINITY;
+                    x[i] = x[i] > -INFINITY ? fmaf(exp2_ftz((x[i] - m) * 1.44269504f), inv, bias[i]) : -INFINITY;
             else
 #pragma unroll
                 for (int i = 0; i < NE; ++i)
-                    x[i] = x[i] > -INFINITY ? rcp_fast(1.f + exp2_fast(x[i] * -1.44269504f)) + bias[i] : -INFINITY;
+                    x[i] = x[i] > -INFINITY ? rcp_fast(1.f + exp2_ftz(x[i] * -1.44269504f)) + bias[i] : -INFINITY;
         } else if (narrow && top2) {  // (the order is the logits', a group's worth is of scores)
 #pragma unroll
             for (int i = 0; i < NE; ++i)
                 see(x[i] == -INFINITY ? -INFINITY
-                    : softmax         ? exp2_fast((x[i] - m) * 1.44269504f) * inv
-                                      : rcp_fast(1.f + exp2_fast(x[i] * -1.44269504f)));
+                    : softmax         ? exp2_ftz((x[i] - m) * 1.44269504f) * inv
+                                      : rcp_fast(1.f + exp2_ftz(x[i] * -1.44269504f)));
         }
         if (narrow && (!same_bias || !top2))
 #pragma unroll
