@@ -33,10 +33,12 @@
 //
 // Bound: HBM for few rows (the prefix once); for many the chain score product,
 // softmax, value product, score product of a stream, with the tensor pipe active
-// half of the time.  Measured, whole calls: 64 sequences over 65536 tokens, 64 /
-// 8 heads of 128, E4M3 199 us (691 TFLOP/s; one launch of the paged kernel 1010);
-// 32 over 8192, 32 / 4 of 128, BF16, chats of up to 1500 tokens 29.5 us (45); 300
-// over 9600, 16 / 2 of 64, FP16 48.7 us (142).
+// half of the time; with few key tiles a block, what is around that: own keys,
+// pieces and join.  Measured, whole calls: 64 sequences over 65536 tokens, 64 / 8
+// heads of 128, E4M3 199 us (691 TFLOP/s; one launch of the paged kernel 1000), 191
+// with an FP16 query; 32 over 8192, 32 / 4 of 128, BF16, chats of up to 1500 tokens
+// 29.6 us (45), heads of 192 and 256, 400 own tokens 36 and 39 us (124); 300 over
+// 9600, 16 / 2 of 64, FP16 48.9 us (142), of which own keys 18 and the join 10.
 #include <algorithm>
 #include <type_traits>
 

@@ -5,8 +5,8 @@
 // lower expert first), and weights from the scores alone.
 //
 // Which of two keys is larger is decided for the real numbers, not for their
-// FP32 roundings: FP32 keys choose, and where two that matter lie within TAU
-// of each other, the keys of the candidates are computed again in 64 bits.
+// FP32 roundings: FP32 keys choose, and where two that matter lie within their
+// errors of each other, the keys of the candidates are computed again in 64 bits.
 // Without a bias (or with the same one for all) the logits themselves are the
 // keys, which needs no second look.
 //
@@ -15,9 +15,12 @@
 // memory; a pick is the largest of the 32 list heads, one redux instruction on
 // order-preserving integers, and the next head of the list that had it.  Whose
 // index a picked key had is found once, for all picks at the same time.
-// Bound: latency for few tokens (64 rows of 256 experts: 4.1 us), instructions
-// for many (65536 rows of 256, 8 groups, 8 picks, FP32: 55 us, 1.3 TB/s; the
-// logits' bytes alone would take 10).
+// Bound: latency for few tokens (33 rows of 256 experts: 4.1 us).  For many
+// (65536 rows of 256, 8 groups, 8 picks, FP32: 55 us, 1.3 TB/s, BF16 52 us; the
+// logits' bytes alone would take 10) the dependent steps and exchanges of the 16
+// warps that an SM has room for: 2.2 of 4 instructions issue a cycle.  Shapes that
+// the eight-lane kernel does not take need a warp a row: 65536 rows of 512, 10
+// picks, 142 us; of 160 in 16 groups 96.
 #include <algorithm>
 
 #include "block_common.cuh"
